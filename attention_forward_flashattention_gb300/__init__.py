@@ -46,9 +46,9 @@ class FaError(RuntimeError):
         self.status = status
 
 
-def header_functions() -> list[str]:
-    """Names of the entry points that include/fa.h declares."""
-    text = open(HEADER).read()
+def header_functions(header: str = HEADER) -> list[str]:
+    """Names of the entry points that a header (include/fa.h) declares."""
+    text = open(header).read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
     return re.findall(r"^\s*(?:fa_status|const char\s*\*|int)\s+(fa_\w+)\s*\(", text, flags=re.M)
 
@@ -104,6 +104,9 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.fa_status_string.restype = ctypes.c_char_p
         lib.fa_version.argtypes = []
         lib.fa_version.restype = i
+        if hasattr(lib, "fa_fwd_cache"):
+            from . import cache
+            cache.bind(lib)
         if path is None:
             _lib = lib
         return lib
@@ -470,3 +473,11 @@ def attention(q, k, v, causal: bool = False, scale: float | None = None):
     if scale is None:
         scale = 1.0 / math.sqrt(q.shape[-1])
     return _attention_function().apply(q, k, v, bool(causal), float(scale))
+
+
+# ------------------------------------------------------------ block cache (include/fa_cache.h)
+
+from .cache import (Cache, FaCache, attention_forward_cache,  # noqa: E402,F401
+                    attention_forward_cache_into, cache_append, cache_empty, cache_plan,
+                    cache_plan_into, fa_cache_append, fa_cache_plan, fa_fwd_cache,
+                    fa_fwd_cache_workspace_size)

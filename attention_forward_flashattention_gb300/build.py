@@ -1,6 +1,6 @@
 """Builds the CUDA libraries in-tree with nvcc for sm_103a.
 
-  _build/libfa_sm103.so    the product: C ABI of include/fa.h
+  _build/libfa_sm103.so    the product: C ABI of include/fa.h and fa_cache.h
   _build/libfa_selftest.so GPU unit tests of the PTX building blocks
 
 Translation units are compiled in parallel (one nvcc process each), then
@@ -23,10 +23,12 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libfa_sm103.so"
 SELFTEST_NAME = "libfa_selftest.so"
 LIB_UNITS = ["fa_host.cu", "fa_fwd_d64.cu", "fa_fwd_d128.cu", "fa_fwd_fp8.cu", "fa_fwd_pair.cu",
-             "fa_bwd_d64.cu", "fa_bwd_d128.cu", "fa_noalloc.cu", "fa_pipeline.cu"]
+             "fa_bwd_d64.cu", "fa_bwd_d128.cu", "fa_noalloc.cu", "fa_pipeline.cu",
+             "fa_cache_host.cu", "fa_cache_plan.cu", "fa_cache_append.cu", "fa_cache_attn.cu"]
 SELFTEST_UNITS = ["selftest.cu"]
 HEADERS = ["ptx.cuh", "fa_common.cuh", "fa_kernel.cuh", "fa_launch.cuh", "fa_pair.cuh", "fa_bwd.cuh",
-           "fa_bwd_launch.cuh", "fa_dispatch.h"]
+           "fa_bwd_launch.cuh", "fa_dispatch.h", "fa_cache.cuh"]
+PUBLIC_HEADERS = ["fa.h", "fa_cache.h"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -59,7 +61,7 @@ def _stale(target: str, sources: list[str]) -> bool:
     if not os.path.exists(target):
         return True
     t = os.path.getmtime(target)
-    deps = [os.path.join(CSRC, s) for s in sources + HEADERS] + [os.path.join(INCLUDE, "fa.h")]
+    deps = [os.path.join(CSRC, s) for s in sources + HEADERS] + [os.path.join(INCLUDE, h) for h in PUBLIC_HEADERS]
     return any(os.path.getmtime(d) > t for d in deps)
 
 

@@ -16,6 +16,7 @@
 
 #include "fa.h"
 #include "fa_bwd.cuh"
+#include "fa_cache.cuh"
 #include "fa_kernel.cuh"
 #include "fa_dispatch.h"
 #include "fa_pair.cuh"
@@ -142,6 +143,16 @@ __global__ void clock_probe_kernel(uint64_t* out, long long cycles) {
 }
 
 }  // namespace
+
+fa_status device_facts(int* sm_count, uint32_t** status) {
+  int dev = 0;
+  DeviceState* st = nullptr;
+  const fa_status s = current_device(&dev, &st, status != nullptr);
+  if (s != FA_OK) return s;
+  *sm_count = st->sm_count;
+  if (status) *status = st->status;
+  return FA_OK;
+}
 
 fa_status check_sizes(int B, int H, int N, int d) {
   if (B <= 0 || H <= 0 || N <= 0) return FA_ERR_INVALID_ARG;

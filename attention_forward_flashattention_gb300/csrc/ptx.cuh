@@ -688,6 +688,23 @@ __device__ __forceinline__ uint32_t pack4_e4m3(float x0, float x1, float x2, flo
   return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
 }
 
+// Two e4m3 codes (the low byte first) as fp16, exactly: every e4m3 value is one.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t codes) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(codes));
+  return h;
+}
+// The same as fp32.
+__device__ __forceinline__ float2 e4m3x2_to_f32(uint32_t codes) {
+  const uint32_t h = e4m3x2_to_f16x2(static_cast<uint16_t>(codes));
+  float2 f;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
+      "cvt.f32.f16 %0, lo;\n\tcvt.f32.f16 %1, hi;\n\t}"
+      : "=f"(f.x), "=f"(f.y)
+      : "r"(h));
+  return f;
+}
+
 // 2^x on the MUFU unit (approximate, flushes denormals; 2^-inf = 0).
 __device__ __forceinline__ float ex2(float x) {
   float y;

@@ -1,0 +1,154 @@
+"""Plain 64-bit implementations of the block cache's calls, on the CPU, for the
+tests (numpy; no code of the library)."""
+import math
+
+import numpy as np
+
+from attention_forward_flashattention_gb300 import inputs as I
+
+MIN_EXP = -40
+CODE_VALUES = I.e4m3_values()
+
+
+def plan(lens, new, table, free, pos, T, bs):
+    """(slots, cu, kv_lens, table, free_next) as lists / arrays: one request after another."""
+    table = np.array(table, dtype=np.int64)
+    slots = [-1] * T
+    cu, kv, rows, wanted, used = [], [], 0, 0, 0
+    for b, (x, m) in enumerate(zip(lens, new)):
+        cu.append(min(rows, T))
+        have, want = (max(x, 0) + bs - 1) // bs, (max(x, 0) + max(m, 0) + bs - 1) // bs
+        ok = x >= 0 and m >= 0 and want <= table.shape[1] and x + m < 2 ** 31
+        need = want - have if ok else 0
+        wanted += need
+        first = rows
+        rows += max(m, 0)
+        if m > 0 and rows > T:
+            ok = False
+        if need and not (0 <= pos and pos + wanted <= len(free)):
+            ok = False
+        if ok:
+            for j in range(need):
+                table[b, have + j] = free[pos + used + j]
+            used += need
+            for i in range(m):
+                at = x + i
+                page = int(table[b, at // bs])
+                slot = page * bs + at % bs
+                slots[first + i] = slot if page >= 0 and slot < 2 ** 31 else -1
+        kv.append(x + m if ok else max(x, 0))
+    cu.append(min(rows, T))
+    return slots, cu, kv, table, pos + used
+
+
+def need_scale(amax):
+    if amax <= 0:
+        return 2.0 ** MIN_EXP
+    e = max(math.ceil(math.log2(amax / 448.0)) - 1, MIN_EXP)   # at or one below the wanted one
+    while amax > 448.0 * 2.0 ** e:
+        e += 1
+    return 2.0 ** e
+
+
+def pow2_above(x):
+    m, e = math.frexp(x)
+    return 2.0 ** (e - 1 if m == 0.5 else e)
+
+
+def encode(x):
+    """e4m3 codes of float64 values; infinities and NaN give NaN."""
+    bad = ~np.isfinite(x)
+    codes = I.to_e4m3_bits(np.where(bad, 0.0, x))
+    return np.where(bad, np.uint8(0x7F), codes)
+
+
+def append(x, slots, codes, scales, bs):
+    """Appends x [T, heads, d] (float64 values) to codes [P, heads, bs, d] and
+    scales [P, heads]; returns new ones."""
+    codes, scales = codes.copy(), scales.astype(np.float64)
+    P, heads = scales.shape
+    T = len(slots)
+    t = 0
+    while t < T:
+        s = int(slots[t])
+        if not 0 <= s < P * bs:
+            t += 1
+            continue
+        n = 1
+        while t + n < T and slots[t + n] == s + n and (s + n) % bs:
+            n += 1
+        p, off = divmod(s, bs)
+        for h in range(heads):
+            v = x[t:t + n, h]
+            fine = np.abs(v[np.isfinite(v)])
+            now = need_scale(fine.max() if fine.size else 0.0)
+            if off:
+                old = scales[p, h]
+                now = max(now, pow2_above(old))
+                if now != old:
+                    codes[p, h, :off] = encode(CODE_VALUES[codes[p, h, :off]] * (old / now))
+            scales[p, h] = now
+            codes[p, h, off:off + n] = encode(v / now)
+        t += n
+    return codes, scales
+
+
+def attend(q, k, v, ks, vs, table, kv_lens, cu, bs, scale, causal):
+    """float64 attention. q [T, H, d] values, k, v codes [P, Hkv, bs, d]. Returns
+    (O, LSE, mag, far, small): mag = the weighted mean of |v|, far = the
+    largest bound on a score's fp32 error over the row's keys (natural units),
+    small = 2^-25 sum |v code| times the largest V scale (the weights' fp16
+    subnormals)."""
+    T, H, d = q.shape
+    P, heads = ks.shape
+    g = H // heads
+    O = np.zeros((T, H, d))
+    L = np.full((T, H), -np.inf)
+    mag, far, small = np.zeros((T, H, d)), np.zeros((T, H)), np.zeros((T, H))
+    width = table.shape[1] * bs
+    for b, length in enumerate(kv_lens):
+        length = min(max(int(length), 0), width)
+        r0, r1 = cu[b], cu[b + 1]
+        n = r1 - r0
+        ids = np.array([table[b, j // bs] for j in range(length)], dtype=np.int64)
+        seen = (ids >= 0) & (ids < P)
+        safe = np.where(seen, ids, 0)
+        at = np.arange(length) % bs
+        for h in range(heads):
+            kk = CODE_VALUES[k[safe, h, at]].reshape(length, d) * ks[safe, h][:, None]
+            vc = CODE_VALUES[v[safe, h, at]].reshape(length, d)
+            vv = vc * vs[safe, h][:, None]
+            for i in range(n):
+                lim = min(length, length - n + i + 1) if causal else length
+                keep = np.flatnonzero(seen[:max(lim, 0)])
+                if keep.size == 0:
+                    continue
+                for j in range(g):
+                    row, head = r0 + i, h * g + j
+                    s = kk[keep] @ q[row, head] * scale
+                    top = s.max()
+                    p = np.exp(s - top)
+                    O[row, head] = p @ vv[keep] / p.sum()
+                    L[row, head] = top + math.log(p.sum())
+                    mag[row, head] = p @ np.abs(vv[keep]) / p.sum()
+                    far[row, head] = ((d + 3) * 2.0 ** -24 * scale
+                                      * (np.abs(kk[keep]) @ np.abs(q[row, head])).max())
+                    small[row, head] = (2.0 ** -25 * np.abs(vc[keep]).sum(axis=0).max()
+                                        * vs[safe, h][keep].max())
+    return O, L, mag, far, small
+
+
+def attend_tolerance(ref, eps, keys):
+    """Bounds on |O - ref| and |LSE - ref|. Weights: rounded to fp16 (half a
+    step, 2^-11), a score's fp32 error `far` twice (numerator and sum), the
+    exponential and the fp32 sums over the keys (keys * 2^-24 and 2^-20); O is
+    rounded to its type once (eps / 2). LSE: the score, the sum, and fp32
+    values of up to |LSE| + 64 in size."""
+    O, L, mag, far, small = ref
+    rel = 2.0 ** -11 + 2 * far + keys * 2.0 ** -24 + 2.0 ** -20
+    tol_o = mag * rel[..., None] * (1 + eps) + np.abs(O) * (eps / 2) + small[..., None] + 1e-30
+    # results below the type's normal range have a fixed step
+    tol_o = tol_o + (2.0 ** -25 if eps == 2.0 ** -10 else 0.0)
+    lf = np.where(np.isfinite(L), np.abs(L), 0.0)
+    tol_l = far + keys * 2.0 ** -24 + 2.0 ** -20 + 8 * 2.0 ** -24 * (lf + 64)
+    return tol_o, tol_l
