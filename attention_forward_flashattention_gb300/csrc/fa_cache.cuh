@@ -2,6 +2,7 @@
 // arguments of its kernels and their launch functions.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -65,8 +66,15 @@ struct CacheAttnArgs {
 cudaError_t launch_cache_plan(const CachePlanArgs& a, int sm_count, cudaStream_t stream);
 cudaError_t launch_cache_append(const CacheAppendArgs& a, int block, int d, bool bf16,
                                 cudaStream_t stream);
-cudaError_t launch_cache_attn(const CacheAttnArgs& a, int d, bool bf16, int sm_count,
-                              cudaStream_t stream);
+// False in *mapped: a tensor map could not be encoded.
+cudaError_t launch_cache_attn(const CacheAttnArgs& a, const fa_cache& c, bool bf16, int sm_count,
+                              cudaStream_t stream, bool* mapped);
+
+// fa_host.cu: a cache's K or V as a 4-D byte map {d, token in block, head,
+// block}; box = `rows` tokens of one head and block, swizzled over its d bytes.
+bool encode_cache(CUtensorMap* m, const void* codes, const fa_cache& c, int rows);
+// Floats of workspace that the attention kernels need, by the SM count alone.
+long long cache_workspace_floats(int d, int sm_count);
 
 // fa_host.cu: the current device's SM count and status word (allocated on first use).
 fa_status device_facts(int* sm_count, uint32_t** status);

@@ -1,88 +1,64 @@
-// fa_fwd_cache: attention over the block cache. One warp per query row: a pass
-// over the row's keys with the running maximum and sum, each lane holding
-// d / 32 elements of q, K, V and O.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
-#include "fa_cache.cuh"
-#include "ptx.cuh"
+// fa_fwd_cache: choice of kernel and launches.
+#include "fa_cache_step.cuh"
 
 namespace fa {
 namespace {
 
-template <int D, bool BF16>
-__global__ void __launch_bounds__(128) fa_cache_row_kernel(const CacheAttnArgs a) {
-  constexpr int kPer = D / 32;
-  const int lane = static_cast<int>(threadIdx.x & 31);
-  const int b = static_cast<int>(blockIdx.y);
-  const SeqRows s = seq_rows(a, b);
-  const long long rows = static_cast<long long>(s.count) * a.H;
-  const int bs1 = (1 << a.block_shift) - 1;
-  for (long long r = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5); r < rows;
-       r += 4LL * gridDim.x) {
-    const int i = static_cast<int>(r / a.H), h = static_cast<int>(r % a.H);
-    const int hk = h / a.group;
-    const int lim = a.causal ? min(s.kv_len, s.kv_len - s.count + i + 1) : s.kv_len;
-    float q[kPer], o[kPer];
-    const uint16_t* qp = static_cast<const uint16_t*>(a.q) + q_offset(a, b, s, i, h) + kPer * lane;
-    for (int e = 0; e < kPer; ++e) {
-      if constexpr (BF16) q[e] = __uint_as_float(static_cast<uint32_t>(qp[e]) << 16);
-      else q[e] = __half2float(__ushort_as_half(qp[e]));
-      o[e] = 0.f;
-    }
-    float m = -INFINITY, l = 0.f;
-    for (int j = 0; j < lim; ++j) {
-      const int id = __ldg(a.table + static_cast<long long>(b) * a.table_width + (j >> a.block_shift));
-      if (id < 0 || id >= a.num_blocks) continue;
-      const long long at = id * a.block_stride + hk * a.head_stride + (j & bs1) * a.token_stride;
-      const float ks = __ldg(a.ks + static_cast<long long>(id) * a.Hkv + hk);
-      const float vs = __ldg(a.vs + static_cast<long long>(id) * a.Hkv + hk);
-      float x = 0.f, v[kPer];
-      for (int e = 0; e < kPer; e += 2) {
-        const int c = kPer * lane + e;
-        const float2 kk = ptx::e4m3x2_to_f32(*reinterpret_cast<const uint16_t*>(a.k + at + c));
-        const float2 vv = ptx::e4m3x2_to_f32(*reinterpret_cast<const uint16_t*>(a.v + at + c));
-        x = fmaf(q[e], kk.x, fmaf(q[e + 1], kk.y, x));
-        v[e] = vv.x * vs;
-        v[e + 1] = vv.y * vs;
-      }
-      for (int w = 16; w > 0; w >>= 1) x += __shfl_xor_sync(0xffffffffu, x, w);
-      x *= ks * a.scale_log2;
-      const float top = fmaxf(m, x);
-      const float keep = exp2f(m - top), p = exp2f(x - top);
-      l = l * keep + p;
-      for (int e = 0; e < kPer; ++e) o[e] = o[e] * keep + p * v[e];
-      m = top;
-    }
-    const bool none = m == -INFINITY && l == 0.f;
-    const float inv = none ? 0.f : 1.f / l;
-    uint16_t* op = static_cast<uint16_t*>(a.o) + o_offset(a, b, s, i, h) + kPer * lane;
-    for (int e = 0; e < kPer; ++e) {
-      if constexpr (BF16) op[e] = __bfloat16_as_ushort(__float2bfloat16_rn(o[e] * inv));
-      else op[e] = __half_as_ushort(__float2half_rn(o[e] * inv));
-    }
-    if (lane == 0)
-      a.lse[lse_index(a, b, s, i, h)] =
-          none ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
-  }
+template <int D, bool BF16, int NT>
+cudaError_t launch_step(const CacheAttnArgs& a, const CUtensorMap* maps, int sm_count,
+                        cudaStream_t stream) {
+  constexpr int kSmem = StepLayout<D>::kSmem;
+  auto kern = fa_cache_step_kernel<D, BF16, NT>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  const int grid = 2 * sm_count;
+  // sequences of at most one round of tiles (a tile for each warp) are never
+  // cut: nothing to join, one launch
+  const bool whole = (static_cast<long long>(a.table_width) << a.block_shift) <=
+                     kStepWarps * step_keys(D);
+  kern<<<grid, kStepThreads, kSmem, stream>>>(maps[0], maps[1], a, whole ? 1 : 0);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || whole) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fa_cache_join_kernel<D, BF16>, a, 8 * NT);
+}
+
+template <int D>
+cudaError_t pick(const CacheAttnArgs& a, const CUtensorMap* maps, bool bf16, int sm_count,
+                 cudaStream_t s) {
+  // rows that share a K / V head, on average: they decide only how many rows
+  // go through the cache together
+  const long long rows = ((static_cast<long long>(a.T) + a.B - 1) / a.B) * a.group;
+  if (rows <= 8)
+    return bf16 ? launch_step<D, true, 1>(a, maps, sm_count, s)
+                : launch_step<D, false, 1>(a, maps, sm_count, s);
+  return bf16 ? launch_step<D, true, 2>(a, maps, sm_count, s)
+              : launch_step<D, false, 2>(a, maps, sm_count, s);
 }
 
 }  // namespace
 
-cudaError_t launch_cache_attn(const CacheAttnArgs& a, int d, bool bf16, int sm_count,
-                              cudaStream_t stream) {
-  const long long rows = static_cast<long long>(a.T) * a.H;
-  long long x = (rows + 3) / 4;
-  if (x > 64LL * sm_count) x = 64LL * sm_count;
-  const dim3 grid(static_cast<unsigned>(x), static_cast<unsigned>(a.B));
-  if (d == 64) {
-    if (bf16) fa_cache_row_kernel<64, true><<<grid, 128, 0, stream>>>(a);
-    else fa_cache_row_kernel<64, false><<<grid, 128, 0, stream>>>(a);
-  } else {
-    if (bf16) fa_cache_row_kernel<128, true><<<grid, 128, 0, stream>>>(a);
-    else fa_cache_row_kernel<128, false><<<grid, 128, 0, stream>>>(a);
-  }
-  return cudaGetLastError();
+long long cache_workspace_floats(int d, int sm_count) {
+  const long long grid = 2LL * sm_count;
+  return 4 * grid + 2 * grid * partial_floats(kStepMaxRows, d);
+}
+
+cudaError_t launch_cache_attn(const CacheAttnArgs& a, const fa_cache& c, bool bf16, int sm_count,
+                              cudaStream_t stream, bool* mapped) {
+  CUtensorMap maps[2];
+  const int keys = step_keys(c.d), rows = c.block < keys ? c.block : keys;
+  *mapped = encode_cache(&maps[0], c.k, c, rows) && encode_cache(&maps[1], c.v, c, rows);
+  if (!*mapped) return cudaErrorUnknown;
+  return c.d == 64 ? pick<64>(a, maps, bf16, sm_count, stream)
+                   : pick<128>(a, maps, bf16, sm_count, stream);
 }
 
 }  // namespace fa

@@ -33,7 +33,8 @@ fa_status check_cache(const fa_cache* c) {
   if (block_shift(c->block) < 0) return FA_ERR_UNSUPPORTED;
   for (const long long s : {c->block_stride, c->head_stride, c->token_stride})
     if (s >= (1LL << 38)) return FA_ERR_UNSUPPORTED;
-  if (static_cast<long long>(c->num_blocks) * c->block > 0x7FFFFFFFLL || c->Hkv > 32767)
+  if (static_cast<long long>(c->num_blocks) * c->block > 0x7FFFFFFFLL || c->Hkv > 32767 ||
+      static_cast<long long>(c->num_blocks) * c->Hkv > 0x7FFFFFFFLL)
     return FA_ERR_UNSUPPORTED;
   return FA_OK;
 }
@@ -141,7 +142,7 @@ fa_status fa_fwd_cache_workspace_size(int B, int T, int H, int Hkv, int d, size_
   int sms = 0;
   const fa_status ds = fa::device_facts(&sms, nullptr);
   if (ds != FA_OK) return ds;
-  *bytes = 16;
+  *bytes = static_cast<size_t>(fa::cache_workspace_floats(d, sms)) * sizeof(float);
   return FA_OK;
 }
 
@@ -169,7 +170,9 @@ fa_status fa_fwd_cache(const void* q, const fa_cache* cache, const int32_t* bloc
       if (ss != FA_OK) return ss;
     }
   }
-  if (static_cast<long long>(T) * H > 0x7FFFFFFFLL || B > 65535) return FA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(T) * H > 0x7FFFFFFFLL || B > (1 << 20) ||
+      static_cast<long long>(table_width) * cache->block > (1LL << 30))
+    return FA_ERR_UNSUPPORTED;
   size_t need = 0;
   const fa_status ws = fa_fwd_cache_workspace_size(B, T, H, cache->Hkv, cache->d, &need);
   if (ws != FA_OK) return ws;
@@ -211,8 +214,10 @@ fa_status fa_fwd_cache(const void* q, const fa_cache* cache, const int32_t* bloc
   a.scale_log2 = scale * 1.4426950408889634f;
   a.ws = static_cast<float*>(workspace);
   (void)cudaGetLastError();
-  return done(fa::launch_cache_attn(a, cache->d, dtype == FA_DTYPE_BF16, sms,
-                                    static_cast<cudaStream_t>(stream)));
+  bool mapped = true;
+  const cudaError_t e = fa::launch_cache_attn(a, *cache, dtype == FA_DTYPE_BF16, sms,
+                                              static_cast<cudaStream_t>(stream), &mapped);
+  return mapped ? done(e) : FA_ERR_CUDA;
 }
 
 }  // extern "C"
