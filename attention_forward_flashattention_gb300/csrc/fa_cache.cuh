@@ -65,7 +65,7 @@ struct CacheAttnArgs {
 
 cudaError_t launch_cache_plan(const CachePlanArgs& a, int sm_count, cudaStream_t stream);
 cudaError_t launch_cache_append(const CacheAppendArgs& a, int block, int d, bool bf16,
-                                cudaStream_t stream);
+                                int sm_count, cudaStream_t stream);
 // False in *mapped: a tensor map could not be encoded.
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, const fa_cache& c, bool bf16, int sm_count,
                               cudaStream_t stream, bool* mapped);

@@ -132,7 +132,7 @@ fa_status fa_cache_append(const void* k, const void* v, const fa_strides* stride
   a.Hkv = cache->Hkv;
   a.n_slots = cache->num_blocks * cache->block;
   (void)cudaGetLastError();
-  return done(fa::launch_cache_append(a, cache->block, cache->d, dtype == FA_DTYPE_BF16,
+  return done(fa::launch_cache_append(a, cache->block, cache->d, dtype == FA_DTYPE_BF16, sms,
                                       static_cast<cudaStream_t>(stream)));
 }
 
