@@ -27,7 +27,7 @@ LIB_UNITS = ["fa_host.cu", "fa_fwd_d64.cu", "fa_fwd_d128.cu", "fa_fwd_fp8.cu", "
              "fa_cache_host.cu", "fa_cache_plan.cu", "fa_cache_append.cu", "fa_cache_attn.cu"]
 SELFTEST_UNITS = ["selftest.cu"]
 HEADERS = ["ptx.cuh", "fa_common.cuh", "fa_kernel.cuh", "fa_launch.cuh", "fa_pair.cuh", "fa_bwd.cuh",
-           "fa_bwd_launch.cuh", "fa_dispatch.h", "fa_cache.cuh", "fa_cache_step.cuh"]
+           "fa_bwd_launch.cuh", "fa_dispatch.h", "fa_cache.cuh", "fa_cache_step.cuh", "fa_cache_chunk.cuh"]
 PUBLIC_HEADERS = ["fa.h", "fa_cache.h"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -300,11 +300,12 @@ def attention_forward_cache(q, cache, block_table, kv_lens, cu_q=None, causal: b
         raise ValueError(f"{H} query heads do not share {heads} K / V heads evenly")
     if d != cache[0].shape[-1]:
         raise ValueError(f"q has d = {d}, the cache {cache[0].shape[-1]}")
+    B, T = block_table.shape[0], math.prod(shape[:-1]) // H
     if index == torch.cuda.current_device():
-        size = fa_fwd_cache_workspace_size(block_table.shape[0], 1, H, heads, d)
+        size = fa_fwd_cache_workspace_size(B, T, H, heads, d)
     else:
         with torch.cuda.device(index):
-            size = fa_fwd_cache_workspace_size(block_table.shape[0], 1, H, heads, d)
+            size = fa_fwd_cache_workspace_size(B, T, H, heads, d)
     with _allocating_on(stream):
         o = torch.empty(shape, dtype=q.dtype, device=dev)
         lse = torch.empty(shape[:-1], dtype=torch.float32, device=dev)

@@ -71,10 +71,12 @@ cudaError_t launch_cache_attn(const CacheAttnArgs& a, const fa_cache& c, bool bf
                               cudaStream_t stream, bool* mapped);
 
 // fa_host.cu: a cache's K or V as a 4-D byte map {d, token in block, head,
-// block}; box = `rows` tokens of one head and block, swizzled over its d bytes.
-bool encode_cache(CUtensorMap* m, const void* codes, const fa_cache& c, int rows);
-// Floats of workspace that the attention kernels need, by the SM count alone.
-long long cache_workspace_floats(int d, int sm_count);
+// block}; box = `rows` tokens of one head and block, swizzled over its d bytes
+// or row after row.
+bool encode_cache(CUtensorMap* m, const void* codes, const fa_cache& c, int rows, bool swizzle);
+// Floats of workspace that the attention of T rows of B sequences needs, `group`
+// query heads to a K / V head.
+long long cache_workspace_floats(int B, int T, int group, int d, int sm_count);
 
 // fa_host.cu: the current device's SM count and status word (allocated on first use).
 fa_status device_facts(int* sm_count, uint32_t** status);

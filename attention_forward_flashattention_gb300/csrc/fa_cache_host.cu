@@ -142,7 +142,7 @@ fa_status fa_fwd_cache_workspace_size(int B, int T, int H, int Hkv, int d, size_
   int sms = 0;
   const fa_status ds = fa::device_facts(&sms, nullptr);
   if (ds != FA_OK) return ds;
-  *bytes = static_cast<size_t>(fa::cache_workspace_floats(d, sms)) * sizeof(float);
+  *bytes = static_cast<size_t>(fa::cache_workspace_floats(B, T, H / Hkv, d, sms)) * sizeof(float);
   return FA_OK;
 }
 

@@ -682,8 +682,9 @@ __global__ void __launch_bounds__(kStepThreads, 2)
 // Joins the partial results of the items that fa_cache_step_kernel's shares
 // cut: block c takes the item that begins in share c and ends in a later one.
 // Warps share a row's parts when there are fewer rows than warps; parts are
-// added in a fixed order.
+// added in a fixed order. Blocks (c, y) take the rows from y * kJoinRows on.
 constexpr int kJoinThreads = 256;
+constexpr int kJoinRows = 32;
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kJoinThreads)
@@ -697,15 +698,19 @@ __global__ void __launch_bounds__(kJoinThreads)
   const float* parts = a.ws + 4LL * gridDim.x;
   const int size = partial_floats(max_rows, D);
   const SeqRows s = seq_rows(a, it.b);
-  const int row0 = it.rb * max_rows;
-  const int rows = min(max_rows, s.count * a.group - row0);
+  const long long row0 = static_cast<long long>(it.rb) * max_rows;
+  const int first = static_cast<int>(blockIdx.y) * kJoinRows;
+  const int rows = static_cast<int>(
+      min(min(static_cast<long long>(max_rows), static_cast<long long>(s.count) * a.group - row0),
+          static_cast<long long>(first + kJoinRows)));
+  if (first >= rows) return;
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
   int per_row = 1;  // warps for a row: a power of two
-  while (per_row * 2 * rows <= kWarps) per_row *= 2;
+  while (per_row * 2 * (rows - first) <= kWarps) per_row *= 2;
   auto part = [&](int p) {
     return parts + (2LL * (static_cast<long long>(blockIdx.x) + p) + (p == 0 ? 1 : 0)) * size;
   };
-  for (int r0 = 0; r0 < rows; r0 += kWarps / per_row) {
+  for (int r0 = first; r0 < rows; r0 += kWarps / per_row) {
     const int r = r0 + warp / per_row, k = warp % per_row;
     float m = -INFINITY, l = 0.f, o[kPer] = {};
     if (r < rows) {
@@ -749,8 +754,8 @@ __global__ void __launch_bounds__(kJoinThreads)
     if (r < rows && k == 0) {
       const bool none = m == -INFINITY;
       const float inv = none ? 0.f : 1.f / l;
-      const int i = (row0 + r) / a.group, j = (row0 + r) - i * a.group;
-      const int h = it.hk * a.group + j;
+      const int i = static_cast<int>((row0 + r) / a.group);
+      const int h = it.hk * a.group + static_cast<int>(row0 + r - static_cast<long long>(i) * a.group);
       uint16_t* out = static_cast<uint16_t*>(a.o) + o_offset(a, it.b, s, i, h) + kPer * lane;
       if constexpr (kPer == 4)
         *reinterpret_cast<uint2*>(out) = make_uint2(pack2<BF16>(o[0] * inv, o[1] * inv),

@@ -144,7 +144,7 @@ __global__ void clock_probe_kernel(uint64_t* out, long long cycles) {
 
 }  // namespace
 
-bool encode_cache(CUtensorMap* m, const void* codes, const fa_cache& c, int rows) {
+bool encode_cache(CUtensorMap* m, const void* codes, const fa_cache& c, int rows, bool swizzle) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.d), static_cast<cuuint64_t>(c.block),
@@ -157,7 +157,8 @@ bool encode_cache(CUtensorMap* m, const void* codes, const fa_cache& c, int rows
   const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(codes), dims, strides, box,
              estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             c.d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             !swizzle ? CU_TENSOR_MAP_SWIZZLE_NONE
+                      : c.d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
