@@ -240,7 +240,8 @@ __device__ __forceinline__ void chunk_copy_role(const CUtensorMap* tm_k, const C
       wait_drain(bar(kRawFull + n % R), (n / R) & 1u, ab, kStatusDrain);
 }
 
-// ---- converters: warps 12-15
+// ---- converters: warps 12-15. A thread takes 16 codes of a row at a time: 32
+// bytes in two chunks of one of the row's 128-byte panels.
 template <int D>
 __device__ __forceinline__ void chunk_convert_role(const CacheAttnArgs& a, ChunkWalk w,
                                                    uint8_t* sgen, uint32_t sbase, uint32_t bars,
@@ -248,22 +249,25 @@ __device__ __forceinline__ void chunk_convert_role(const CacheAttnArgs& a, Chunk
   using L = ChunkLayout<D>;
   constexpr int S = L::kStages, R = L::kRaw;
   constexpr int kRawFull = kCbKVFull + 2 * S, kRawFree = kRawFull + R;
-  constexpr int kLanesPerRow = D / 16;                 // 16 bytes each
+  constexpr int kLanesPerRow = D / 16;
   constexpr int kRowsPerLoad = 4 * 32 / kLanesPerRow;  // of the four warps together
   constexpr int kLoads = 4;                            // in registers at once
   constexpr int kRounds = kChunkKeys / kRowsPerLoad / kLoads;
   auto bar = [&](int i) { return bars + 8u * static_cast<uint32_t>(i); };
   const int cw = warp & 3;
-  const int r0 = cw * (32 / kLanesPerRow) + lane / kLanesPerRow;  // this thread's first row
-  const int c = lane % kLanesPerRow;                              // its 16-byte chunk
-  // 16 codes become 32 bytes, two chunks of the row's 128-byte panel; lanes of
-  // the second panel write theirs in the other order (bank conflicts)
-  const int panel = D == 128 ? c >> 2 : 0;
-  const uint32_t x7 = static_cast<uint32_t>(r0 & 7);  // (rows of a thread are equal mod 8)
-  static_assert(kRowsPerLoad % 8 == 0, "one swizzle for all of a thread's rows");
-  const uint32_t ch = static_cast<uint32_t>(2 * (D == 128 ? c & 3 : c));
-  const uint32_t to0 = static_cast<uint32_t>(panel * kPanelBytes + r0 * 128) + (((ch + panel) ^ x7) << 4);
-  const uint32_t to1 = static_cast<uint32_t>(panel * kPanelBytes + r0 * 128) + (((ch + (panel ^ 1)) ^ x7) << 4);
+  // Row and chunk of a lane. d = 128: 16 lanes take two rows, eight of them the
+  // first half of one row and the second half of the other, which conflicts
+  // neither on the 128-byte rows read nor on the swizzled panels written. d = 64:
+  // eight lanes take two rows of 64 bytes, one after another.
+  const int l16 = lane & 15;
+  const int r0 = D == 128 ? cw * 4 + (lane >> 4) * 2 + (((l16 >> 2) ^ (l16 >> 3)) & 1)
+                          : cw * 8 + (lane >> 2);
+  const int c = D == 128 ? (l16 & 7) : (lane & 3);
+  const int panel = c >> 2;
+  static_assert(kRowsPerLoad % 8 == 0, "one swizzle for all rows of a thread");
+  const uint32_t row_at = static_cast<uint32_t>(panel * kPanelBytes + r0 * 128);
+  const uint32_t ch = static_cast<uint32_t>(2 * (c & 3)), x7 = static_cast<uint32_t>(r0 & 7);
+  const uint32_t to0 = row_at + ((ch ^ x7) << 4), to1 = row_at + (((ch + 1u) ^ x7) << 4);
   unsigned long long* const s_nan = reinterpret_cast<unsigned long long*>(sgen + L::kOffNan);
   const uint8_t* const s_hidden = sgen + L::kOffBar + kChunkSlotHidden;
   uint32_t ring = 0, count = 0;  // slots filled, tiles done
@@ -271,72 +275,72 @@ __device__ __forceinline__ void chunk_convert_role(const CacheAttnArgs& a, Chunk
   do {
     const int first_seen = keys_seen(
         a, w.s, static_cast<int>(static_cast<long long>(w.rb) * kChunkRows / a.group));
-    for (int t = w.t0; t < w.real_end && ok; ++t) {
-      const int key0 = t * kChunkKeys;
+    const int halves = 2 * max(0, w.real_end - w.t0);  // K and V of each tile
 #pragma unroll 1
-      for (int is_v = 0; is_v < 2; ++is_v) {
-        const uint32_t slot = ring % S, raw = ring % R;
-        if (!(ok = wait_bounded_warp(bar(kRawFull + raw), (ring / R) & 1u, ab, kStatusProducer) &&
-                   wait_bounded_warp(bar(kCbKVFull + S + slot), ((ring / S) & 1u) ^ 1u, ab,
-                                     kStatusProducer)))
-          break;
-        const uint32_t src = sbase + L::kOffRaw + raw * L::kRawBytes +
-                             static_cast<uint32_t>(r0 * D + 16 * c);
-        const uint32_t dst = sbase + L::kOffKV + slot * L::kTileBytes;
-        const uint32_t hidden = s_hidden[raw];
-        const bool edge = hidden != 0u || (is_v && key0 + kChunkKeys > first_seen);
+    for (int h = 0; h < halves; ++h, ++ring) {
+      const bool is_v = (h & 1) != 0;
+      const int key0 = (w.t0 + (h >> 1)) * kChunkKeys;
+      const uint32_t slot = ring % S, raw = ring % R;
+      if (!(ok = wait_bounded_warp(bar(kRawFull + raw), (ring / R) & 1u, ab, kStatusProducer) &&
+                 wait_bounded_warp(bar(kCbKVFull + S + slot), ((ring / S) & 1u) ^ 1u, ab,
+                                   kStatusProducer)))
+        break;
+      const uint32_t src = sbase + L::kOffRaw + raw * L::kRawBytes +
+                           static_cast<uint32_t>(r0 * D + 16 * c);
+      const uint32_t dst = sbase + L::kOffKV + slot * L::kTileBytes;
+      const uint32_t hidden = s_hidden[raw];
+      const bool edge = hidden != 0u || (is_v && key0 + kChunkKeys > first_seen);
 #pragma unroll 1
-        for (int rd = 0; rd < kRounds; ++rd) {
-          uint4 x[kLoads];
+      for (int rd = 0; rd < kRounds; ++rd) {
+        const int off = rd * kLoads * kRowsPerLoad;  // first row of the round
+        uint4 x[kLoads];
 #pragma unroll
-          for (int l = 0; l < kLoads; ++l)
-            x[l] = lds128(src + static_cast<uint32_t>((rd * kLoads + l) * kRowsPerLoad * D));
-          if (edge) {
+        for (int l = 0; l < kLoads; ++l)
+          x[l] = lds128(src + static_cast<uint32_t>((off + l * kRowsPerLoad) * D));
+        if (edge) {
 #pragma unroll
-            for (int l = 0; l < kLoads; ++l) {
-              const int row = r0 + (rd * kLoads + l) * kRowsPerLoad, key = key0 + row;
-              if (((hidden >> (row >> 4)) & 1u) || (is_v && key >= w.s.kv_len)) {
-                x[l] = make_uint4(0u, 0u, 0u, 0u);
-              } else if (is_v && key >= first_seen) {
-                // seen by later rows only: a weight of 0 times NaN must not reach
-                // the others, so NaN is taken out and its key noted per column
-                uint32_t v[4] = {x[l].x, x[l].y, x[l].z, x[l].w};
-                if (nan_bytes(v[0]) | nan_bytes(v[1]) | nan_bytes(v[2]) | nan_bytes(v[3])) {
+          for (int l = 0; l < kLoads; ++l) {
+            const int row = r0 + off + l * kRowsPerLoad, key = key0 + row;
+            if (((hidden >> (row >> 4)) & 1u) || (is_v && key >= w.s.kv_len)) {
+              x[l] = make_uint4(0u, 0u, 0u, 0u);
+            } else if (is_v && key >= first_seen) {
+              // seen by later rows only: a weight of 0 times NaN must not reach
+              // the others, so NaN is taken out and its key noted per column
+              uint32_t v[4] = {x[l].x, x[l].y, x[l].z, x[l].w};
+              if (nan_bytes(v[0]) | nan_bytes(v[1]) | nan_bytes(v[2]) | nan_bytes(v[3])) {
 #pragma unroll
-                  for (int q = 0; q < 4; ++q) {
-                    const uint32_t bad = nan_bytes(v[q]);
-                    for (int y = 0; y < 4; ++y)
-                      if ((bad >> (8 * y)) & 0x80u) {
-                        atomicMax(s_nan + (w.item & 7) * D + 16 * c + 4 * q + y,
-                                  (static_cast<unsigned long long>(w.item + 1) << 32) |
-                                      static_cast<unsigned>(0x7FFFFFFF - key));
-                        v[q] &= ~(0xFFu << (8 * y));
-                      }
-                  }
-                  x[l] = make_uint4(v[0], v[1], v[2], v[3]);
+                for (int q = 0; q < 4; ++q) {
+                  const uint32_t bad = nan_bytes(v[q]);
+                  for (int y = 0; y < 4; ++y)
+                    if ((bad >> (8 * y)) & 0x80u) {
+                      atomicMax(s_nan + (w.item & 7) * D + 16 * c + 4 * q + y,
+                                (static_cast<unsigned long long>(w.item + 1) << 32) |
+                                    static_cast<unsigned>(0x7FFFFFFF - key));
+                      v[q] &= ~(0xFFu << (8 * y));
+                    }
                 }
+                x[l] = make_uint4(v[0], v[1], v[2], v[3]);
               }
             }
           }
+        }
 #pragma unroll
-          for (int l = 0; l < kLoads; ++l) {
-            const uint32_t at = dst + static_cast<uint32_t>((rd * kLoads + l) * kRowsPerLoad * 128);
-            const uint32_t a0 = panel ? x[l].z : x[l].x, a1 = panel ? x[l].w : x[l].y;
-            const uint32_t b0 = panel ? x[l].x : x[l].z, b1 = panel ? x[l].y : x[l].w;
-            ptx::st_shared_v4(at + to0, widen_lo(a0), widen_hi(a0), widen_lo(a1), widen_hi(a1));
-            ptx::st_shared_v4(at + to1, widen_lo(b0), widen_hi(b0), widen_lo(b1), widen_hi(b1));
-          }
+        for (int l = 0; l < kLoads; ++l) {
+          const uint32_t at = dst + static_cast<uint32_t>((off + l * kRowsPerLoad) * 128);
+          ptx::st_shared_v4(at + to0, widen_lo(x[l].x), widen_hi(x[l].x), widen_lo(x[l].y),
+                            widen_hi(x[l].y));
+          ptx::st_shared_v4(at + to1, widen_lo(x[l].z), widen_hi(x[l].z), widen_lo(x[l].w),
+                            widen_hi(x[l].w));
         }
-        ptx::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          ptx::mbar_arrive(bar(kRawFree + raw));
-          ptx::mbar_arrive(bar(kCbKVFull + slot));
-          if (is_v) ptx::mbar_arrive(bar(kCbVDone + (count & 7)));
-        }
-        ++ring;
       }
-      ++count;
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        ptx::mbar_arrive(bar(kRawFree + raw));
+        ptx::mbar_arrive(bar(kCbKVFull + slot));
+        if (is_v) ptx::mbar_arrive(bar(kCbVDone + (count & 7)));
+      }
+      count += is_v ? 1u : 0u;
     }
   } while (ok && w.next(a));
 }
