@@ -43,6 +43,25 @@ struct CacheAppendArgs {
   int T, Hkv, n_slots;  // n_slots = num_blocks * block
 };
 
+// What the join kernel has to do for CTA c: join the partial results of an item
+// (16 bytes; what = rows << 16 | parts, 0: nothing).
+struct alignas(16) JoinItem {
+  int b, hk, rb, what;
+};
+__host__ __device__ inline JoinItem join_item(int b, int hk, int rb, int rows, int parts) {
+  return JoinItem{b, hk, rb, (rows << 16) | parts};
+}
+__host__ __device__ inline int join_parts(const JoinItem& j) { return j.what & 0xFFFF; }
+__host__ __device__ inline int join_rows(const JoinItem& j) { return j.what >> 16; }
+
+// The partial results of a call's launches: the step kernel's (0), the chunk kernel's (1).
+struct JoinSides {
+  JoinItem* join[2];
+  float* parts[2];
+  int ctas[2];  // of the launch; 0: nothing to join
+  int rows[2];  // of an item
+};
+
 struct CacheAttnArgs {
   const void* q;
   void* o;
@@ -60,7 +79,11 @@ struct CacheAttnArgs {
   int causal;
   float scale_log2;  // scale * log2(e)
   uint32_t* status;
-  float* ws;
+  // sequences of more than rows_over and at most rows_upto rows to a K / V head
+  // are this launch's; the others are left alone
+  int rows_over, rows_upto;
+  JoinItem* join;  // [CTAs of the launch]
+  float* parts;    // [CTAs of the launch][2] partial results
 };
 
 cudaError_t launch_cache_plan(const CachePlanArgs& a, int sm_count, cudaStream_t stream);
@@ -68,7 +91,7 @@ cudaError_t launch_cache_append(const CacheAppendArgs& a, int block, int d, bool
                                 int sm_count, cudaStream_t stream);
 // False in *mapped: a tensor map could not be encoded.
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, const fa_cache& c, bool bf16, int sm_count,
-                              cudaStream_t stream, bool* mapped);
+                              float* ws, cudaStream_t stream, bool* mapped);
 
 // fa_host.cu: a cache's K or V as a 4-D byte map {d, token in block, head,
 // block}; box = `rows` tokens of one head and block, swizzled over its d bytes
@@ -102,6 +125,12 @@ __device__ __forceinline__ SeqRows seq_rows(const CacheAttnArgs& a, int b) {
   const int len = max(__ldg(a.kv_lens + b), 0);
   s.kv_len = len < most ? len : static_cast<int>(most);
   return s;
+}
+
+// Whether a launch computes a sequence.
+__device__ __forceinline__ bool takes_seq(const CacheAttnArgs& a, const SeqRows& s) {
+  const long long rows = static_cast<long long>(s.count) * a.group;
+  return rows > a.rows_over && rows <= a.rows_upto;
 }
 
 // Element offsets of query row i of sequence b, head h, in q / o, and its LSE index.

@@ -1,94 +1,156 @@
-// fa_fwd_cache: choice of kernel and launches.
+// fa_fwd_cache: choice of kernels and launches.
+#include <climits>
+
 #include "fa_cache_chunk.cuh"
 
 namespace fa {
 namespace {
 
-// The join of a launch of `grid` shares with `rows` rows an item, set up while
-// that launch still runs.
-template <int D, bool BF16>
-cudaError_t launch_join(const CacheAttnArgs& a, int grid, int rows, cudaStream_t stream) {
+// Kernels of a call. The lengths are device memory, so the choice goes by the
+// sizes that the host knows. Both kernels compute any number of rows; they
+// differ in how many go through the cache together.
+struct AttnPlan {
+  int nt = 0;          // 8-row groups of the step kernel's instance; 0: not launched
+  bool chunk = false;  // the chunk kernel
+  int upto = INT_MAX;  // with both: most rows of the step kernel's sequences
+};
+
+AttnPlan plan_attn(int B, int T, int group, bool ragged) {
+  AttnPlan p;
+  const long long most = static_cast<long long>(T) * group;  // rows of a sequence to a K / V head
+  if (!ragged || B == 1 || T <= B || most <= kStepMaxRows) {
+    // sequences of one size, of a token each (as a rule), or small in any case
+    const long long rows = !ragged ? most / B : (T <= B && B > 1 ? group : most);
+    p.nt = rows <= 8 ? 1 : (rows <= kStepMaxRows ? 2 : 0);
+    p.chunk = p.nt == 0;
+  } else if (group > kStepMaxRows) {
+    p.chunk = true;
+  } else {
+    // a batch of single tokens and longer pieces, in a mixture that only the
+    // device knows: each sequence goes to the kernel of its size
+    p.nt = 2;
+    p.chunk = true;
+    p.upto = kStepMaxRows;
+  }
+  return p;
+}
+
+int step_grid(const AttnPlan& p, int sm_count) { return p.nt == 0 ? 0 : 2 * sm_count; }
+
+// Workspace: the join items of both launches, then their partial results.
+long long plan_floats(const AttnPlan& p, int d, int sm_count) {
+  const long long s = step_grid(p, sm_count), c = p.chunk ? sm_count : 0;
+  return 4 * (s + c) + 2 * s * partial_floats(8 * p.nt, d) + 2 * c * partial_floats(kChunkRows, d);
+}
+
+// Launches `kern` so that it may be set up while the launch before it ends.
+template <typename... Params, typename... Args>
+cudaError_t launch_early(void (*kern)(Params...), dim3 grid, int threads, int smem,
+                         cudaStream_t stream, Args... args) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid),
-                     static_cast<unsigned>((rows + kJoinRows - 1) / kJoinRows));
-  cfg.blockDim = dim3(kJoinThreads);
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = stream;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fa_cache_join_kernel<D, BF16>, a, rows);
+  return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 template <int D, bool BF16, int NT>
-cudaError_t launch_step(const CacheAttnArgs& a, const CUtensorMap* maps, int sm_count,
+cudaError_t launch_step(const CacheAttnArgs& a, const CUtensorMap* maps, bool whole, int grid,
                         cudaStream_t stream) {
   constexpr int kSmem = StepLayout<D>::kSmem;
   auto kern = fa_cache_step_kernel<D, BF16, NT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  const int grid = 2 * sm_count;
-  // sequences of at most one round of tiles (a tile for each warp) are never
-  // cut: nothing to join, one launch
-  const bool whole = (static_cast<long long>(a.table_width) << a.block_shift) <=
-                     kStepWarps * step_keys(D);
   kern<<<grid, kStepThreads, kSmem, stream>>>(maps[0], maps[1], a, whole ? 1 : 0);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || whole) return e;
-  return launch_join<D, BF16>(a, grid, 8 * NT, stream);
+  return cudaGetLastError();
 }
 
 template <int D, bool BF16>
-cudaError_t launch_chunk(const CacheAttnArgs& a, const CUtensorMap* maps, int sm_count,
-                         cudaStream_t stream) {
-  constexpr int kSmem = ChunkLayout<D>::kSmem;
-  auto kern = fa_cache_chunk_kernel<D, BF16>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (e != cudaSuccess) return e;
-  kern<<<sm_count, kChunkThreads, kSmem, stream>>>(maps[0], maps[1], a);
-  e = cudaGetLastError();
-  return e != cudaSuccess ? e : launch_join<D, BF16>(a, sm_count, kChunkRows, stream);
-}
-
-// Rows that share a K / V head, on average over the sequences: up to 16 go
-// through the step kernel, more through the chunk kernel. Either one computes
-// any number of rows.
-bool runs_steps(int B, int T, int group) {
-  return ((static_cast<long long>(T) + B - 1) / B) * group <= kStepMaxRows;
-}
-
-template <int D>
-cudaError_t pick(const CacheAttnArgs& a, const CUtensorMap* maps, bool bf16, int sm_count,
-                 cudaStream_t s) {
-  if (!runs_steps(a.B, a.T, a.group))
-    return bf16 ? launch_chunk<D, true>(a, maps, sm_count, s)
-                : launch_chunk<D, false>(a, maps, sm_count, s);
-  if (((static_cast<long long>(a.T) + a.B - 1) / a.B) * a.group <= 8)
-    return bf16 ? launch_step<D, true, 1>(a, maps, sm_count, s)
-                : launch_step<D, false, 1>(a, maps, sm_count, s);
-  return bf16 ? launch_step<D, true, 2>(a, maps, sm_count, s)
-              : launch_step<D, false, 2>(a, maps, sm_count, s);
+cudaError_t launch_all(CacheAttnArgs a, const fa_cache& c, const AttnPlan& p, int sm_count,
+                       float* ws, cudaStream_t stream, bool* mapped) {
+  const int sgrid = step_grid(p, sm_count), cgrid = p.chunk ? sm_count : 0;
+  JoinSides sides{};
+  sides.join[0] = reinterpret_cast<JoinItem*>(ws);
+  sides.join[1] = sides.join[0] + sgrid;
+  sides.parts[0] = ws + 4LL * (sgrid + cgrid);
+  sides.parts[1] = sides.parts[0] + 2LL * sgrid * partial_floats(8 * p.nt, D);
+  sides.rows[0] = 8 * p.nt;
+  sides.rows[1] = kChunkRows;
+  sides.ctas[1] = cgrid;
+  if (p.nt != 0) {
+    // sequences of at most one round of tiles (one for each warp) are not cut:
+    // nothing to join
+    const bool whole = (static_cast<long long>(a.table_width) << a.block_shift) <=
+                       kStepWarps * step_keys(D);
+    sides.ctas[0] = whole ? 0 : sgrid;
+    a.rows_over = 0;
+    a.rows_upto = p.upto;
+    a.join = sides.join[0];
+    a.parts = sides.parts[0];
+    CUtensorMap maps[2];
+    const int rows = c.block < step_keys(D) ? c.block : step_keys(D);
+    *mapped = encode_cache(&maps[0], c.k, c, rows, true) && encode_cache(&maps[1], c.v, c, rows, true);
+    if (!*mapped) return cudaErrorUnknown;
+    const cudaError_t e = p.nt == 2 ? launch_step<D, BF16, 2>(a, maps, whole, sgrid, stream)
+                                    : launch_step<D, BF16, 1>(a, maps, whole, sgrid, stream);
+    if (e != cudaSuccess) return e;
+  }
+  if (p.chunk) {
+    constexpr int kSmem = ChunkLayout<D>::kSmem;
+    auto kern = fa_cache_chunk_kernel<D, BF16>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    a.rows_over = p.nt != 0 ? p.upto : 0;
+    a.rows_upto = INT_MAX;
+    a.join = sides.join[1];
+    a.parts = sides.parts[1];
+    CUtensorMap maps[2];
+    *mapped = encode_cache(&maps[0], c.k, c, c.block, false) &&
+              encode_cache(&maps[1], c.v, c, c.block, false);
+    if (!*mapped) return cudaErrorUnknown;
+    // after a step launch it takes the SMs that are done with that one (its
+    // CTAs wait for the step launch before they end)
+    if (p.nt != 0) {
+      e = launch_early(kern, dim3(cgrid), kChunkThreads, kSmem, stream, maps[0], maps[1], a);
+    } else {
+      kern<<<cgrid, kChunkThreads, kSmem, stream>>>(maps[0], maps[1], a);
+      e = cudaGetLastError();
+    }
+    if (e != cudaSuccess) return e;
+  }
+  const int n = sides.ctas[0] + sides.ctas[1];
+  if (n == 0) return cudaSuccess;
+  const int rows = cgrid > 0 ? sides.rows[1] : sides.rows[0];
+  return launch_early(fa_cache_join_kernel<D, BF16>,
+                      dim3(static_cast<unsigned>(n),
+                           static_cast<unsigned>((rows + kJoinRows - 1) / kJoinRows)),
+                      kJoinThreads, 0, stream, a, sides);
 }
 
 }  // namespace
 
 long long cache_workspace_floats(int B, int T, int group, int d, int sm_count) {
-  const bool steps = runs_steps(B, T, group);
-  const long long grid = steps ? 2LL * sm_count : sm_count;
-  return 4 * grid + 2 * grid * partial_floats(steps ? kStepMaxRows : kChunkRows, d);
+  // the larger of what a ragged call and one of equal sequences take
+  const long long r = plan_floats(plan_attn(B, T, group, true), d, sm_count);
+  const long long u = T % B == 0 ? plan_floats(plan_attn(B, T, group, false), d, sm_count) : 0;
+  return r > u ? r : u;
 }
 
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, const fa_cache& c, bool bf16, int sm_count,
-                              cudaStream_t stream, bool* mapped) {
-  CUtensorMap maps[2];
-  const bool steps = runs_steps(a.B, a.T, a.group);
-  const int keys = steps ? step_keys(c.d) : kChunkKeys, rows = c.block < keys ? c.block : keys;
-  *mapped = encode_cache(&maps[0], c.k, c, rows, steps) &&
-            encode_cache(&maps[1], c.v, c, rows, steps);
-  if (!*mapped) return cudaErrorUnknown;
-  return c.d == 64 ? pick<64>(a, maps, bf16, sm_count, stream)
-                   : pick<128>(a, maps, bf16, sm_count, stream);
+                              float* ws, cudaStream_t stream, bool* mapped) {
+  const AttnPlan p = plan_attn(a.B, a.T, a.group, a.cu_q != nullptr);
+  *mapped = true;
+  if (c.d == 64)
+    return bf16 ? launch_all<64, true>(a, c, p, sm_count, ws, stream, mapped)
+                : launch_all<64, false>(a, c, p, sm_count, ws, stream, mapped);
+  return bf16 ? launch_all<128, true>(a, c, p, sm_count, ws, stream, mapped)
+              : launch_all<128, false>(a, c, p, sm_count, ws, stream, mapped);
 }
 
 }  // namespace fa

@@ -44,7 +44,7 @@ constexpr int kChunkKeys = 128;
 constexpr int kChunkMinShare = 2;  // tiles
 // Registers a thread after setmaxnreg (sum 512 = 4 x 128): MMA and copy
 // warpgroup, each softmax warpgroup, converters.
-constexpr uint32_t kChunkRegsMma = 56, kChunkRegsSoftmax = 192, kChunkRegsConvert = 72;
+constexpr uint32_t kChunkRegsMma = 64, kChunkRegsSoftmax = 184, kChunkRegsConvert = 80;
 static_assert(kChunkRegsMma + 2 * kChunkRegsSoftmax + kChunkRegsConvert == 512, "register split");
 
 template <int D>
@@ -94,7 +94,9 @@ __device__ __forceinline__ int keys_seen(const CacheAttnArgs& a, const SeqRows& 
 // Row blocks of a sequence, and the tiles that one of them reads (counted: at
 // least one, so that rows without keys are written).
 __device__ __forceinline__ int chunk_row_blocks(const CacheAttnArgs& a, const SeqRows& s) {
-  return static_cast<int>((static_cast<long long>(s.count) * a.group + kChunkRows - 1) / kChunkRows);
+  return takes_seq(a, s) ? static_cast<int>(
+                               (static_cast<long long>(s.count) * a.group + kChunkRows - 1) / kChunkRows)
+                         : 0;
 }
 __device__ __forceinline__ int chunk_real_tiles(const CacheAttnArgs& a, const SeqRows& s, int rb) {
   const long long last = min((rb + 1LL) * kChunkRows, static_cast<long long>(s.count) * a.group) - 1;
@@ -251,8 +253,7 @@ __device__ __forceinline__ void chunk_convert_role(const CacheAttnArgs& a, Chunk
   constexpr int kRawFull = kCbKVFull + 2 * S, kRawFree = kRawFull + R;
   constexpr int kLanesPerRow = D / 16;
   constexpr int kRowsPerLoad = 4 * 32 / kLanesPerRow;  // of the four warps together
-  constexpr int kLoads = 4;                            // in registers at once
-  constexpr int kRounds = kChunkKeys / kRowsPerLoad / kLoads;
+  constexpr int kLoads = kChunkKeys / kRowsPerLoad;
   auto bar = [&](int i) { return bars + 8u * static_cast<uint32_t>(i); };
   const int cw = warp & 3;
   // Row and chunk of a lane. d = 128: 16 lanes take two rows, eight of them the
@@ -290,48 +291,47 @@ __device__ __forceinline__ void chunk_convert_role(const CacheAttnArgs& a, Chunk
       const uint32_t dst = sbase + L::kOffKV + slot * L::kTileBytes;
       const uint32_t hidden = s_hidden[raw];
       const bool edge = hidden != 0u || (is_v && key0 + kChunkKeys > first_seen);
+      if (edge) {
+        // put right in the raw tile, each thread the codes that it reads below
 #pragma unroll 1
-      for (int rd = 0; rd < kRounds; ++rd) {
-        const int off = rd * kLoads * kRowsPerLoad;  // first row of the round
-        uint4 x[kLoads];
+        for (int l = 0; l < kLoads; ++l) {
+          const int row = r0 + l * kRowsPerLoad, key = key0 + row;
+          const uint32_t at = src + static_cast<uint32_t>(l * kRowsPerLoad * D);
+          if (((hidden >> (row >> 4)) & 1u) || (is_v && key >= w.s.kv_len)) {
+            ptx::st_shared_v4(at, 0u, 0u, 0u, 0u);
+          } else if (is_v && key >= first_seen) {
+            // seen by later rows only: a weight of 0 times NaN must not reach
+            // the others, so NaN is taken out and its key noted per column
+            const uint4 x = lds128(at);
+            uint32_t v[4] = {x.x, x.y, x.z, x.w};
+            if (nan_bytes(v[0]) | nan_bytes(v[1]) | nan_bytes(v[2]) | nan_bytes(v[3])) {
 #pragma unroll
-        for (int l = 0; l < kLoads; ++l)
-          x[l] = lds128(src + static_cast<uint32_t>((off + l * kRowsPerLoad) * D));
-        if (edge) {
-#pragma unroll
-          for (int l = 0; l < kLoads; ++l) {
-            const int row = r0 + off + l * kRowsPerLoad, key = key0 + row;
-            if (((hidden >> (row >> 4)) & 1u) || (is_v && key >= w.s.kv_len)) {
-              x[l] = make_uint4(0u, 0u, 0u, 0u);
-            } else if (is_v && key >= first_seen) {
-              // seen by later rows only: a weight of 0 times NaN must not reach
-              // the others, so NaN is taken out and its key noted per column
-              uint32_t v[4] = {x[l].x, x[l].y, x[l].z, x[l].w};
-              if (nan_bytes(v[0]) | nan_bytes(v[1]) | nan_bytes(v[2]) | nan_bytes(v[3])) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                  const uint32_t bad = nan_bytes(v[q]);
-                  for (int y = 0; y < 4; ++y)
-                    if ((bad >> (8 * y)) & 0x80u) {
-                      atomicMax(s_nan + (w.item & 7) * D + 16 * c + 4 * q + y,
-                                (static_cast<unsigned long long>(w.item + 1) << 32) |
-                                    static_cast<unsigned>(0x7FFFFFFF - key));
-                      v[q] &= ~(0xFFu << (8 * y));
-                    }
-                }
-                x[l] = make_uint4(v[0], v[1], v[2], v[3]);
+              for (int q = 0; q < 4; ++q) {
+                const uint32_t bad = nan_bytes(v[q]);
+                for (int y = 0; y < 4; ++y)
+                  if ((bad >> (8 * y)) & 0x80u) {
+                    atomicMax(s_nan + (w.item & 7) * D + 16 * c + 4 * q + y,
+                              (static_cast<unsigned long long>(w.item + 1) << 32) |
+                                  static_cast<unsigned>(0x7FFFFFFF - key));
+                    v[q] &= ~(0xFFu << (8 * y));
+                  }
               }
+              ptx::st_shared_v4(at, v[0], v[1], v[2], v[3]);
             }
           }
         }
+      }
+      uint4 x[kLoads];
 #pragma unroll
-        for (int l = 0; l < kLoads; ++l) {
-          const uint32_t at = dst + static_cast<uint32_t>((off + l * kRowsPerLoad) * 128);
-          ptx::st_shared_v4(at + to0, widen_lo(x[l].x), widen_hi(x[l].x), widen_lo(x[l].y),
-                            widen_hi(x[l].y));
-          ptx::st_shared_v4(at + to1, widen_lo(x[l].z), widen_hi(x[l].z), widen_lo(x[l].w),
-                            widen_hi(x[l].w));
-        }
+      for (int l = 0; l < kLoads; ++l)
+        x[l] = lds128(src + static_cast<uint32_t>(l * kRowsPerLoad * D));
+#pragma unroll
+      for (int l = 0; l < kLoads; ++l) {
+        const uint32_t at = dst + static_cast<uint32_t>(l * kRowsPerLoad * 128);
+        ptx::st_shared_v4(at + to0, widen_lo(x[l].x), widen_hi(x[l].x), widen_lo(x[l].y),
+                          widen_hi(x[l].y));
+        ptx::st_shared_v4(at + to1, widen_lo(x[l].z), widen_hi(x[l].z), widen_lo(x[l].w),
+                          widen_hi(x[l].w));
       }
       ptx::fence_proxy_async_smem();
       __syncwarp();
@@ -606,11 +606,11 @@ __device__ __forceinline__ void chunk_softmax_role(const CacheAttnArgs& a, Chunk
     const bool begins = w.t0 == 0, ends = w.t1 == w.tiles;
     float* part = nullptr;
     if (!begins || !ends)
-      part = a.ws + 4LL * gridDim.x +
-             (2LL * blockIdx.x + (begins ? 1 : 0)) * partial_floats(kChunkRows, D);
+      part = a.parts + (2LL * blockIdx.x + (begins ? 1 : 0)) * partial_floats(kChunkRows, D);
     if (!ends && begins && wg == 0 && r == 0)
-      reinterpret_cast<JoinItem*>(a.ws)[blockIdx.x] =
-          JoinItem{w.b, w.hk, w.rb, 1 + static_cast<int>((w.tiles - w.t1 + share - 1) / share)};
+      a.join[blockIdx.x] =
+          join_item(w.b, w.hk, w.rb, rows,
+                    1 + static_cast<int>((w.tiles - w.t1 + share - 1) / share));
     const bool two = !pair && n > 1;  // results of two warpgroups
     if (two && wg == 1) {
       s_m[r] = m_ref;
@@ -754,7 +754,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     }
     *abort_flag = 0u;
     ptx::fence_mbar_init();
-    reinterpret_cast<JoinItem*>(a.ws)[blockIdx.x] = JoinItem{0, 0, 0, 0};
+    a.join[blockIdx.x] = JoinItem{0, 0, 0, 0};
   }
   for (int i = tid; i < 8 * D; i += kChunkThreads)
     reinterpret_cast<unsigned long long*>(sgen + L::kOffNan)[i] = 0ull;
@@ -782,7 +782,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   const long long share = max((total + gridDim.x - 1) / gridDim.x,
                               static_cast<long long>(kChunkMinShare));
   const long long u0 = share * blockIdx.x, u1 = min(u0 + share, total);
-  if (u0 >= u1) return;
+  if (u0 >= u1) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
   if (u0 >= upto - mine && u0 < upto) {
     long long at = upto - mine, head_tiles;
     int b = b0;
@@ -834,6 +837,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   __syncthreads();
   ptx::tc_fence_after();
   if (warp == 0) ptx::tmem_dealloc(tmem, L::kTmemCols);
+  // This launch may run beside the step kernel's last CTAs. It ends behind it,
+  // so that the join, which waits for this one, finds both complete.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 }  // namespace fa

@@ -212,10 +212,10 @@ fa_status fa_fwd_cache(const void* q, const fa_cache* cache, const int32_t* bloc
   a.block_shift = block_shift(cache->block);
   a.causal = causal != 0;
   a.scale_log2 = scale * 1.4426950408889634f;
-  a.ws = static_cast<float*>(workspace);
   (void)cudaGetLastError();
   bool mapped = true;
   const cudaError_t e = fa::launch_cache_attn(a, *cache, dtype == FA_DTYPE_BF16, sms,
+                                              static_cast<float*>(workspace),
                                               static_cast<cudaStream_t>(stream), &mapped);
   return mapped ? done(e) : FA_ERR_CUDA;
 }

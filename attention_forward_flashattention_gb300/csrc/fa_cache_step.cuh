@@ -51,11 +51,6 @@ __host__ __device__ constexpr int step_keys(int d) { return kStepTileBytes / d; 
 // Floats of a partial result of `rows` rows: O, m, l.
 __host__ __device__ constexpr int partial_floats(int rows, int d) { return rows * (d + 2); }
 
-// What the join kernel has to do for CTA c: join `parts` partial results of an item.
-struct JoinItem {
-  int b, hk, rb, parts;
-};
-
 // Position of a CTA's share in the list of tiles. An item with no keys counts
 // as one (empty) tile, so that its rows are written.
 template <int KT>
@@ -68,7 +63,9 @@ struct StepWalk {
 
   __device__ __forceinline__ static int row_blocks(const CacheAttnArgs& a, const SeqRows& s,
                                                    int rows) {
-    return static_cast<int>((static_cast<long long>(s.count) * a.group + rows - 1) / rows);
+    return takes_seq(a, s)
+               ? static_cast<int>((static_cast<long long>(s.count) * a.group + rows - 1) / rows)
+               : 0;
   }
   __device__ __forceinline__ static long long units(const CacheAttnArgs& a, const SeqRows& s,
                                                     int rows, bool whole) {
@@ -281,9 +278,8 @@ __global__ void __launch_bounds__(kStepThreads, 2)
   const long long fair = (total + gridDim.x - 1) / gridDim.x;
   const long long share = max(fair, static_cast<long long>(whole ? 1 : kStepWarps));
   const long long u0 = share * blockIdx.x, u1 = min(u0 + share, total);
-  JoinItem* const join =
-      reinterpret_cast<JoinItem*>(a.ws) + blockIdx.x;
-  float* const parts = a.ws + 4LL * gridDim.x;
+  JoinItem* const join = a.join + blockIdx.x;
+  float* const parts = a.parts;
   if (tid == 0 && !whole) *join = JoinItem{0, 0, 0, 0};
   if (u0 >= u1) return;
   if (u0 >= upto - mine && u0 < upto) {
@@ -599,8 +595,8 @@ __global__ void __launch_bounds__(kStepThreads, 2)
     if (!begins) part = parts + 2LL * blockIdx.x * partial_floats(kRows, D);
     else if (!ends) part = parts + (2LL * blockIdx.x + 1) * partial_floats(kRows, D);
     if (part != nullptr && begins && tid == 0)
-      *join = JoinItem{now.b, now.hk, now.rb,
-                       1 + static_cast<int>((now.tiles - now.t1 + share - 1) / share)};
+      *join = join_item(now.b, now.hk, now.rb, rows,
+                        1 + static_cast<int>((now.tiles - now.t1 + share - 1) / share));
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -679,66 +675,65 @@ __global__ void __launch_bounds__(kStepThreads, 2)
       wait_drain(bars + 8u * (n % kStepStages), (n / kStepStages) & 1u, ab, kStatusDrain);
 }
 
-// Joins the partial results of the items that fa_cache_step_kernel's shares
-// cut: block c takes the item that begins in share c and ends in a later one.
-// Warps share a row's parts when there are fewer rows than warps; parts are
-// added in a fixed order. Blocks (c, y) take the rows from y * kJoinRows on.
+// Joins the partial results of the items that the shares of a step or chunk
+// launch cut: blocks (c, y) take the rows from y * kJoinRows on of the item that
+// begins in share c and ends in a later one. Warps share a row's parts when
+// there are fewer rows than warps; parts are added in a fixed order. (Blocks
+// that first found all items and shared their rows evenly were slower by the
+// time of that search, 3 us.)
 constexpr int kJoinThreads = 256;
 constexpr int kJoinRows = 32;
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kJoinThreads)
-    fa_cache_join_kernel(const CacheAttnArgs a, const int max_rows) {
+__global__ void __launch_bounds__(kJoinThreads, 2)
+    fa_cache_join_kernel(const CacheAttnArgs a, const JoinSides sides) {
   constexpr int kWarps = kJoinThreads / 32, kPer = D / 32;
   __shared__ float s_o[kWarps][D];
-  __shared__ float s_m[kWarps], s_l[kWarps];
+  __shared__ float s_l[kWarps];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const JoinItem it = reinterpret_cast<const JoinItem*>(a.ws)[blockIdx.x];
-  if (it.parts == 0) return;
-  const float* parts = a.ws + 4LL * gridDim.x;
-  const int size = partial_floats(max_rows, D);
-  const SeqRows s = seq_rows(a, it.b);
-  const long long row0 = static_cast<long long>(it.rb) * max_rows;
+  const bool second = static_cast<int>(blockIdx.x) >= sides.ctas[0];
+  const int cta = static_cast<int>(blockIdx.x) - (second ? sides.ctas[0] : 0);
+  const int4 word = __ldcg(reinterpret_cast<const int4*>(second ? sides.join[1] : sides.join[0]) + cta);
+  const JoinItem it{word.x, word.y, word.z, word.w};
   const int first = static_cast<int>(blockIdx.y) * kJoinRows;
-  const int rows = static_cast<int>(
-      min(min(static_cast<long long>(max_rows), static_cast<long long>(s.count) * a.group - row0),
-          static_cast<long long>(first + kJoinRows)));
+  const int n = join_parts(it), rows = min(join_rows(it), first + kJoinRows);
   if (first >= rows) return;
+  const int max_rows = second ? sides.rows[1] : sides.rows[0];
+  const float* parts = second ? sides.parts[1] : sides.parts[0];
+  const int size = partial_floats(max_rows, D);
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
   int per_row = 1;  // warps for a row: a power of two
   while (per_row * 2 * (rows - first) <= kWarps) per_row *= 2;
-  auto part = [&](int p) {
-    return parts + (2LL * (static_cast<long long>(blockIdx.x) + p) + (p == 0 ? 1 : 0)) * size;
-  };
+  auto part = [&](int p) { return parts + (2LL * (cta + p) + (p == 0 ? 1 : 0)) * size; };
+  const SeqRows s = seq_rows(a, it.b);
   for (int r0 = first; r0 < rows; r0 += kWarps / per_row) {
     const int r = r0 + warp / per_row, k = warp % per_row;
     float m = -INFINITY, l = 0.f, o[kPer] = {};
     if (r < rows) {
       // the largest reference of all of the row's parts first, so that nothing is rescaled
-      for (int p = lane; p < it.parts; p += 32) m = fmaxf(m, part(p)[max_rows * D + r]);
+      for (int p = lane; p < n; p += 32) m = fmaxf(m, __ldcg(part(p) + max_rows * D + r));
 #pragma unroll
       for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
 #pragma unroll 8
-      for (int p = k; p < it.parts; p += per_row) {
+      for (int p = k; p < n; p += per_row) {
         const float* q = part(p);
-        const float mp = q[max_rows * D + r];
+        const float mp = __ldcg(q + max_rows * D + r);
         const float f = mp == -INFINITY ? 0.f : ptx::ex2(mp - m);
-        l = fmaf(q[max_rows * D + max_rows + r], f, l);
+        l = fmaf(__ldcg(q + max_rows * D + max_rows + r), f, l);
         if constexpr (kPer == 4) {
-          const float4 v = *reinterpret_cast<const float4*>(q + r * D + 4 * lane);
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(q + r * D + 4 * lane));
           o[0] = fmaf(v.x, f, o[0]);
           o[1] = fmaf(v.y, f, o[1]);
           o[2] = fmaf(v.z, f, o[2]);
           o[3] = fmaf(v.w, f, o[3]);
         } else {
-          const float2 v = *reinterpret_cast<const float2*>(q + r * D + 2 * lane);
+          const float2 v = __ldcg(reinterpret_cast<const float2*>(q + r * D + 2 * lane));
           o[0] = fmaf(v.x, f, o[0]);
           o[1] = fmaf(v.y, f, o[1]);
         }
       }
     }
-    if (per_row > 1) {
-      __syncthreads();
+    if (per_row > 1) {  // (one turn of the loop: each row has its warps)
 #pragma unroll
       for (int e = 0; e < kPer; ++e) s_o[warp][kPer * lane + e] = o[e];
       if (lane == 0) s_l[warp] = l;
@@ -754,8 +749,9 @@ __global__ void __launch_bounds__(kJoinThreads)
     if (r < rows && k == 0) {
       const bool none = m == -INFINITY;
       const float inv = none ? 0.f : 1.f / l;
-      const int i = static_cast<int>((row0 + r) / a.group);
-      const int h = it.hk * a.group + static_cast<int>(row0 + r - static_cast<long long>(i) * a.group);
+      const long long row = static_cast<long long>(it.rb) * max_rows + r;
+      const int i = static_cast<int>(row / a.group);
+      const int h = it.hk * a.group + static_cast<int>(row - static_cast<long long>(i) * a.group);
       uint16_t* out = static_cast<uint16_t*>(a.o) + o_offset(a, it.b, s, i, h) + kPer * lane;
       if constexpr (kPer == 4)
         *reinterpret_cast<uint2*>(out) = make_uint2(pack2<BF16>(o[0] * inv, o[1] * inv),

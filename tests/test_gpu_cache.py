@@ -267,6 +267,16 @@ def test_query_counts(n, H, heads, d, dtype):
                    q_layout="bhnd" if n % 2 else "bnhd", seed=n)
 
 
+@pytest.mark.parametrize("d,dtype,H,heads,bs", [(128, "bf16", 8, 2, 64), (64, "fp16", 16, 4, 16),
+                                                (128, "fp16", 2, 2, 128), (64, "bf16", 60, 1, 32)])
+def test_mixed_batches(d, dtype, H, heads, bs):
+    """Single tokens, drafts and chunks in one call, with and without room for them."""
+    lens = [700, 33, 1, 0, 260, 900, 64, 130, 5, 1024]
+    counts = [1, 1, 1, 1, 200, 7, 0, 130, 3, 1]
+    attention_case(lens, counts, H, heads, bs, d, dtype, True, seed=d + H)
+    attention_case(lens, counts[::-1], H, heads, bs, d, dtype, False, seed=d + H + 1)
+
+
 @pytest.mark.parametrize("lens,counts", [([3, 0, 40], [10, 1, 45]), ([1], [300])])
 def test_rows_before_the_first_key(lens, counts):
     """More query rows than keys: the first rows see nothing."""
@@ -414,7 +424,9 @@ def test_long_sequences_split_and_joined():
     rng = np.random.default_rng(12)
     for lens, n, H, heads, bs, d, dtype in (
             ([131071, 1, 70000], 1, 8, 2, 128, 128, "bf16"), ([40003], 3, 2, 1, 16, 64, "fp16"),
-            ([50001, 33], 24, 4, 1, 64, 128, "fp16"), ([30011, 0, 513], 160, 2, 2, 32, 64, "bf16")):
+            ([50001, 33], 24, 4, 1, 64, 128, "fp16"), ([30011, 0, 513], 160, 2, 2, 32, 64, "bf16"),
+            ([70001], 5, 8, 1, 128, 128, "bf16"), ([70001], 3, 8, 1, 16, 128, "fp16"),
+            ([60007], 6, 16, 2, 32, 64, "bf16")):
         B = len(lens)
         need = [(x + bs - 1) // bs for x in lens]
         P = sum(need)
