@@ -2,6 +2,8 @@
 
   _build/libfa_sm103.so    the product: C ABI of include/fa.h and fa_cache.h
   _build/libfa_selftest.so GPU unit tests of the PTX building blocks
+  _build/_fa_cache_torch.so  the block cache's calls on torch tensors (host
+                           code, g++, linked against libfa_sm103.so)
 
 Translation units are compiled in parallel (one nvcc process each), then
 linked. ptxas resource usage (registers, spills, shared memory) of every
@@ -9,10 +11,12 @@ kernel is kept in _build/ptxas_<unit>.log.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -26,6 +30,8 @@ LIB_UNITS = ["fa_host.cu", "fa_fwd_d64.cu", "fa_fwd_d128.cu", "fa_fwd_fp8.cu", "
              "fa_bwd_d64.cu", "fa_bwd_d128.cu", "fa_noalloc.cu", "fa_pipeline.cu",
              "fa_cache_host.cu", "fa_cache_plan.cu", "fa_cache_append.cu", "fa_cache_attn.cu"]
 SELFTEST_UNITS = ["selftest.cu"]
+TORCH_NAME = "_fa_cache_torch.so"
+TORCH_UNIT = "fa_cache_torch.cpp"
 HEADERS = ["ptx.cuh", "fa_common.cuh", "fa_kernel.cuh", "fa_launch.cuh", "fa_pair.cuh", "fa_bwd.cuh",
            "fa_bwd_launch.cuh", "fa_dispatch.h", "fa_cache.cuh", "fa_cache_step.cuh", "fa_cache_chunk.cuh"]
 PUBLIC_HEADERS = ["fa.h", "fa_cache.h"]
@@ -57,6 +63,32 @@ def selftest_path() -> str:
     return os.path.join(OUT, SELFTEST_NAME)
 
 
+def torch_path() -> str:
+    return os.path.join(OUT, TORCH_NAME)
+
+
+def _torch_dir() -> str:
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        raise RuntimeError("PyTorch not found")
+    return list(spec.submodule_search_locations)[0]
+
+
+def _torch_compile(nvcc: str, obj: str) -> list[str]:
+    inc = [os.path.join(_torch_dir(), "include"), os.path.join(_cuda_home(nvcc), "include"),
+           sysconfig.get_paths()["include"], INCLUDE]
+    # (system headers: their warnings are not ours)
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall"] + [x for i in inc for x in ("-isystem", i)] + [
+        "-c", os.path.join(CSRC, TORCH_UNIT), "-o", obj]
+
+
+def _torch_link(obj: str, out: str) -> list[str]:
+    lib = os.path.join(_torch_dir(), "lib")
+    return ["g++", "-shared", "-o", out, obj, "-L" + OUT, "-l:" + LIB_NAME, "-L" + lib,
+            "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-ltorch", "-lc10_cuda", "-lc10",
+            "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib]
+
+
 def _stale(target: str, sources: list[str]) -> bool:
     if not os.path.exists(target):
         return True
@@ -66,16 +98,22 @@ def _stale(target: str, sources: list[str]) -> bool:
 
 
 def build(force: bool = False, verbose: bool = False) -> tuple[str, str]:
-    """Compiles both libraries if any source is newer; returns their paths."""
+    """Compiles the libraries and the torch module if any source is newer;
+    returns the libraries' paths."""
     nvcc = nvcc_path()
     os.makedirs(OUT, exist_ok=True)
     jobs = []
     for units, name in ((LIB_UNITS, LIB_NAME), (SELFTEST_UNITS, SELFTEST_NAME)):
         if force or _stale(os.path.join(OUT, name), units):
             jobs.append((units, name))
-    if not jobs:
+    torch_job = force or bool(jobs) or _stale(torch_path(), [TORCH_UNIT])
+    if not torch_job:
         return lib_path(), selftest_path()
     procs = []
+    torch_obj = os.path.join(OUT, "fa_cache_torch.o")
+    log = open(os.path.join(OUT, "ptxas_fa_cache_torch.log"), "w")
+    procs.append((TORCH_UNIT, subprocess.Popen(_torch_compile(nvcc, torch_obj), stdout=log,
+                                               stderr=subprocess.STDOUT), log))
     for units, _ in jobs:
         for u in units:
             obj = os.path.join(OUT, u.replace(".cu", ".o"))
@@ -93,9 +131,9 @@ def build(force: bool = False, verbose: bool = False) -> tuple[str, str]:
     if failed:
         msgs = []
         for u in failed:
-            with open(os.path.join(OUT, "ptxas_" + u.replace(".cu", ".log"))) as f:
+            with open(os.path.join(OUT, f"ptxas_{os.path.splitext(u)[0]}.log")) as f:
                 msgs.append(f"--- {u}\n" + f.read()[-6000:])
-        raise RuntimeError("nvcc failed:\n" + "\n".join(msgs))
+        raise RuntimeError("compilation failed:\n" + "\n".join(msgs))
     libdir = os.path.join(_cuda_home(nvcc), "lib64")
     for units, name in jobs:
         objs = [os.path.join(OUT, u.replace(".cu", ".o")) for u in units]
@@ -104,6 +142,9 @@ def build(force: bool = False, verbose: bool = False) -> tuple[str, str]:
             "-Xlinker", "-rpath", "-Xlinker", libdir]
         subprocess.run(cmd, check=True)
         os.replace(tmp, os.path.join(OUT, name))
+    tmp = torch_path() + f".tmp{os.getpid()}"
+    subprocess.run(_torch_link(torch_obj, tmp), check=True)
+    os.replace(tmp, torch_path())
     return lib_path(), selftest_path()
 
 

@@ -6,17 +6,20 @@ appending keys and values, and the attention that reads it.
     fa.cache_append(k, v, slots, cache)                  # k, v: [T, heads, d]
     o, lse = fa.attention_forward_cache(q, cache, table, kv_lens, cu)   # q: [T, H, d]
 
-Like the rest of the binding this only marshals arguments.
+Like the rest of the binding this only marshals arguments; it does so in host
+code (_build/_fa_cache_torch.so), because a decoding step's calls are so short
+that the same checks and allocations in Python would take longer than they do.
 """
 from __future__ import annotations
 
 import ctypes
-import math
+import importlib.machinery
+import importlib.util
 import os
+import threading
 from typing import NamedTuple
 
-from . import (FA_DTYPE_BF16, FA_DTYPE_FP16, FA_OK, FaError, FaStrides, _allocating_on, _build,
-               load_library)
+from . import FA_OK, FaError, FaStrides, _build, load_library
 
 HEADER = os.path.join(_build.INCLUDE, "fa_cache.h")
 
@@ -105,71 +108,27 @@ def _strides2(strides):
 
 # ------------------------------------------------------------ torch helpers
 
-def _dtype16(t) -> int:
-    import torch
-    if t.dtype is torch.float16:
-        return FA_DTYPE_FP16
-    if t.dtype is torch.bfloat16:
-        return FA_DTYPE_BF16
-    raise TypeError(f"unsupported dtype {t.dtype} (fp16 or bf16)")
+_lock = threading.Lock()
+_native = None
 
 
-def _describe(cache, device: int) -> FaCache:
-    """The FaCache of a Cache whose tensors are on CUDA device `device`."""
-    import torch
-    k, v, ks, vs = cache
-    st, shape = k.stride(), k.shape
-    if not (len(shape) == 4 and shape == v.shape and st == v.stride() and st[3] == 1
-            and k.element_size() == 1 and v.element_size() == 1
-            and ks.shape == shape[:2] and vs.shape == shape[:2]
-            and ks.dtype is torch.float32 and vs.dtype is torch.float32
-            and ks.is_contiguous() and vs.is_contiguous()):
-        raise ValueError("cache: k, v must be [blocks, heads, block, d] 8-bit tensors of equal "
-                         "strides (1 along d) and k_scales, v_scales contiguous float32 "
-                         "[blocks, heads]")
-    if not k.get_device() == v.get_device() == ks.get_device() == vs.get_device() == device:
-        raise ValueError("cache: tensors must be on the same CUDA device as the other arguments")
-    n, heads, block, d = shape
-    # an axis of length one has no stride of its own
-    return FaCache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), n, block, heads, d,
-                   st[0] if n > 1 else 16, st[1] if heads > 1 else 16, st[2])
-
-
-def _index(t, device: int, *shape) -> int:
-    """The address of a contiguous int32 tensor of this shape on CUDA device `device`."""
-    import torch
-    if not (t.dtype is torch.int32 and t.shape == shape and t.get_device() == device
-            and t.is_contiguous()):
-        raise ValueError(f"expected a contiguous int32 tensor of shape {tuple(shape)} on CUDA "
-                         f"device {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
-
-
-def _cuda_index(t, what: str) -> int:
-    """The CUDA device index of a tensor; raises for one elsewhere."""
-    i = t.get_device()
-    if i < 0:
-        raise ValueError(f"{what}: tensors must be on a CUDA device")
-    return i
-
-
-def _call(fn, what: str, device: int, stream, *args) -> None:
-    """fn(*args, stream handle) with the tensors' device current; raises on a status."""
-    import torch
-    if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(device)
-    elif stream.device_index != device:
-        raise ValueError(f"{what}: the stream is on CUDA device {stream.device_index}, the "
-                         f"tensors on {device}")
-    else:
-        handle = stream.cuda_stream
-    if device == torch.cuda.current_device():
-        rc = fn(*args, handle)
-    else:
-        with torch.cuda.device(device):
-            rc = fn(*args, handle)
-    if rc != FA_OK:
-        raise FaError(rc, what)
+def _module():
+    """The host code of the torch calls (built in-tree by build.build()). Raises if absent."""
+    global _native
+    if _native is None:
+        import torch  # noqa: F401  (its libraries, before the module that uses them)
+        load_library()
+        with _lock:
+            if _native is None:
+                p = _build.torch_path()
+                if not os.path.exists(p):
+                    raise RuntimeError(f"torch module not built: {p} (run __graft_entry__.build())")
+                loader = importlib.machinery.ExtensionFileLoader("_fa_cache_torch", p)
+                m = importlib.util.module_from_spec(
+                    importlib.util.spec_from_file_location("_fa_cache_torch", p, loader=loader))
+                loader.exec_module(m)
+                _native = m
+    return _native
 
 
 def cache_empty(num_blocks: int, heads: int, block: int, d: int, device=None) -> Cache:
@@ -188,13 +147,10 @@ def cache_plan_into(lens, new_lens, block_table, free_blocks, free_pos, slots, c
     """Enqueues fa_cache_plan on contiguous int32 CUDA tensors: lens, new_lens,
     kv_lens [B], block_table [B, width] (in and out), free_blocks [n], free_pos
     and free_next [1], slots [T], cu_new [B + 1]."""
-    dev = _cuda_index(lens, "fa_cache_plan")
-    (B,), (T,), (n,), width = lens.shape, slots.shape, free_blocks.shape, block_table.shape[1]
-    _call(load_library().fa_cache_plan, "fa_cache_plan", dev, stream,
-          _index(lens, dev, B), _index(new_lens, dev, B), _index(block_table, dev, B, width),
-          width, _index(free_blocks, dev, n), n, _index(free_pos, dev, 1), _index(slots, dev, T),
-          T, _index(cu_new, dev, B + 1), _index(kv_lens, dev, B), _index(free_next, dev, 1), B,
-          block)
+    r = _module().cache_plan(lens, new_lens, block_table, free_blocks, free_pos,
+                             (slots, cu_new, kv_lens, free_next), 0, block, stream)
+    if type(r) is int:
+        raise FaError(r, "fa_cache_plan")
 
 
 def cache_plan(lens, new_lens, block_table, free_blocks, free_pos, n_tokens: int, block: int,
@@ -205,38 +161,20 @@ def cache_plan(lens, new_lens, block_table, free_blocks, free_pos, n_tokens: int
     the number of rows to plan, at least the sum of new_lens (slots behind the
     last token are -1). Requests that cannot be served keep their length and
     get slots -1 (see fa_cache.h)."""
-    import torch
-    _cuda_index(lens, "fa_cache_plan")
-    B, dev, i32 = lens.shape[0], lens.device, torch.int32
-    with _allocating_on(stream):
-        kv_lens, slots = torch.empty_like(lens), torch.empty(n_tokens, dtype=i32, device=dev)
-        cu_new = torch.empty(B + 1, dtype=i32, device=dev)
-        free_next = torch.empty_like(free_pos)
-    cache_plan_into(lens, new_lens, block_table, free_blocks, free_pos, slots, cu_new, kv_lens,
-                    free_next, block, stream)
-    return slots, cu_new, kv_lens, free_next
+    r = (_native or _module()).cache_plan(lens, new_lens, block_table, free_blocks, free_pos, None,
+                                          n_tokens, block, stream)
+    if type(r) is int:
+        raise FaError(r, "fa_cache_plan")
+    return r
 
 
 def cache_append(k, v, slots, cache, stream=None) -> None:
     """Enqueues fa_cache_append: k, v [T, heads, d] fp16 / bf16 CUDA tensors
     (unit stride along d, the others multiples of 8) into the slots [T] of a
     Cache, in 8 bits, with its blocks' scales."""
-    dev = _cuda_index(k, "fa_cache_append")
-    desc = _describe(cache, dev)
-    T, heads, d = k.shape
-    ks, vs = k.stride(), v.stride()
-    if not (v.shape == k.shape and v.dtype is k.dtype and v.get_device() == dev
-            and heads == desc.Hkv and d == desc.d and ks[2] == 1 and vs[2] == 1):
-        raise ValueError("k, v must be [T, heads, d] tensors of one dtype with the cache's heads "
-                         "and d, and unit d stride")
-    code, sl = _dtype16(k), _index(slots, dev, T)
-    if T == 0:
-        return
-    one = heads == 1  # an axis of length one has no stride of its own
-    st = (FaStrides * 2)((0, d if one else ks[1], ks[0] if T > 1 else d),
-                         (0, d if one else vs[1], vs[0] if T > 1 else d))
-    _call(load_library().fa_cache_append, "fa_cache_append", dev, stream,
-          k.data_ptr(), v.data_ptr(), st, sl, T, ctypes.byref(desc), code)
+    r = (_native or _module()).cache_append(k, v, slots, cache, stream)
+    if r is not None:
+        raise FaError(r, "fa_cache_append")
 
 
 def attention_forward_cache_into(q, cache, block_table, kv_lens, o, lse, workspace, cu_q=None,
@@ -248,43 +186,10 @@ def attention_forward_cache_into(q, cache, block_table, kv_lens, o, lse, workspa
     along d, the other strides are multiples of 8; lse is contiguous float32.
     block_table [B, width] and kv_lens [B] are contiguous int32; workspace: a
     uint8 tensor of fa_fwd_cache_workspace_size bytes."""
-    import torch
-    dev = _cuda_index(q, "fa_fwd_cache")
-    desc = _describe(cache, dev)
-    shape, qs, os_ = q.shape, q.stride(), o.stride()
-    B, width = block_table.shape
-    d = desc.d
-    if not (o.shape == shape and o.dtype is q.dtype and qs[-1] == 1 and os_[-1] == 1
-            and lse.shape == shape[:-1] and lse.dtype is torch.float32 and lse.is_contiguous()
-            and shape[-1] == d and workspace.dtype is torch.uint8 and workspace.is_contiguous()
-            and o.get_device() == lse.get_device() == workspace.get_device() == dev):
-        raise ValueError("q, o must be [T, H, d], [B, H, d] or [B, H, n, d] tensors of one dtype "
-                         "with the cache's d and unit d stride, lse contiguous float32 of their "
-                         "shape without d, workspace contiguous uint8, all on one device")
-    # (an axis of length one has no stride of its own)
-    if cu_q is not None and len(shape) == 3:
-        T, H = shape[0], shape[1]
-        cu = _index(cu_q, dev, B + 1)
-        q3 = (8, qs[1] if H > 1 else d, qs[0] if T > 1 else d)
-        o3 = (8, os_[1] if H > 1 else d, os_[0] if T > 1 else d)
-    elif cu_q is None and len(shape) in (3, 4) and shape[0] == B:
-        H, n = shape[1], shape[2] if len(shape) == 4 else 1
-        T, cu = B * n, None
-        q3 = (qs[0] if B > 1 else 8, qs[1] if H > 1 else d, qs[2] if n > 1 else d)
-        o3 = (os_[0] if B > 1 else 8, os_[1] if H > 1 else d, os_[2] if n > 1 else d)
-    else:
-        raise ValueError("q must be [T, H, d] with cu_q, or [B, H, d] or [B, H, n, d] without")
-    tab, kv, code = _index(block_table, dev, B, width), _index(kv_lens, dev, B), _dtype16(q)
-    if H == 0 or H % desc.Hkv:
-        raise ValueError(f"{H} query heads do not share {desc.Hkv} K / V heads evenly")
-    if T == 0:
-        return
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    _call(load_library().fa_fwd_cache, "fa_fwd_cache", dev, stream,
-          q.data_ptr(), ctypes.byref(desc), tab, width, kv, cu, o.data_ptr(), lse.data_ptr(), B, T,
-          H, (FaStrides * 2)(q3, o3), 1 if causal else 0, scale, code, workspace.data_ptr(),
-          workspace.numel())
+    r = _module().attention_forward_cache(q, cache, block_table, kv_lens, cu_q, (o, lse, workspace),
+                                          causal, scale, stream)
+    if type(r) is int:
+        raise FaError(r, "fa_fwd_cache")
 
 
 def attention_forward_cache(q, cache, block_table, kv_lens, cu_q=None, causal: bool = True,
@@ -292,24 +197,8 @@ def attention_forward_cache(q, cache, block_table, kv_lens, cu_q=None, causal: b
     """(O, LSE) of the last query tokens of each sequence over its cached keys:
     see attention_forward_cache_into for the shapes. O has q's shape and dtype;
     rows that belong to no sequence are not written."""
-    import torch
-    index, dev = _cuda_index(q, "fa_fwd_cache"), q.device
-    shape = q.shape
-    H, heads, d = shape[1], cache[0].shape[1], shape[-1]
-    if H == 0 or heads == 0 or H % heads:
-        raise ValueError(f"{H} query heads do not share {heads} K / V heads evenly")
-    if d != cache[0].shape[-1]:
-        raise ValueError(f"q has d = {d}, the cache {cache[0].shape[-1]}")
-    B, T = block_table.shape[0], math.prod(shape[:-1]) // H
-    if index == torch.cuda.current_device():
-        size = fa_fwd_cache_workspace_size(B, T, H, heads, d)
-    else:
-        with torch.cuda.device(index):
-            size = fa_fwd_cache_workspace_size(B, T, H, heads, d)
-    with _allocating_on(stream):
-        o = torch.empty(shape, dtype=q.dtype, device=dev)
-        lse = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
-        ws = torch.empty(size, dtype=torch.uint8, device=dev)
-    attention_forward_cache_into(q, cache, block_table, kv_lens, o, lse, ws, cu_q, causal, scale,
-                                 stream)
-    return o, lse
+    r = (_native or _module()).attention_forward_cache(q, cache, block_table, kv_lens, cu_q, None,
+                                                       causal, scale, stream)
+    if type(r) is int:
+        raise FaError(r, "fa_fwd_cache")
+    return r
