@@ -61,7 +61,8 @@ struct ChunkLayout {
   static constexpr int kOffScale = kOffRaw + kRaw * kRawBytes;
   static constexpr int kOffNan = kOffScale + 16 * 8 * 16;    // [8 items][D] uint64
   static constexpr int kOffStats = kOffNan + 8 * D * 8;      // [2][128] m, l of the odd tiles
-  static constexpr int kOffBar = kOffStats + 1024;
+  static constexpr int kOffShelf = kOffStats + 1024;  // [8 warps] 64 bytes
+  static constexpr int kOffBar = kOffShelf + 512;
   static constexpr int kSmem = kOffBar + 512 + 1024;  // barriers, alignment slack
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kColS = 0, kColO = 256;
@@ -442,71 +443,124 @@ __device__ __forceinline__ void chunk_mma_role(const CacheAttnArgs& a, ChunkWalk
 }
 
 // ---- softmax and epilogue: warps 4-7 (tile 0) and 8-11 (tile 1)
+
+// What a softmax warp needs between its tile loops only, kept in shared memory
+// meanwhile (16 words a warp): the loop holds 128 scores in registers.
+struct ChunkShelf {
+  ChunkWalk w;
+  uint32_t flags;  // parities: bits 0-1 items with O_i, bit 2 split items
+  int share;
+};
+static_assert(sizeof(ChunkWalk) == 56 && sizeof(ChunkShelf) == 64, "16 words");
+
+__device__ __forceinline__ void shelve(uint32_t at, const ChunkShelf& k, int lane) {
+  uint32_t u[16];
+  __builtin_memcpy(u, &k, 64);
+  if (lane == 0) {
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) ptx::st_shared_v4(at + 4u * i, u[i], u[i + 1], u[i + 2], u[i + 3]);
+  }
+  __syncwarp();
+}
+__device__ __forceinline__ ChunkShelf unshelve(uint32_t at) {
+  uint32_t u[16];
+#pragma unroll
+  for (int i = 0; i < 16; i += 4) {
+    const uint4 v = lds128(at + 4u * i);
+    u[i] = v.x;
+    u[i + 1] = v.y;
+    u[i + 2] = v.z;
+    u[i + 3] = v.w;
+  }
+  __syncwarp();
+  ChunkShelf k;
+  __builtin_memcpy(&k, u, 64);
+  return k;
+}
+
+// Query token and head of row `r` of an item.
+struct RowAt {
+  int i, head;
+};
+__device__ __forceinline__ RowAt row_at(const CacheAttnArgs& a, const ChunkWalk& w, int r) {
+  const int row = w.rb * kChunkRows + r;  // (T * H is in int range)
+  const int i = row / a.group;
+  return {i, w.hk * a.group + row - i * a.group};
+}
+
 template <int D, bool BF16>
-__device__ __forceinline__ void chunk_softmax_role(const CacheAttnArgs& a, ChunkWalk w,
-                                                   long long share, uint8_t* sgen, uint32_t sbase,
+__device__ __forceinline__ void chunk_softmax_role(const CacheAttnArgs& a, const ChunkWalk& start,
+                                                   int share, uint8_t* sgen, uint32_t sbase,
                                                    uint32_t bars, uint32_t tmem, const AbortCtx& ab,
                                                    int warp, int lane) {
   using L = ChunkLayout<D>;
+  constexpr int kLanes = D / 8, kRowsPerTurn = 32 / kLanes;  // 16 bytes of a 16-bit row each
   auto bar = [&](int i) { return bars + 8u * static_cast<uint32_t>(i); };
   const int wg = (warp >> 2) - 1;
   const int r = (warp & 3) * 32 + lane;
   const uint32_t tl = ptx::tmem_lane_base(tmem, warp);
-  const uint32_t tS = tl + L::kColS + 128u * wg;
-  const float4* const s_scale = reinterpret_cast<const float4*>(sgen + L::kOffScale);
-  const unsigned long long* const s_nan =
-      reinterpret_cast<const unsigned long long*>(sgen + L::kOffNan);
-  float* const s_m = reinterpret_cast<float*>(sgen + L::kOffStats);
-  float* const s_l = s_m + 128;
-  const bool one_scale = a.block_shift == 7;  // a tile is one block
-  uint32_t sn = 0, on[2] = {0u, 0u}, splits = 0, count = 0;  // phases, tiles before the item
-  bool ok = true;
-  do {
-    const int n = w.n();
-    const int rows = w.rows(a);
-    const bool pair = rows > 128;
-    const int rr = pair ? 128 * wg + r : r;  // row of the item
-    const bool there = rr < rows;
-    const long long row = static_cast<long long>(w.rb) * kChunkRows + (there ? rr : 0);
-    const int iq = static_cast<int>(row / a.group);
-    const int head = w.hk * a.group + static_cast<int>(row - static_cast<long long>(iq) * a.group);
-    const int lim = keys_seen(a, w.s, iq);
-    // keys that all rows of this tile see
-    const int lim0 = keys_seen(a, w.s, static_cast<int>(
-                         (static_cast<long long>(w.rb) * kChunkRows + (pair ? 128 * wg : 0)) / a.group));
-    const bool works = n > 0 && (pair || n > wg);  // this warpgroup has tiles
+  const uint32_t shelf = sbase + L::kOffShelf + static_cast<uint32_t>(warp - 4) * 64u;
+  uint32_t sn = 0, count = 0;  // S tiles taken; tiles before the item
+  shelve(shelf, ChunkShelf{start, 0u, share}, lane);
+  for (;;) {
+    // ---- an item: Q, and what its tile loop needs
+    int n, step, k0, lim, lim0;  // tiles, step, first key; keys that the row and that all rows see
+    bool idle;
     float crow = a.scale_log2;
-    float m_ref = -INFINITY, l = 0.f;
-    if (n > 0) {
-      // Q: this thread's row, widened or rescaled to fp16, in the swizzled layout
-      uint32_t q[D / 2];
-      const uint16_t* p = static_cast<const uint16_t*>(a.q) + q_offset(a, w.b, w.s, iq, head);
+    {
+      const ChunkShelf k = unshelve(shelf);
+      const ChunkWalk& w = k.w;
+      n = w.n();
+      const int rows = w.rows(a);
+      const bool pair = rows > 128;
+      const int base = pair ? 128 * wg : 0;  // the tile's first row
+      step = pair ? 1 : 2;
+      k0 = (w.t0 + (pair ? 0 : wg)) * kChunkKeys;
+      lim = keys_seen(a, w.s, row_at(a, w, base + r < rows ? base + r : 0).i);
+      lim0 = keys_seen(a, w.s, row_at(a, w, base).i);
+      // (a warp without rows hands P over as it is: its rows of O are not read)
+      idle = base + r - lane >= rows;
+      if (n > 0) {
+        // this thread's row of Q, widened or rescaled to fp16, into the swizzled
+        // layout. (A row for each thread, not 16 lanes to a row, which reads
+        // whole lines but has to loop over the rows: 2048 x 16384 chunk 387 us,
+        // drafts 70.6 us; 378 and 68.7 us so. Unrolled, its code alone took
+        // longer to fetch than the rows: 415 us.)
+        const bool there = base + r < rows;
+        const RowAt at = row_at(a, w, there ? base + r : 0);
+        const uint16_t* p = static_cast<const uint16_t*>(a.q) + q_offset(a, w.b, w.s, at.i, at.head);
+        uint32_t q[D / 2];
 #pragma unroll
-      for (int e = 0; e < D / 8; ++e) {
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (there) v = *reinterpret_cast<const uint4*>(p + 8 * e);
-        q[4 * e] = v.x;
-        q[4 * e + 1] = v.y;
-        q[4 * e + 2] = v.z;
-        q[4 * e + 3] = v.w;
-      }
-      crow *= rows_to_f16<D / 2, 1, BF16>(q);
-      if (pair || wg == 0) {
-        const uint32_t rowp = sbase + L::kOffQ + (pair ? wg : 0) * L::kTileBytes +
-                              static_cast<uint32_t>(r) * 128u;
-        const uint32_t x7 = static_cast<uint32_t>(r & 7);
+        for (int e = 0; e < D / 8; ++e) {
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (there) v = *reinterpret_cast<const uint4*>(p + 8 * e);
+          q[4 * e] = v.x;
+          q[4 * e + 1] = v.y;
+          q[4 * e + 2] = v.z;
+          q[4 * e + 3] = v.w;
+        }
+        const float fac = rows_to_f16<D / 2, 1, BF16>(q);
+        if (pair || wg == 0) {
+          const uint32_t to = sbase + L::kOffQ +
+                              static_cast<uint32_t>((pair ? wg : 0) * L::kTileBytes + r * 128);
 #pragma unroll
-        for (int e = 0; e < D / 8; ++e)
-          ptx::st_shared_v4(rowp + (e >> 3) * kPanelBytes + ((static_cast<uint32_t>(e & 7) ^ x7) << 4),
-                            q[4 * e], q[4 * e + 1], q[4 * e + 2], q[4 * e + 3]);
-        ptx::fence_proxy_async_smem();
-        ptx::mbar_arrive(bar(kCbQFull + (pair ? wg : 0)));
+          for (int e = 0; e < D / 8; ++e)
+            ptx::st_shared_v4(to + (e >> 3) * kPanelBytes + (static_cast<uint32_t>((e & 7) ^ (r & 7)) << 4),
+                              q[4 * e], q[4 * e + 1], q[4 * e + 2], q[4 * e + 3]);
+        }
+        crow *= fac;
+        if (pair || wg == 0) {
+          ptx::fence_proxy_async_smem();
+          ptx::mbar_arrive(bar(kCbQFull + (pair ? wg : 0)));
+        }
       }
     }
+    const uint32_t tS = tl + L::kColS + 128u * wg;
     const uint32_t tO = tl + L::kColO + static_cast<uint32_t>(D) * wg;
-    const int step = pair ? 1 : 2;
-    bool first = true;
-    for (int j = pair ? 0 : wg; j < n; j += step) {
+    const bool one_scale = a.block_shift == 7;  // a tile is one block
+    float m_ref = -INFINITY, l = 0.f;
+    bool first = true, ok = true;
+    for (int j = step == 1 ? 0 : wg; j < n; j += step, k0 += step * kChunkKeys) {
       const uint32_t tix = count + static_cast<uint32_t>(j);
       if (!(ok = wait_bounded_warp(bar(kCbSFull + wg), sn & 1u, ab, kStatusSoftmax) &&
                  wait_bounded_warp(bar(kCbScaleFull + (tix & 15u)), (tix >> 4) & 1u, ab,
@@ -514,6 +568,11 @@ __device__ __forceinline__ void chunk_softmax_role(const CacheAttnArgs& a, Chunk
         break;
       ++sn;
       ptx::tc_fence_after();
+      if (idle) {
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(bar(kCbPFull + wg));
+        continue;
+      }
       uint32_t sr[2][2][32];
       float mx_lo, mx_hi;
       ptx::tmem_ld64_max(tS, sr[0], mx_lo);
@@ -523,13 +582,16 @@ __device__ __forceinline__ void chunk_softmax_role(const CacheAttnArgs& a, Chunk
       float s[128];
 #pragma unroll
       for (int c = 0; c < 128; ++c) s[c] = __uint_as_float(sr[c >> 6][(c >> 5) & 1][c & 31]);
-      const float4* sc = s_scale + (tix & 15u) * 8;
-      const int k0 = (w.t0 + j) * kChunkKeys;
+      const float4* const sc = reinterpret_cast<const float4*>(sgen + L::kOffScale) + (tix & 15u) * 8;
+      auto scales = [&](int g) {  // {ks, log2 vs, 1 / vs} of a 16-key group
+        const float4 v = sc[g];
+        return make_float3(v.x * crow, v.y, v.z);
+      };
       const bool need_mask = k0 + kChunkKeys > lim0;
       float m_tile;
       if (one_scale && !need_mask) {
-        const float4 f = sc[0];
-        m_tile = fmaf(fmaxf(mx_lo, mx_hi), f.x * crow, f.y);
+        const float3 f = scales(0);
+        m_tile = fmaf(fmaxf(mx_lo, mx_hi), f.x, f.y);
       } else {
         if (need_mask) {
           const int see = lim - k0;
@@ -539,14 +601,14 @@ __device__ __forceinline__ void chunk_softmax_role(const CacheAttnArgs& a, Chunk
         m_tile = -INFINITY;
 #pragma unroll
         for (int g = 0; g < 8; ++g) {
-          const float4 f = sc[g];
+          const float3 f = scales(g);
           float t0 = fmaxf(s[16 * g], s[16 * g + 1]), t1 = fmaxf(s[16 * g + 2], s[16 * g + 3]);
 #pragma unroll
           for (int c = 4; c < 16; c += 4) {
             t0 = ptx::fmax3(t0, s[16 * g + c], s[16 * g + c + 1]);
             t1 = ptx::fmax3(t1, s[16 * g + c + 2], s[16 * g + c + 3]);
           }
-          m_tile = fmaxf(m_tile, fmaf(fmaxf(t0, t1), f.x * crow, f.y));
+          m_tile = fmaxf(m_tile, fmaf(fmaxf(t0, t1), f.x, f.y));
         }
       }
       float alpha = 1.f;
@@ -555,13 +617,13 @@ __device__ __forceinline__ void chunk_softmax_role(const CacheAttnArgs& a, Chunk
         m_ref = m_tile;
       }
       const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
-      float lsum = 0.f;
+      l *= alpha;
       uint32_t pk[2][32];
 #pragma unroll
       for (int g = 0; g < 8; ++g) {
-        const float4 f = sc[g];
-        const float fr = f.x * crow, add = f.y + neg;
-        const float2 f2 = make_float2(fr, fr), a2 = make_float2(add, add);
+        const float3 f = scales(g);
+        const float add = f.y + neg;
+        const float2 f2 = make_float2(f.x, f.x), a2 = make_float2(add, add);
         float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
@@ -572,7 +634,7 @@ __device__ __forceinline__ void chunk_softmax_role(const CacheAttnArgs& a, Chunk
           else sum0 = ptx::fadd2(sum0, make_float2(p0, p1));
         }
         sum0 = ptx::fadd2(sum0, sum1);
-        lsum = fmaf(sum0.x + sum0.y, f.z, lsum);
+        l = fmaf(sum0.x + sum0.y, f.z, l);
       }
       ptx::tmem_st32(tS, pk[0]);
       ptx::tmem_st32(tS + 32u, pk[1]);
@@ -597,42 +659,48 @@ __device__ __forceinline__ void chunk_softmax_role(const CacheAttnArgs& a, Chunk
       ptx::tmem_st_wait();
       ptx::tc_fence_before();
       ptx::mbar_arrive(bar(kCbPFull + wg));
-      l = l * alpha + lsum;
       first = false;
     }
-    if (!ok) break;
+    if (!ok) return;
 
     // ---- epilogue
+    ChunkShelf k = unshelve(shelf);
+    ChunkWalk& w = k.w;
+    const int rows = w.rows(a);
+    const bool pair = rows > 128;
+    const int base = pair ? 128 * wg : 0;
+    const bool there = base + r < rows;
+    const bool works = n > 0 && (pair || n > wg);  // this warpgroup had tiles
     const bool begins = w.t0 == 0, ends = w.t1 == w.tiles;
     float* part = nullptr;
     if (!begins || !ends)
       part = a.parts + (2LL * blockIdx.x + (begins ? 1 : 0)) * partial_floats(kChunkRows, D);
     if (!ends && begins && wg == 0 && r == 0)
       a.join[blockIdx.x] =
-          join_item(w.b, w.hk, w.rb, rows,
-                    1 + static_cast<int>((w.tiles - w.t1 + share - 1) / share));
+          join_item(w.b, w.hk, w.rb, rows, 1 + (w.tiles - w.t1 + k.share - 1) / k.share);
     const bool two = !pair && n > 1;  // results of two warpgroups
+    float* const s_m = reinterpret_cast<float*>(sgen + L::kOffStats);
     if (two && wg == 1) {
       s_m[r] = m_ref;
-      s_l[r] = l;
+      s_m[128 + r] = l;
       ptx::mbar_arrive(bar(kCbStats));
     }
     if (pair || wg == 0) {
       // the last V of the item has been converted: its NaN columns are known
       if (n > 0) {
         const uint32_t tix = count + static_cast<uint32_t>(n - 1);
-        if (!(ok = wait_bounded_warp(bar(kCbVDone + (tix & 7u)), (tix >> 3) & 1u, ab,
-                                     kStatusEpilogue)))
-          break;
+        if (!wait_bounded_warp(bar(kCbVDone + (tix & 7u)), (tix >> 3) & 1u, ab, kStatusEpilogue))
+          return;
       }
       float f0 = 1.f, f1 = 0.f;  // factors of O of this and of the other warpgroup
-      if (works && !(ok = wait_bounded_warp(bar(kCbOFull + wg), on[wg] & 1u, ab, kStatusEpilogue)))
-        break;
+      if (works &&
+          !wait_bounded_warp(bar(kCbOFull + wg), (k.flags >> wg) & 1u, ab, kStatusEpilogue))
+        return;
       if (two) {
-        if (!(ok = wait_bounded_warp(bar(kCbOFull + 1), on[1] & 1u, ab, kStatusEpilogue) &&
-                   wait_bounded_warp(bar(kCbStats), splits & 1u, ab, kStatusEpilogue)))
-          break;
-        const float m1 = s_m[r], l1 = s_l[r];
+        if (!(wait_bounded_warp(bar(kCbOFull + 1), (k.flags >> 1) & 1u, ab, kStatusEpilogue) &&
+              wait_bounded_warp(bar(kCbStats), (k.flags >> 2) & 1u, ab, kStatusEpilogue)))
+          return;
+        const float m1 = s_m[r], l1 = s_m[128 + r];
         const float top = fmaxf(m_ref, m1);
         f0 = m_ref == -INFINITY ? 0.f : ptx::ex2(m_ref - top);
         f1 = m1 == -INFINITY ? 0.f : ptx::ex2(m1 - top);
@@ -645,26 +713,30 @@ __device__ __forceinline__ void chunk_softmax_role(const CacheAttnArgs& a, Chunk
         const float inv = none ? 0.f : 1.f / l;
         f0 *= inv;
         f1 *= inv;
-        if (there)
-          a.lse[lse_index(a, w.b, w.s, iq, head)] =
+        if (there) {
+          const RowAt at = row_at(a, w, base + r);
+          a.lse[lse_index(a, w.b, w.s, at.i, at.head)] =
               none ? -INFINITY : (m_ref + log2f(l)) * 0.69314718055994531f;
+        }
       } else if (there) {
-        part[kChunkRows * D + rr] = m_ref;
-        part[kChunkRows * D + kChunkRows + rr] = l;
+        part[kChunkRows * D + base + r] = m_ref;
+        part[kChunkRows * D + kChunkRows + base + r] = l;
       }
-      uint16_t* out = static_cast<uint16_t*>(a.o) + o_offset(a, w.b, w.s, iq, head);
-      const unsigned long long* nan = s_nan + (w.item & 7) * D;
+      const uint32_t sQ = sbase + L::kOffQ + static_cast<uint32_t>((pair ? wg : 0) * L::kTileBytes);
+      const uint32_t tO0 = tl + L::kColO + static_cast<uint32_t>(D) * wg;
+      const unsigned long long* nan =
+          reinterpret_cast<const unsigned long long*>(sgen + L::kOffNan) + (w.item & 7) * D;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         float v[32];
         if (works) {
           uint32_t o[32];
-          ptx::tmem_ld32(tO + 32u * c, o);
+          ptx::tmem_ld32(tO0 + 32u * c, o);
           ptx::tmem_ld_wait(o);
 #pragma unroll
           for (int e = 0; e < 32; ++e) v[e] = none ? 0.f : __uint_as_float(o[e]) * f0;
           if (two) {
-            ptx::tmem_ld32(tO + D + 32u * c, o);
+            ptx::tmem_ld32(tO0 + D + 32u * c, o);
             ptx::tmem_ld_wait(o);
 #pragma unroll
             for (int e = 0; e < 32; ++e) v[e] = none ? 0.f : fmaf(__uint_as_float(o[e]), f1, v[e]);
@@ -676,20 +748,38 @@ __device__ __forceinline__ void chunk_softmax_role(const CacheAttnArgs& a, Chunk
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
           const unsigned long long u = nan[32 * c + e];
-          if (static_cast<int>(u >> 32) == w.item + 1 && 0x7FFFFFFF - static_cast<int>(u & 0xFFFFFFFFu) < lim)
+          if (static_cast<int>(u >> 32) == w.item + 1 &&
+              0x7FFFFFFF - static_cast<int>(u & 0xFFFFFFFFu) < lim)
             v[e] = __int_as_float(0x7FFFFFFF);
         }
-        if (there && part == nullptr) {
+        if (part == nullptr) {
+          // through the Q tile, whose products are done: the rows' chunks, swizzled
 #pragma unroll
-          for (int e = 0; e < 32; e += 8)
-            *reinterpret_cast<uint4*>(out + 32 * c + e) =
-                make_uint4(pack2<BF16>(v[e], v[e + 1]), pack2<BF16>(v[e + 2], v[e + 3]),
-                           pack2<BF16>(v[e + 4], v[e + 5]), pack2<BF16>(v[e + 6], v[e + 7]));
+          for (int e = 0; e < 32; e += 8) {
+            const uint32_t ch = static_cast<uint32_t>(4 * c + e / 8);
+            ptx::st_shared_v4(sQ + static_cast<uint32_t>(r) * 128u + (ch >> 3) * kPanelBytes +
+                                  (((ch & 7u) ^ static_cast<uint32_t>(r & 7)) << 4),
+                              pack2<BF16>(v[e], v[e + 1]), pack2<BF16>(v[e + 2], v[e + 3]),
+                              pack2<BF16>(v[e + 4], v[e + 5]), pack2<BF16>(v[e + 6], v[e + 7]));
+          }
         } else if (there) {
+          // partial results column by column: neighbouring rows are neighbours
 #pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<float4*>(part + rr * D + 32 * c + e) =
-                make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+          for (int e = 0; e < 32; ++e) part[(32 * c + e) * kChunkRows + base + r] = v[e];
+        }
+        __syncwarp();
+      }
+      if (part == nullptr) {
+        const int e = lane % kLanes, tr0 = (warp & 3) * 32 + lane / kLanes;
+        RowAt at = row_at(a, w, base + tr0);
+        int j = at.head - w.hk * a.group;
+#pragma unroll 1
+        for (int tr = tr0; tr < tr0 + 32 && base + tr < rows; tr += kRowsPerTurn) {
+          const uint4 x = lds128(sQ + (e >> 3) * kPanelBytes + static_cast<uint32_t>(tr) * 128u +
+                                 (static_cast<uint32_t>((e & 7) ^ (tr & 7)) << 4));
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) +
+                                    o_offset(a, w.b, w.s, at.i, w.hk * a.group + j) + 8 * e) = x;
+          for (j += kRowsPerTurn; j >= a.group; j -= a.group) ++at.i;
         }
         __syncwarp();
       }
@@ -697,19 +787,14 @@ __device__ __forceinline__ void chunk_softmax_role(const CacheAttnArgs& a, Chunk
       if (two) ptx::mbar_arrive(bar(kCbMerged));
     } else if (two) {
       // O1 and the stats are free for the next item only when they have been read
-      if (!(ok = wait_bounded_warp(bar(kCbMerged), splits & 1u, ab, kStatusEpilogue))) break;
+      if (!wait_bounded_warp(bar(kCbMerged), (k.flags >> 2) & 1u, ab, kStatusEpilogue)) return;
       ptx::tc_fence_after();
     }
-    if (pair && n > 0) {
-      ++on[0];
-      ++on[1];
-    } else {
-      on[0] += n > 0 ? 1u : 0u;
-      on[1] += n > 1 ? 1u : 0u;
-    }
-    splits += two ? 1u : 0u;
+    if (n > 0) k.flags ^= 1u | (pair || n > 1 ? 2u : 0u) | (two ? 4u : 0u);
     count += static_cast<uint32_t>(n);
-  } while (w.next(a));
+    if (!w.next(a)) return;
+    shelve(shelf, k, lane);
+  }
 }
 
 template <int D, bool BF16>
@@ -827,7 +912,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     else if (warp == 1) chunk_copy_role<D>(&tm_k, &tm_v, a, w, sgen, sbase, bars, ab, lane);
   } else if (wgrp < 3) {
     ptx::setmaxnreg_inc<kChunkRegsSoftmax>();
-    chunk_softmax_role<D, BF16>(a, w, share, sgen, sbase, bars, tmem, ab, warp, lane);
+    chunk_softmax_role<D, BF16>(a, w, static_cast<int>(share), sgen, sbase, bars, tmem, ab, warp,
+                                lane);
   } else {
     ptx::setmaxnreg_dec<kChunkRegsConvert>();
     chunk_convert_role<D>(a, w, sgen, sbase, bars, ab, warp, lane);

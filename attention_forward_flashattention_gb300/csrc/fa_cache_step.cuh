@@ -677,18 +677,69 @@ __global__ void __launch_bounds__(kStepThreads, 2)
 
 // Joins the partial results of the items that the shares of a step or chunk
 // launch cut: blocks (c, y) take the rows from y * kJoinRows on of the item that
-// begins in share c and ends in a later one. Warps share a row's parts when
-// there are fewer rows than warps; parts are added in a fixed order. (Blocks
-// that first found all items and shared their rows evenly were slower by the
-// time of that search, 3 us.)
+// begins in share c and ends in a later one. Parts are added in a fixed order.
+// (Blocks that first found all items and shared their rows evenly were slower
+// by the time of that search, 3 us.)
 constexpr int kJoinThreads = 256;
 constexpr int kJoinRows = 32;
+
+// The chunk kernel's partial results lie column by column ([D][max_rows], then m
+// and l): a lane takes a row, a warp D / 8 of its columns, and the joined rows
+// go out through shared memory.
+template <int D, bool BF16>
+__device__ __forceinline__ void join_columns(const CacheAttnArgs& a, const JoinItem& it,
+                                             const float* parts, int cta, int max_rows, int first,
+                                             int rows, float* s_rows, int warp, int lane) {
+  constexpr int kCols = D / (kJoinThreads / 32), kPitch = D + 4;
+  const int n = join_parts(it), size = partial_floats(max_rows, D);
+  const int r = first + lane;
+  const bool there = r < rows;
+  auto part = [&](int p) { return parts + (2LL * (cta + p) + (p == 0 ? 1 : 0)) * size + r; };
+  float m = -INFINITY, l = 0.f, o[kCols] = {};
+  if (there) {
+#pragma unroll 4
+    for (int p = 0; p < n; ++p) m = fmaxf(m, __ldcg(part(p) + max_rows * D));
+#pragma unroll 2
+    for (int p = 0; p < n; ++p) {
+      const float* q = part(p);
+      const float mp = __ldcg(q + max_rows * D);
+      const float f = mp == -INFINITY ? 0.f : ptx::ex2(mp - m);
+      l = fmaf(__ldcg(q + max_rows * D + max_rows), f, l);
+#pragma unroll
+      for (int c = 0; c < kCols; ++c)
+        o[c] = fmaf(__ldcg(q + (warp * kCols + c) * max_rows), f, o[c]);
+    }
+    const float inv = m == -INFINITY ? 0.f : 1.f / l;
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) s_rows[lane * kPitch + warp * kCols + c] = o[c] * inv;
+  }
+  __syncthreads();
+  const SeqRows s = seq_rows(a, it.b);
+  for (int e = static_cast<int>(threadIdx.x); e < kJoinRows * (D / 8); e += kJoinThreads) {
+    const int rr = e / (D / 8), c = 8 * (e % (D / 8));
+    if (first + rr >= rows) break;
+    const long long row = static_cast<long long>(it.rb) * max_rows + first + rr;
+    const int i = static_cast<int>(row / a.group);
+    const int h = it.hk * a.group + static_cast<int>(row - static_cast<long long>(i) * a.group);
+    const float* v = s_rows + rr * kPitch + c;
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + o_offset(a, it.b, s, i, h) + c) =
+        make_uint4(pack2<BF16>(v[0], v[1]), pack2<BF16>(v[2], v[3]), pack2<BF16>(v[4], v[5]),
+                   pack2<BF16>(v[6], v[7]));
+  }
+  if (warp == 0 && there) {
+    const long long row = static_cast<long long>(it.rb) * max_rows + r;
+    const int i = static_cast<int>(row / a.group);
+    const int h = it.hk * a.group + static_cast<int>(row - static_cast<long long>(i) * a.group);
+    a.lse[lse_index(a, it.b, s, i, h)] =
+        m == -INFINITY ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+  }
+}
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kJoinThreads, 2)
     fa_cache_join_kernel(const CacheAttnArgs a, const JoinSides sides) {
   constexpr int kWarps = kJoinThreads / 32, kPer = D / 32;
-  __shared__ float s_o[kWarps][D];
+  __shared__ float s_rows[kJoinRows * (D + 4)];
   __shared__ float s_l[kWarps];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const bool second = static_cast<int>(blockIdx.x) >= sides.ctas[0];
@@ -702,6 +753,13 @@ __global__ void __launch_bounds__(kJoinThreads, 2)
   const float* parts = second ? sides.parts[1] : sides.parts[0];
   const int size = partial_floats(max_rows, D);
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
+  if (second) {
+    join_columns<D, BF16>(a, it, parts, cta, max_rows, first, rows, s_rows, warp, lane);
+    return;
+  }
+  // the step kernel's lie row by row; warps share a row's parts when there are
+  // fewer rows than warps
+  float (*const s_o)[D] = reinterpret_cast<float(*)[D]>(s_rows);
   int per_row = 1;  // warps for a row: a power of two
   while (per_row * 2 * (rows - first) <= kWarps) per_row *= 2;
   auto part = [&](int p) { return parts + (2LL * (cta + p) + (p == 0 ? 1 : 0)) * size; };
