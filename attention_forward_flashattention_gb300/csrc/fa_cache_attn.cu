@@ -35,7 +35,7 @@ AttnPlan plan_attn(int B, int T, int group, bool ragged) {
   return p;
 }
 
-int step_grid(const AttnPlan& p, int sm_count) { return p.nt == 0 ? 0 : 2 * sm_count; }
+int step_grid(const AttnPlan& p, int sm_count) { return p.nt == 0 ? 0 : step_ctas(p.nt) * sm_count; }
 
 // Workspace: the join items of both launches, then their partial results.
 long long plan_floats(const AttnPlan& p, int d, int sm_count) {
@@ -63,7 +63,7 @@ cudaError_t launch_early(void (*kern)(Params...), dim3 grid, int threads, int sm
 template <int D, bool BF16, int NT>
 cudaError_t launch_step(const CacheAttnArgs& a, const CUtensorMap* maps, bool whole, int grid,
                         cudaStream_t stream) {
-  constexpr int kSmem = StepLayout<D>::kSmem;
+  constexpr int kSmem = StepLayout<D, NT>::kSmem;
   auto kern = fa_cache_step_kernel<D, BF16, NT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;

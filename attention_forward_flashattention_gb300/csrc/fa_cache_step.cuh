@@ -26,7 +26,7 @@
 // m moves (and O, l are rescaled) only when an e_j exceeds it by more than 8.
 //
 // Splitting: the items' tiles form one list, cut into equal shares for the
-// persistent CTAs (two on each SM). A share that begins or ends inside an item
+// persistent CTAs (two or three on each SM). A share that begins or ends inside an item
 // writes a partial result (O, m, l), which fa_cache_join_kernel joins in order.
 #pragma once
 
@@ -41,7 +41,14 @@ namespace fa {
 
 constexpr int kStepWarps = 4;
 constexpr int kStepThreads = 32 * kStepWarps;
-constexpr int kStepStages = 3;
+// CTAs on an SM and stages of a ring, by the rows of an item. What bounds the
+// kernel is the latency of its instructions (a warp issues one in 5 cycles and
+// hardly ever waits for a copy), so 8 rows, which leave room for three CTAs'
+// registers, run on 12 warps with two stages each. Against 8 warps with three
+// stages: B128 H16 1000 keys, d 64, 60 us (76), B4 H16 4096 keys 21.3 (22.1),
+// ragged B96 236 (240), but B2 131071 keys 95 (92).
+__host__ __device__ constexpr int step_ctas(int nt) { return nt == 1 ? 3 : 2; }
+__host__ __device__ constexpr int step_stages(int nt) { return nt == 1 ? 2 : 3; }
 constexpr int kStepTileBytes = 4096;  // of K, and of V
 constexpr int kStepMaxRows = 16;      // rows of an item: 8 NT, NT = 1 or 2
 
@@ -183,36 +190,40 @@ __device__ __forceinline__ float rows_to_f16(uint32_t (&w)[N]) {
 }
 
 // Shared memory (all of it dynamic: a static array would be padded to the
-// ring's alignment). It must fit twice into an SM.
-template <int D>
+// ring's alignment).
+template <int D, int NT>
 struct StepLayout {
+  static constexpr int kStages = step_stages(NT);
   static constexpr int kBoxes = step_keys(D) / 16;  // blocks of a tile, at most
-  static constexpr int kRing = kStepWarps * kStepStages * 2 * kStepTileBytes;
-  static constexpr int kOffMerge = kRing;  // merged rows: [warp][8][D] floats
-  static constexpr int kOffStats = kOffMerge + kStepWarps * 8 * D * 4;  // m, l: [2][warp][8]
+  static constexpr int kRing = kStepWarps * kStages * 2 * kStepTileBytes;
+  static constexpr int kOffMerge = kRing;  // merged rows: [warp][8][64] floats
+  static constexpr int kOffStats = kOffMerge + kStepWarps * 8 * 64 * 4;  // m, l: [2][warp][8]
   static constexpr int kOffBar = kOffStats + 2 * kStepWarps * 8 * 4;
-  static constexpr int kOffIdx = kOffBar + kStepWarps * kStepStages * 8;  // [warp][stage][box]
-  static constexpr int kOffNan = kOffIdx + kStepWarps * kStepStages * kBoxes * 4;  // [D]
+  static constexpr int kOffIdx = kOffBar + kStepWarps * kStages * 8;  // [warp][stage][box]
+  static constexpr int kOffNan = kOffIdx + kStepWarps * kStages * kBoxes * 4;  // [D]
   static constexpr int kOffWords = kOffNan + D * 4;
   static constexpr int kSmem = kOffWords + 8;
   // 228 KB on an SM, 1 KB of it reserved for each CTA
-  static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs on an SM");
+  static_assert(step_ctas(NT) * (kSmem + 1024) <= 228 * 1024, "CTAs on an SM");
 };
 
-// Place (in pairs of floats) of columns D / 8 g + 2 i and + 1 in merged row r:
-// the exclusive ors spread the 16 lanes of a store over all banks.
+// Results are merged 64 columns at a time. Place (in pairs of floats) in merged
+// row r of the columns of part h that lane group g holds in O^T tile i of its
+// kI ones: the exclusive ors spread the 16 lanes of a store over all banks.
 template <int D>
 __device__ __forceinline__ int merge_pair(int r, int g, int i) {
-  return (D / 16 * g + (i ^ ((g >> 1) & (D / 32 - 1)))) ^ (r & 6);
+  constexpr int kI = 4;  // tiles of O^T in 64 columns of each lane group's share
+  return (kI * g + (i ^ ((g >> 1) & (kI / 2 - 1)))) ^ (r & 6);
 }
 
 // D: head dimension; BF16: type of q and o; NT: 8-row groups of an item.
 template <int D, bool BF16, int NT>
-__global__ void __launch_bounds__(kStepThreads, 2)
+__global__ void __launch_bounds__(kStepThreads, step_ctas(NT))
     fa_cache_step_kernel(const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_v, const CacheAttnArgs a,
                          const int whole_items) {
-  using L = StepLayout<D>;
+  using L = StepLayout<D, NT>;
+  constexpr int kStages = L::kStages;
   constexpr int KT = step_keys(D);
   constexpr int kSub = KT / 16;      // 16-key groups of a tile
   constexpr int kMt = D / 16;        // 16-row tiles of O^T
@@ -224,9 +235,9 @@ __global__ void __launch_bounds__(kStepThreads, 2)
   const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
   const uint32_t base = ptx::smem_u32(smem);
-  const uint32_t ring = base + static_cast<uint32_t>(warp * kStepStages * 2 * kStepTileBytes);
-  const uint32_t bars = base + L::kOffBar + static_cast<uint32_t>(warp * kStepStages * 8);
-  int* const s_idx = reinterpret_cast<int*>(smem + L::kOffIdx) + warp * kStepStages * L::kBoxes;
+  const uint32_t ring = base + static_cast<uint32_t>(warp * kStages * 2 * kStepTileBytes);
+  const uint32_t bars = base + L::kOffBar + static_cast<uint32_t>(warp * kStages * 8);
+  int* const s_idx = reinterpret_cast<int*>(smem + L::kOffIdx) + warp * kStages * L::kBoxes;
   float* const s_merge = reinterpret_cast<float*>(smem + L::kOffMerge);
   float* const s_m = reinterpret_cast<float*>(smem + L::kOffStats);
   float* const s_l = s_m + kStepWarps * 8;
@@ -240,7 +251,7 @@ __global__ void __launch_bounds__(kStepThreads, 2)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (lane == 0) {
-    for (int i = 0; i < kStepStages; ++i) ptx::mbar_init(bars + 8u * i, 1);
+    for (int i = 0; i < kStages; ++i) ptx::mbar_init(bars + 8u * i, 1);
     ptx::fence_mbar_init();
     if (warp == 0) {
       ptx::prefetch_tmap(&tm_k);
@@ -336,7 +347,7 @@ __global__ void __launch_bounds__(kStepThreads, 2)
     }
   };
   uint32_t fired = 0, used = 0;  // tiles copied into and taken from the ring
-  for (int i = 0; i < kStepStages; ++i) {
+  for (int i = 0; i < kStages; ++i) {
     prepare();
     if (!more) break;
     fire(i);
@@ -348,7 +359,7 @@ __global__ void __launch_bounds__(kStepThreads, 2)
   float scale_next = 1.f;
   int idx_next = -1;
   auto load_scales = [&](uint32_t n) {
-    idx_next = s_idx[(n % kStepStages) * L::kBoxes + (t & (L::kBoxes - 1))];
+    idx_next = s_idx[(n % kStages) * L::kBoxes + (t & (L::kBoxes - 1))];
     scale_next = 1.f;
     if (lane < 8 && idx_next >= 0) scale_next = __ldg((lane < 4 ? a.ks : a.vs) + idx_next);
   };
@@ -405,13 +416,13 @@ __global__ void __launch_bounds__(kStepThreads, 2)
 
     const int last = now.last(whole);
     for (int tile = now.first(whole) + warp; tile < last; tile += kStepWarps) {
-      const int slot = static_cast<int>(used % kStepStages);
+      const int slot = static_cast<int>(used % kStages);
       const float sc = scale_next;
       const int idx = idx_next;
       prepare();
       const bool refill = more && alive;
       if (used + 1 < fired) load_scales(used + 1);
-      if (alive) alive = wait_bounded_warp(bars + 8u * slot, (used / kStepStages) & 1u, ab,
+      if (alive) alive = wait_bounded_warp(bars + 8u * slot, (used / kStages) & 1u, ab,
                                            kStatusSoftmax);
       const uint32_t sk = ring + static_cast<uint32_t>(slot * 2 * kStepTileBytes);
       const uint32_t sv = sk + kStepTileBytes;
@@ -608,58 +619,65 @@ __global__ void __launch_bounds__(kStepThreads, 2)
           s_m[warp * 8 + 2 * t + h] = m[nt][h];
           s_l[warp * 8 + 2 * t + h] = v;
         }
-        float2* row = reinterpret_cast<float2*>(s_merge + (warp * 8 + 2 * t + h) * D);
-#pragma unroll
-        for (int i = 0; i < kMt; ++i)
-          row[merge_pair<D>(2 * t + h, g, i)] = make_float2(o[nt][i][h], o[nt][i][2 + h]);
       }
-      __syncthreads();
-      any_nan = *s_any_nan != 0;  // (no warp is at another item's tiles here)
-      constexpr int kPairs = D / 2;
-      for (int e = tid; e < 8 * kPairs; e += kStepThreads) {
-        const int r = e / kPairs, c = 2 * (e % kPairs);
-        const int rr = 8 * nt + r;  // row of the item
-        if (rr >= rows) break;
-        float top = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kStepWarps; ++w) top = fmaxf(top, s_m[w * 8 + r]);
-        const int pair = merge_pair<D>(r, c / (D / 8), (c % (D / 8)) / 2);
-        float sum = 0.f;
-        float2 acc = make_float2(0.f, 0.f);
+      for (int half = 0; half < D / 64; ++half) {  // tiles 4 half .. 4 half + 3 of O^T
 #pragma unroll
-        for (int w = 0; w < kStepWarps; ++w) {
-          const float mw = s_m[w * 8 + r];
-          const float f = mw == -INFINITY ? 0.f : ptx::ex2(mw - top);
-          const float2 v = reinterpret_cast<const float2*>(s_merge + (w * 8 + r) * D)[pair];
-          sum = fmaf(s_l[w * 8 + r], f, sum);
-          acc.x = fmaf(v.x, f, acc.x);
-          acc.y = fmaf(v.y, f, acc.y);
+        for (int h = 0; h < 2; ++h) {
+          float2* row = reinterpret_cast<float2*>(s_merge + (warp * 8 + 2 * t + h) * 64);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            row[merge_pair<D>(2 * t + h, g, i)] =
+                make_float2(o[nt][4 * half + i][h], o[nt][4 * half + i][2 + h]);
         }
-        const int i_q = (row0 + rr) / a.group, j_q = (row0 + rr) - i_q * a.group;
-        if (any_nan) {
-          const int sees = a.causal ? min(behind + i_q + 1, now.s.kv_len) : now.s.kv_len;
-          if (s_nan[c] < sees) acc.x = __int_as_float(0x7FFFFFFF);
-          if (s_nan[c + 1] < sees) acc.y = __int_as_float(0x7FFFFFFF);
-        }
-        if (part != nullptr) {
-          *reinterpret_cast<float2*>(part + rr * D + c) = acc;
-          if (c == 0) {
-            part[kRows * D + rr] = top;
-            part[kRows * D + kRows + rr] = sum;
+        __syncthreads();
+        any_nan = *s_any_nan != 0;  // (no warp is at another item's tiles here)
+        for (int e = tid; e < 8 * 32; e += kStepThreads) {
+          const int r = e >> 5, gg = (e >> 2) & 7, i = e & 3;
+          const int c = D / 8 * gg + 2 * (4 * half + i);  // columns c and c + 1
+          const int rr = 8 * nt + r;                      // row of the item
+          if (rr >= rows) break;
+          float top = -INFINITY;
+#pragma unroll
+          for (int w = 0; w < kStepWarps; ++w) top = fmaxf(top, s_m[w * 8 + r]);
+          const int pair = merge_pair<D>(r, gg, i);
+          float sum = 0.f;
+          float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int w = 0; w < kStepWarps; ++w) {
+            const float mw = s_m[w * 8 + r];
+            const float f = mw == -INFINITY ? 0.f : ptx::ex2(mw - top);
+            const float2 v = reinterpret_cast<const float2*>(s_merge + (w * 8 + r) * 64)[pair];
+            sum = fmaf(s_l[w * 8 + r], f, sum);
+            acc.x = fmaf(v.x, f, acc.x);
+            acc.y = fmaf(v.y, f, acc.y);
           }
-        } else {
-          const bool none = top == -INFINITY;
-          const float inv = none ? 0.f : 1.f / sum;
-          const int h = now.hk * a.group + j_q;
-          *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) +
-                                       o_offset(a, now.b, now.s, i_q, h) + c) =
-              pack2<BF16>(acc.x * inv, acc.y * inv);
-          if (c == 0)
-            a.lse[lse_index(a, now.b, now.s, i_q, h)] =
-                none ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+          const int i_q = (row0 + rr) / a.group, j_q = (row0 + rr) - i_q * a.group;
+          if (any_nan) {
+            const int sees = a.causal ? min(behind + i_q + 1, now.s.kv_len) : now.s.kv_len;
+            if (s_nan[c] < sees) acc.x = __int_as_float(0x7FFFFFFF);
+            if (s_nan[c + 1] < sees) acc.y = __int_as_float(0x7FFFFFFF);
+          }
+          if (part != nullptr) {
+            *reinterpret_cast<float2*>(part + rr * D + c) = acc;
+            if (c == 0) {
+              part[kRows * D + rr] = top;
+              part[kRows * D + kRows + rr] = sum;
+            }
+          } else {
+            const bool none = top == -INFINITY;
+            const float inv = none ? 0.f : 1.f / sum;
+            const int h = now.hk * a.group + j_q;
+            *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) +
+                                         o_offset(a, now.b, now.s, i_q, h) + c) =
+                pack2<BF16>(acc.x * inv, acc.y * inv);
+            if (c == 0)
+              a.lse[lse_index(a, now.b, now.s, i_q, h)] =
+                  none ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+          }
         }
+        __syncthreads();
       }
-      __syncthreads();
     }
     if (any_nan) {
       for (int c = tid; c < D; c += kStepThreads) s_nan[c] = 0x7FFFFFFF;
@@ -669,10 +687,11 @@ __global__ void __launch_bounds__(kStepThreads, 2)
     }
     if (!now.next(a, kRows, whole)) break;
   }
-  // (every copy has been waited for, unless a wait gave up)
+  // (every copy has been waited for, unless a wait gave up: then those in
+  // flight land before the CTA ends, as far as they do)
   if (!alive)
-    for (uint32_t n = used > kStepStages ? used - kStepStages : 0; n < fired; ++n)
-      wait_drain(bars + 8u * (n % kStepStages), (n / kStepStages) & 1u, ab, kStatusDrain);
+    for (uint32_t n = used > kStages ? used - kStages : 0; n < fired; ++n)
+      wait_drain(bars + 8u * (n % kStages), (n / kStages) & 1u, ab, kStatusDrain);
 }
 
 // Joins the partial results of the items that the shares of a step or chunk
