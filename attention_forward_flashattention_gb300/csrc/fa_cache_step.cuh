@@ -164,6 +164,12 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
 // Two fp32 values as fp16, lo in the low half.
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) { return pack2<false>(lo, hi); }
 
+__device__ __forceinline__ float2 unpack_f16(uint32_t w) {
+  __half2 h;
+  __builtin_memcpy(&h, &w, 4);
+  return __half22float2(h);
+}
+
 // N packed pairs of a query row, as fp16 values of `fac` (returned), a power of
 // two that brings the row into fp16's range (bf16 queries; 1 for fp16): the
 // conversion loses nothing that fp32 sums of the products would keep. kShare:
@@ -519,7 +525,9 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas(NT))
       }
 
       // P' and the sums; P'^T as B fragments
-      uint32_t p[kSub][NT][2];
+      // (for fp16 queries in two parts: a weight's rounding to 11 bits would add
+      // as much to the error as the rounding of O itself; bf16's O hides it)
+      uint32_t p[kSub][NT][2], p_low[BF16 ? 1 : kSub][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const float n0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
@@ -530,8 +538,14 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas(NT))
           const float p2 = ptx::ex2(s[u][nt][2] - n0), p3 = ptx::ex2(s[u][nt][3] - n1);
           l[nt][0] = fmaf(p0 + p2, iv[u], l[nt][0]);
           l[nt][1] = fmaf(p1 + p3, iv[u], l[nt][1]);
-          p[u][nt][0] = transpose_8x8(pack_f16(p0, p1));
-          p[u][nt][1] = transpose_8x8(pack_f16(p2, p3));
+          const uint32_t h0 = pack_f16(p0, p1), h1 = pack_f16(p2, p3);
+          p[u][nt][0] = transpose_8x8(h0);
+          p[u][nt][1] = transpose_8x8(h1);
+          if constexpr (!BF16) {
+            const float2 b0 = unpack_f16(h0), b1 = unpack_f16(h1);
+            p_low[u][nt][0] = transpose_8x8(pack_f16(p0 - b0.x, p1 - b0.y));
+            p_low[u][nt][1] = transpose_8x8(pack_f16(p2 - b1.x, p3 - b1.y));
+          }
         }
       }
 
@@ -588,7 +602,11 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas(NT))
           const uint32_t y = __byte_perm(v[2][i / 2], v[3][i / 2], sel);
           const uint32_t a0 = widen_lo(x), a1 = widen_hi(x), a2 = widen_lo(y), a3 = widen_hi(y);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma_16816(o[nt][i], a0, a1, a2, a3, p[u][nt][0], p[u][nt][1]);
+          for (int nt = 0; nt < NT; ++nt) {
+            mma_16816(o[nt][i], a0, a1, a2, a3, p[u][nt][0], p[u][nt][1]);
+            if constexpr (!BF16)
+              mma_16816(o[nt][i], a0, a1, a2, a3, p_low[u][nt][0], p_low[u][nt][1]);
+          }
         }
       }
       __syncwarp();  // the slot is read by every lane

@@ -38,7 +38,7 @@ typedef struct fa_cache {
   void* v;
   float* k_scales;        /* [num_blocks][Hkv], contiguous; finite and > 0 where read */
   float* v_scales;
-  int num_blocks;         /* >= 1, num_blocks * block <= 2^31 - 1 */
+  int num_blocks;         /* >= 1, times block and times Hkv at most 2^31 - 1 */
   int block;              /* tokens in a block: 16, 32, 64 or 128 */
   int Hkv;                /* K / V heads */
   int d;                  /* head dimension, 64 or 128 */
@@ -103,7 +103,8 @@ fa_status fa_cache_plan(const int32_t* lens, const int32_t* new_lens, int32_t* b
  * new tokens, the scale becomes the smallest power of two s >= 2^-40 with
  * amax <= 448 s, or the block's present scale (rounded up to a power of two)
  * if that is larger and the block holds older tokens; a block whose row 0 is
- * among the new tokens starts afresh. Codes are value / s rounded to nearest
+ * among the new tokens starts afresh. (A present scale that is not above 0 is
+ * taken as none.) Codes are value / s rounded to nearest
  * even; if s grew, the codes of the block's older rows (those before the first
  * new one) are brought to it, code * old / s, rounded again. With powers of
  * two that is exact, and loses bits only where a code becomes subnormal.
@@ -137,7 +138,8 @@ fa_status fa_cache_append(const void* k, const void* v, const fa_strides* stride
  *               their keys: they weigh nothing.
  * kv_lens     : [B] int32; taken as within 0 .. table_width * block.
  * B, T, H     : sequences, query rows, query heads (a multiple of Hkv), >= 1
- *               (T >= 0; 0: nothing is enqueued). T * H <= 2^31 - 1.
+ *               (T >= 0; 0: nothing is enqueued). B <= 2^20, T * H <= 2^31 - 1,
+ *               table_width * block <= 2^30.
  * Rows of o and lse that belong to no sequence are left as they are. Keys at
  * and behind kv_lens[b], and those that the causal rule hides, do not reach a
  * row, whatever their codes: NaN neither.
@@ -146,8 +148,12 @@ fa_status fa_cache_append(const void* k, const void* v, const fa_strides* stride
  *               the same time. Nothing is kept in it between calls.
  * Scores, softmax sums and O are formed in fp32 from the exact products of
  * 16-bit queries and 8-bit codes; the weights are rounded to fp16 (relative
- * 2^-11 at most) for the product with V, whatever `dtype` is. V scales of one
- * sequence may differ by a factor of up to 2^100.
+ * 2^-11 at most) for the product with V, whatever `dtype` is, but kept in two
+ * such parts for FA_DTYPE_FP16 and up to 16 rows to a K / V head. V scales of
+ * one sequence may differ by a factor of up to 2^100.
+ * Up to three launches (a kernel for sequences of up to 16 rows to a K / V
+ * head, one for more, and one that joins what they split), by the sizes that
+ * the host knows. Deterministic: the same call gives the same bits.
  */
 fa_status fa_fwd_cache(const void* q, const fa_cache* cache, const int32_t* block_table,
                        int table_width, const int32_t* kv_lens, const int32_t* cu_q, void* o,

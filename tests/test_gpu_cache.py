@@ -632,6 +632,114 @@ def test_graph_replays_a_step(n, H, heads, d):
     assert fa.fa_check(0) == fa.FA_OK
 
 
+def test_workspace_and_empty_calls():
+    """A workspace that is too small is refused; calls of nothing succeed."""
+    import torch
+    rng = np.random.default_rng(20)
+    cache = make_cache(4, 2, 16, 64, "head", rng)
+    tab, lens = ints(np.arange(4).reshape(2, 2)), ints([20, 30])
+    q = torch.randn(2, 4, 64, device=DEV).half()
+    o, lse = torch.full_like(q, 7.0), torch.full((2, 4), 7.0, device=DEV)
+    size = fa.fa_fwd_cache_workspace_size(2, 2, 4, 2, 64)
+    with pytest.raises(fa.FaError) as e:
+        fa.attention_forward_cache_into(q, cache, tab, lens, o, lse,
+                                        torch.empty(size - 16, dtype=torch.uint8, device=DEV))
+    assert e.value.status == fa.FA_ERR_INVALID_ARG
+    torch.cuda.synchronize()
+    assert (o == 7).all() and (lse == 7).all()
+    fa.attention_forward_cache_into(q, cache, tab, lens, o, lse,
+                                    torch.empty(size, dtype=torch.uint8, device=DEV))
+    assert not (o == 7).all()
+    desc = fa.FaCache(cache.k.data_ptr(), cache.v.data_ptr(), cache.k_scales.data_ptr(),
+                      cache.v_scales.data_ptr(), 4, 16, 2, 64, 2 * 16 * 64, 16 * 64, 64)
+    st = ((8, 64, 128), (8, 64, 128))
+    assert fa.fa_cache_append(q.data_ptr(), q.data_ptr(), st, lens.data_ptr(), 0, desc,
+                              fa.FA_DTYPE_FP16) == fa.FA_OK
+    assert fa.fa_fwd_cache(q.data_ptr(), desc, tab.data_ptr(), 2, lens.data_ptr(), None,
+                           o.data_ptr(), lse.data_ptr(), 2, 0, 4, st, True, 0.1, fa.FA_DTYPE_FP16,
+                           o.data_ptr(), 0) in (fa.FA_OK, fa.FA_ERR_INVALID_ARG)
+    slots, cu, kv, nxt = fa.cache_plan(ints([3]), ints([0]), ints([[1]]), ints([]), ints([0]), 0, 16)
+    assert slots.numel() == 0 and cu.tolist() == [0, 0] and kv.tolist() == [3] and nxt.tolist() == [0]
+
+
+def test_concurrent_calls_on_streams():
+    """Step, chunk and mixed calls at once on their own streams give the bits
+    that they give one after another."""
+    import torch
+    rng = np.random.default_rng(21)
+    cache = make_cache(400, 2, 32, 128, "head", rng)
+    tab = ints(rng.permutation(400).reshape(4, 100))
+    lens = ints([3200, 1500, 33, 2999])
+    qs = [torch.randn(n, 8, 128, device=DEV).bfloat16() for n in (4, 160, 4 + 70)]
+    cus = [None, ints([0, 40, 80, 120, 160]), ints([0, 1, 2, 3, 74])]
+    calls = [lambda s, q=q, c=c: fa.attention_forward_cache(q, cache, tab, lens, c, stream=s)
+             for q, c in zip(qs, cus)]
+    ref = []
+    for c in calls:
+        ref.append([t.clone() for t in c(None)])
+        torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(6)]
+    main = torch.cuda.current_stream()
+    for s in streams:
+        s.wait_stream(main)
+    got = [(i % 3, calls[i % 3](s)) for _ in range(3) for i, s in enumerate(streams)]
+    torch.cuda.synchronize()
+    for i, out in got:
+        assert all(torch.equal(a, b) for a, b in zip(out, ref[i]))
+    assert fa.fa_check(0) == fa.FA_OK
+
+
+def test_calls_from_threads():
+    """First and later calls from several host threads, each on its own stream."""
+    import threading
+
+    import torch
+    rng = np.random.default_rng(22)
+    cache = make_cache(60, 2, 16, 64, "head", rng)
+    tab, lens = ints(np.arange(60).reshape(3, 20)), ints([300, 17, 120])
+    q = torch.randn(3, 6, 64, device=DEV).half()
+    ref = fa.attention_forward_cache(q, cache, tab, lens)
+    torch.cuda.synchronize()
+    out = [None] * 4
+
+    def work(i):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(20):
+                r = fa.attention_forward_cache(q, cache, tab, lens, stream=s)
+            s.synchronize()
+        out[i] = r
+    ts = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    assert all(torch.equal(a, b) for r in out for a, b in zip(r, ref))
+
+
+def test_outputs_and_queries_in_other_layouts():
+    """q and o as views into wider rows (a fused projection), head-major and
+    token-major."""
+    import torch
+    rng = np.random.default_rng(23)
+    cache = make_cache(40, 2, 16, 128, "pair", rng)
+    tab, lens = ints(np.arange(40).reshape(2, 20)), ints([310, 290])
+    for n in (1, 6, 40):
+        wide = torch.randn(2 * n, 3, 4, 128, device=DEV).bfloat16()
+        q = wide[:, 1]
+        cu = ints([0, n, 2 * n])
+        ref = fa.attention_forward_cache(q.contiguous(), cache, tab, lens, cu)
+        got = fa.attention_forward_cache(q, cache, tab, lens, cu)
+        assert all(torch.equal(a, b) for a, b in zip(got, ref))
+        store = torch.zeros(2 * n, 4, 2, 128, device=DEV).bfloat16()
+        o, lse = store[:, :, 0], torch.empty(2 * n, 4, device=DEV)
+        ws = torch.empty(fa.fa_fwd_cache_workspace_size(2, 2 * n, 4, 2, 128), dtype=torch.uint8,
+                         device=DEV)
+        fa.attention_forward_cache_into(q, cache, tab, lens, o, lse, ws, cu)
+        assert torch.equal(o, ref[0]) and torch.equal(lse, ref[1])
+        assert (store[:, :, 1] == 0).all()
+
+
 def test_binding_refusals():
     import torch
     c = fa.cache_empty(4, 2, 16, 64, device=DEV)
