@@ -323,16 +323,23 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas(NT))
   int at_tile = ahead.first(whole) + warp;
   bool more = true;
   int id = -1, fire_tile = 0, fire_hk = 0;
+  const int32_t* table = nullptr;  // of the item that is copied, and its blocks that hold keys
+  int held = 0;
+  auto enter = [&] {
+    table = a.table + static_cast<long long>(ahead.b) * a.table_width;
+    held = (ahead.s.kv_len + (1 << a.block_shift) - 1) >> a.block_shift;
+  };
+  enter();
   auto prepare = [&] {
     while (more && at_tile >= ahead.last(whole)) {
       more = ahead.next(a, kRows, whole);
       at_tile = ahead.first(whole) + warp;
+      enter();
     }
     if (!more) return;
     id = -1;
     const int bi = ((at_tile * KT) >> a.block_shift) + lane;
-    if (lane < boxes && (static_cast<long long>(bi) << a.block_shift) < ahead.s.kv_len)
-      id = __ldg(a.table + static_cast<long long>(ahead.b) * a.table_width + bi);
+    if (lane < boxes && bi < held) id = __ldg(table + bi);
     fire_tile = at_tile;
     fire_hk = ahead.hk;
     at_tile += kStepWarps;
@@ -435,7 +442,7 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas(NT))
       const int key0 = tile * KT;
       const uint32_t hidden = __ballot_sync(0xffffffffu, lane < boxes && idx < 0);
       const bool edge = key0 + KT > all_see || hidden != 0u;
-      const float lv_all = log2f(sc), iv_all = 1.f / sc;  // (lanes 4 - 7: of the V scales)
+      const float lv_all = ptx::lg2(sc), iv_all = ptx::rcp(sc);  // (lanes 4 - 7: of the V scales)
 
       // S^T = K Q^T for the tile's keys
       float s[kSub][NT][4];
