@@ -82,6 +82,7 @@ struct CacheAttnArgs {
   // sequences of more than rows_over and at most rows_upto rows to a K / V head
   // are this launch's; the others are left alone
   int rows_over, rows_upto;
+  int item_rows;   // of a work item of the chunk kernel: 128 or 256
   JoinItem* join;  // [CTAs of the launch]
   float* parts;    // [CTAs of the launch][2] partial results
 };

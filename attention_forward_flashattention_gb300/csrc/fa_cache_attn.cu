@@ -6,6 +6,11 @@
 namespace fa {
 namespace {
 
+// e4m3 tiles that hold a query tile in the chunk kernel for items of up to 128
+// rows (0: there is none; at d = 64 a row is half a swizzled panel): two parts
+// are exact for bf16's 8-bit significands, three for fp16's 11 bits.
+constexpr int chunk_parts(int d, bool bf16) { return d == 64 ? 0 : bf16 ? 2 : 3; }
+
 // Kernels of a call. The lengths are device memory, so the choice goes by the
 // sizes that the host knows. Both kernels compute any number of rows; they
 // differ in how many go through the cache together.
@@ -13,13 +18,16 @@ struct AttnPlan {
   int nt = 0;          // 8-row groups of the step kernel's instance; 0: not launched
   bool chunk = false;  // the chunk kernel
   int upto = INT_MAX;  // with both: most rows of the step kernel's sequences
+  int item_rows = kChunkRows;  // most rows of the chunk kernel's items: 256 or 128
 };
 
 AttnPlan plan_attn(int B, int T, int group, bool ragged) {
   AttnPlan p;
   const long long most = static_cast<long long>(T) * group;  // rows of a sequence to a K / V head
   if (!ragged || B == 1 || T <= B || most <= kStepMaxRows) {
-    // sequences of one size, of a token each (as a rule), or small in any case
+    // sequences of one size, of a token each (as a rule), or small in any case. Up to
+    // 16 rows the step kernel: 16 sequences, 4 K / V heads, 8192 keys take 46 us with
+    // 16 rows there; the chunk kernel takes 58 to 66 us for any number from 17 to 64.
     const long long rows = !ragged ? most / B : (T <= B && B > 1 ? group : most);
     p.nt = rows <= 8 ? 1 : (rows <= kStepMaxRows ? 2 : 0);
     p.chunk = p.nt == 0;
@@ -71,6 +79,25 @@ cudaError_t launch_step(const CacheAttnArgs& a, const CUtensorMap* maps, bool wh
   return cudaGetLastError();
 }
 
+template <int D, bool BF16, int PARTS>
+cudaError_t launch_chunk(const CacheAttnArgs& a, const fa_cache& c, const AttnPlan& p, int grid,
+                         cudaStream_t stream, bool* mapped) {
+  constexpr int kSmem = ChunkLayout<D, PARTS>::kSmem;
+  auto kern = fa_cache_chunk_kernel<D, BF16, PARTS>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  CUtensorMap maps[2];
+  *mapped = encode_cache(&maps[0], c.k, c, c.block, PARTS > 0) &&
+            encode_cache(&maps[1], c.v, c, c.block, false);
+  if (!*mapped) return cudaErrorUnknown;
+  // after a step launch it takes the SMs that are done with that one (its
+  // CTAs wait for the step launch before they end)
+  if (p.nt != 0)
+    return launch_early(kern, dim3(grid), kChunkThreads, kSmem, stream, maps[0], maps[1], a);
+  kern<<<grid, kChunkThreads, kSmem, stream>>>(maps[0], maps[1], a);
+  return cudaGetLastError();
+}
+
 template <int D, bool BF16>
 cudaError_t launch_all(CacheAttnArgs a, const fa_cache& c, const AttnPlan& p, int sm_count,
                        float* ws, cudaStream_t stream, bool* mapped) {
@@ -81,7 +108,7 @@ cudaError_t launch_all(CacheAttnArgs a, const fa_cache& c, const AttnPlan& p, in
   sides.parts[0] = ws + 4LL * (sgrid + cgrid);
   sides.parts[1] = sides.parts[0] + 2LL * sgrid * partial_floats(8 * p.nt, D);
   sides.rows[0] = 8 * p.nt;
-  sides.rows[1] = kChunkRows;
+  sides.rows[1] = p.item_rows;
   sides.ctas[1] = cgrid;
   if (p.nt != 0) {
     // sequences of at most one round of tiles (one for each warp) are not cut:
@@ -102,26 +129,15 @@ cudaError_t launch_all(CacheAttnArgs a, const fa_cache& c, const AttnPlan& p, in
     if (e != cudaSuccess) return e;
   }
   if (p.chunk) {
-    constexpr int kSmem = ChunkLayout<D>::kSmem;
-    auto kern = fa_cache_chunk_kernel<D, BF16>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e != cudaSuccess) return e;
+    a.item_rows = p.item_rows;
     a.rows_over = p.nt != 0 ? p.upto : 0;
     a.rows_upto = INT_MAX;
     a.join = sides.join[1];
     a.parts = sides.parts[1];
-    CUtensorMap maps[2];
-    *mapped = encode_cache(&maps[0], c.k, c, c.block, false) &&
-              encode_cache(&maps[1], c.v, c, c.block, false);
-    if (!*mapped) return cudaErrorUnknown;
-    // after a step launch it takes the SMs that are done with that one (its
-    // CTAs wait for the step launch before they end)
-    if (p.nt != 0) {
-      e = launch_early(kern, dim3(cgrid), kChunkThreads, kSmem, stream, maps[0], maps[1], a);
-    } else {
-      kern<<<cgrid, kChunkThreads, kSmem, stream>>>(maps[0], maps[1], a);
-      e = cudaGetLastError();
-    }
+    const cudaError_t e =
+        p.item_rows == kChunkRows
+            ? launch_chunk<D, BF16, 0>(a, c, p, cgrid, stream, mapped)
+            : launch_chunk<D, BF16, chunk_parts(D, BF16)>(a, c, p, cgrid, stream, mapped);
     if (e != cudaSuccess) return e;
   }
   const int n = sides.ctas[0] + sides.ctas[1];
@@ -144,7 +160,13 @@ long long cache_workspace_floats(int B, int T, int group, int d, int sm_count) {
 
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, const fa_cache& c, bool bf16, int sm_count,
                               float* ws, cudaStream_t stream, bool* mapped) {
-  const AttnPlan p = plan_attn(a.B, a.T, a.group, a.cu_q != nullptr);
+  AttnPlan p = plan_attn(a.B, a.T, a.group, a.cu_q != nullptr);
+  // Items of 128 rows, K unwidened, where sequences have up to 128 rows to a K / V
+  // head on average. Us with items of 256 rows beside it, bf16 (fp16), 4 K / V heads:
+  // 16 x 24 rows over 8192 keys 58 / 70 (66 / 69), 16 x 64 rows 58 / 70 (59 / 67), 16 x
+  // 128 rows 67 / 77 (69 / 74), one sequence of 4096 rows among 63 of 8 127 / 127 (129 / 127).
+  if (chunk_parts(c.d, bf16) > 0 && static_cast<long long>(a.T) * a.group <= 128LL * a.B)
+    p.item_rows = 128;
   *mapped = true;
   if (c.d == 64)
     return bf16 ? launch_all<64, true>(a, c, p, sm_count, ws, stream, mapped)

@@ -6,16 +6,21 @@
 // least as many keys). More than 128 rows: two tiles of 128 that share every
 // KV tile of 128 keys, and the softmax of one runs while the tensor core works
 // for the other (pair mode). At most 128 rows, a group's drafts or the last
-// rows of a chunk: both halves of the machine work on the same rows, one on
-// the even KV tiles and one on the odd ones, and their results are merged
-// from tensor memory at the end (split mode).
+// rows of a chunk: one Q tile, S in two buffers; of every KV tile one warpgroup
+// takes the first and the other the second 64 keys, each with a maximum, a sum
+// and an O of its own, which are merged at the end (split mode). So S of a tile
+// is formed while the softmax is at the one before.
 //
-// kind::f16 on fp16 operands whatever the queries' type: every e4m3 code is an
-// fp16 value, so K and V lose nothing (the 8-bit kind would need Q and P in 8
-// bits, 2^-4 each), and bf16 queries are brought into fp16's range row by row
-// with a power of two (rows_to_f16). TMA brings the blocks that the table lists
-// into a ring of 8-bit tiles; converter warps widen them into the swizzled
-// operand tiles, and zero what no row may see.
+// The operands are fp16 (kind::f16) whatever the queries' type: every e4m3 code
+// is an fp16 value, so K and V lose nothing, and bf16 queries are brought into
+// fp16's range row by row with a power of two (rows_to_f16). TMA brings the blocks
+// that the table lists into a ring of 8-bit tiles; converter warps widen them
+// into the swizzled operand tiles, and zero what no row may see.
+// PARTS > 0 (split mode only, d 128): Q is written as the sum of PARTS e4m3 tiles
+// (query_parts), and K goes from the cache into the product as it is
+// (kind::f8f6f4). That leaves the converters half of their work for some more
+// time of the tensor core. P cannot be cut up in that way: e4m3's smallest step,
+// 2^-9, would take away the weights of a flat row beside one large one.
 //
 // Both scales go into the exponent, as in fa_cache_step.cuh: e = c ks s + log2
 // vs, P' = 2^(e - m), O = sum P' v8, l = sum P' / vs.
@@ -23,15 +28,25 @@
 // Warp roles (16 warps):
 //   warp 0       issues the MMAs (elected lane), owns the tensor memory
 //   warp 1       copies: table entries, scales, TMA
-//   warps 4-7    softmax and epilogue of tile 0 (split mode: even KV tiles)
-//   warps 8-11   softmax and epilogue of tile 1 (split mode: odd KV tiles)
+//   warps 4-7    softmax and epilogue of tile 0 (split mode: the first 64 keys)
+//   warps 8-11   softmax and epilogue of tile 1 (split mode: the others)
 //   warps 12-15  converters
 // Tensor memory: S0 0-127, S1 128-255, O0 256.., O1 256 + D..; P_i goes over the
-// first 64 columns of S_i.
+// first 64 columns of S_i (split mode: 32 columns of each half).
 //
 // Splitting: as in fa_cache_step.cuh, the items' tiles form one list that is
 // cut into equal shares, one for each SM; fa_cache_join_kernel joins the
 // partial results of cut items.
+//
+// What bounds it. Pair mode: the chain S - softmax - P V - S of each Q tile, as in
+// the forward kernel of whole matrices; tensor memory is full, so S has no second
+// buffer. 2048 tokens behind 14336 others, 32 heads of d 128 on 8: 375 us, 1.37
+// PFLOP/s (71 % of a matrix product's burst rate), tensor pipe active 61 %. Split
+// mode: 16 x 40 rows, 4 K / V heads, 8192 keys: 59 us (with all of K widened, too,
+// and whole tiles for each warpgroup 69 us); a KV tile takes 2400 cycles, 1700 of
+// them the MMAs (shared-memory traffic, 208 KB a tile) and 1700 a
+// warpgroup's softmax, whose warps stand alone on their schedulers. The other
+// third of the time is the launch, Q, the epilogues and the join.
 #pragma once
 
 #include "fa_cache_step.cuh"
@@ -47,27 +62,34 @@ constexpr int kChunkMinShare = 2;  // tiles
 constexpr uint32_t kChunkRegsMma = 64, kChunkRegsSoftmax = 184, kChunkRegsConvert = 80;
 static_assert(kChunkRegsMma + 2 * kChunkRegsSoftmax + kChunkRegsConvert == 512, "register split");
 
-template <int D>
+// PARTS = 0: items of up to 256 rows, K and V widened. PARTS > 0: items of up to
+// 128 rows, Q in PARTS e4m3 tiles, V widened.
+template <int D, int PARTS>
 struct ChunkLayout {
   static constexpr int kPanels = D / 64;
   static constexpr int kTileBytes = kPanels * kPanelBytes;  // 128 rows of fp16
   static constexpr int kRawBytes = kChunkKeys * D;          // 128 rows of codes
-  static constexpr int kStages = D == 128 ? 3 : 6;          // K / V slots (fp16)
-  static constexpr int kRaw = D == 128 ? 3 : 6;             // K / V slots (codes)
-  static constexpr int kOffQ = 0;                           // Q0, Q1
-  static constexpr int kOffKV = 2 * kTileBytes;
+  static constexpr int kQBytes = PARTS > 0 ? PARTS * kRawBytes : kTileBytes;
+  static constexpr int kHalves = PARTS > 0 ? 1 : 2;  // of a tile that are widened: V, or K and V
+  static constexpr int kStages = PARTS > 0 ? 2 : D == 128 ? 3 : 6;            // fp16 slots
+  static constexpr int kRaw = PARTS > 0 ? 3 : D == 128 ? 3 : 6;  // slots of codes
+  static constexpr int kDirect = PARTS > 0 ? 3 : 0;                            // K slots
+  static constexpr int kOffQ = 0;                                              // Q0, Q1
+  static constexpr int kOffKV = (PARTS > 0 ? 1 : 2) * kQBytes;
   static constexpr int kOffRaw = kOffKV + kStages * kTileBytes;
+  static constexpr int kOffK = kOffRaw + kRaw * kRawBytes;
   // scales of a tile's 16-key groups: [16 tiles][8] {ks, log2 vs, 1 / vs, 0}
-  static constexpr int kOffScale = kOffRaw + kRaw * kRawBytes;
+  static constexpr int kOffScale = kOffK + kDirect * kRawBytes;
   static constexpr int kOffNan = kOffScale + 16 * 8 * 16;    // [8 items][D] uint64
-  static constexpr int kOffStats = kOffNan + 8 * D * 8;      // [2][128] m, l of the odd tiles
+  static constexpr int kOffStats = kOffNan + 8 * D * 8;      // [2][128] m, l of the second halves
   static constexpr int kOffShelf = kOffStats + 1024;  // [8 warps] 64 bytes
   static constexpr int kOffBar = kOffShelf + 512;
-  static constexpr int kSmem = kOffBar + 512 + 1024;  // barriers, alignment slack
+  static constexpr int kSmem = kOffBar + 544 + 1024;  // barriers, alignment slack
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kColS = 0, kColO = 256;
   static_assert(kSmem <= 232448, "shared memory budget");
-  static_assert(kRaw <= 8 && kStages + kRaw <= 12, "barrier block");
+  static_assert(kRaw <= 8 && kStages + kRaw + kDirect <= 12, "barrier block");
+  static_assert(kQBytes >= kTileBytes, "the epilogue stages its rows there");
 };
 
 enum ChunkBar : int {
@@ -78,14 +100,17 @@ enum ChunkBar : int {
   kCbStats = 8,       // 128 threads of tile 1: its m, l in shared memory (split mode)
   kCbMerged = 9,      // 128 threads of tile 0: O1 and the stats read (split mode)
   kCbDrain = 10,      // MMA: every tcgen05 op completed
-  kCbScaleFull = 11,  // [16] copy warp: scales of tile n in entry n % 16
-  kCbVDone = 27,      // [8] converter warps: V of tile n converted (its NaN recorded)
+  kCbPSplit = 11,     // [2] 256 softmax threads: both halves of P_b written (split mode)
+  kCbOStep = 13,      // MMA: a tile's products with V done (split mode)
+  kCbScaleFull = 14,  // [16] copy warp: scales of tile n in entry n % 16
+  kCbVDone = 30,      // [8] converter warps: V of tile n converted (its NaN recorded)
   // [stages] converter warps: operand slot filled; [stages] MMA: slot free;
-  // [raw] TMA: raw slot filled; [raw] converter warps: slot free
-  kCbKVFull = 35,
+  // [raw] TMA: raw slot filled; [raw] converter warps: slot free;
+  // [direct] TMA: K slot filled; [direct] MMA: slot free
+  kCbKVFull = 38,
 };
-constexpr int kChunkSlotTmem = 480, kChunkSlotAbort = 484, kChunkSlotStart = 488;
-constexpr int kChunkSlotHidden = 504;  // [raw] bytes: bit g: 16-key group g is hidden
+constexpr int kChunkSlotTmem = 496, kChunkSlotAbort = 500, kChunkSlotStart = 504;
+constexpr int kChunkSlotAnyNan = 528, kChunkSlotHidden = 520;  // [raw] bytes: bit g: 16-key group g is hidden
 
 // Keys that query token i of a sequence sees.
 __device__ __forceinline__ int keys_seen(const CacheAttnArgs& a, const SeqRows& s, int i) {
@@ -96,11 +121,11 @@ __device__ __forceinline__ int keys_seen(const CacheAttnArgs& a, const SeqRows& 
 // least one, so that rows without keys are written).
 __device__ __forceinline__ int chunk_row_blocks(const CacheAttnArgs& a, const SeqRows& s) {
   return takes_seq(a, s) ? static_cast<int>(
-                               (static_cast<long long>(s.count) * a.group + kChunkRows - 1) / kChunkRows)
+                               (static_cast<long long>(s.count) * a.group + a.item_rows - 1) / a.item_rows)
                          : 0;
 }
 __device__ __forceinline__ int chunk_real_tiles(const CacheAttnArgs& a, const SeqRows& s, int rb) {
-  const long long last = min((rb + 1LL) * kChunkRows, static_cast<long long>(s.count) * a.group) - 1;
+  const long long last = min((rb + 1LL) * a.item_rows, static_cast<long long>(s.count) * a.group) - 1;
   return (keys_seen(a, s, static_cast<int>(last / a.group)) + kChunkKeys - 1) / kChunkKeys;
 }
 // Tiles of one head of a sequence.
@@ -160,23 +185,24 @@ struct ChunkWalk {
     return true;
   }
   __device__ __forceinline__ int rows(const CacheAttnArgs& a) const {
-    return static_cast<int>(min(static_cast<long long>(kChunkRows),
+    return static_cast<int>(min(static_cast<long long>(a.item_rows),
                                 static_cast<long long>(s.count) * a.group -
-                                    static_cast<long long>(rb) * kChunkRows));
+                                    static_cast<long long>(rb) * a.item_rows));
   }
   __device__ __forceinline__ int n() const { return max(0, real_end - t0); }
 };
 
 // ---- copies: warp 1. Lane j < 128 / block handles the j-th block of a tile,
 // lane g < 8 the scales of the g-th 16-key group.
-template <int D>
+template <int D, int PARTS>
 __device__ __forceinline__ void chunk_copy_role(const CUtensorMap* tm_k, const CUtensorMap* tm_v,
                                                 const CacheAttnArgs& a, ChunkWalk w, uint8_t* sgen,
                                                 uint32_t sbase, uint32_t bars, const AbortCtx& ab,
                                                 int lane) {
-  using L = ChunkLayout<D>;
+  using L = ChunkLayout<D, PARTS>;
   constexpr int R = L::kRaw;
   constexpr int kRawFull = kCbKVFull + 2 * L::kStages, kRawFree = kRawFull + R;
+  constexpr int kKFull = kRawFree + R, kKFree = kKFull + L::kDirect;
   auto bar = [&](int i) { return bars + 8u * static_cast<uint32_t>(i); };
   float4* const s_scale = reinterpret_cast<float4*>(sgen + L::kOffScale);
   uint8_t* const s_hidden = sgen + L::kOffBar + kChunkSlotHidden;
@@ -185,33 +211,70 @@ __device__ __forceinline__ void chunk_copy_role(const CUtensorMap* tm_k, const C
     ptx::prefetch_tmap(tm_k);
     ptx::prefetch_tmap(tm_v);
   }
-  uint32_t ring = 0, count = 0;
+  uint32_t ring = 0, count = 0, asked = 0;  // V (K and V), tiles, K
   bool ok = true;
   do {
-    // the table entry of this lane's block in tile t, or -1
-    auto entry = [&](int t) {
-      const long long key = static_cast<long long>(t) * kChunkKeys + (lane << a.block_shift);
+    // Table entries and scales are read for four tiles at a time (lane 8 q + g:
+    // 16-key group g of tile q), entries two rounds and scales one round ahead:
+    // two trips to memory one after another for each tile would take longer
+    // than its products.
+    auto entries = [&](int t) {  // block of this lane's group, or -1
+      const long long key = (static_cast<long long>(t) + (lane >> 3)) * kChunkKeys +
+                            ((16 * (lane & 7)) & -(1 << a.block_shift));  // the block's first
       int id = -1;
-      if (lane < boxes && key < w.s.kv_len)
+      if (t + (lane >> 3) < w.real_end && key < w.s.kv_len)
         id = __ldg(a.table + static_cast<long long>(w.b) * a.table_width + (key >> a.block_shift));
       return id >= 0 && id < a.num_blocks ? id : -1;
     };
-    int next = w.t0 < w.real_end ? entry(w.t0) : -1;
-    for (int t = w.t0; t < w.real_end; ++t) {
-      const int id = next;
-      const uint32_t have = __ballot_sync(0xffffffffu, id >= 0);
-      // this lane's 16-key group
-      const int gid = __shfl_sync(0xffffffffu, id, (lane & 7) >> (a.block_shift - 4));
-      const uint32_t hidden = __ballot_sync(0xffffffffu, lane < 8 && gid < 0);
-      float ks = 1.f, vs = 1.f;
-      if (lane < 8 && gid >= 0) {
-        const long long at = static_cast<long long>(gid) * a.Hkv + w.hk;
-        ks = __ldg(a.ks + at);
-        vs = __ldg(a.vs + at);
+    auto scales = [&](int id) {
+      float2 f = make_float2(1.f, 0.f);
+      if (id >= 0) {
+        const long long at = static_cast<long long>(id) * a.Hkv + w.hk;
+        f = make_float2(__ldg(a.ks + at), __ldg(a.vs + at));
       }
-      if (t + 1 < w.real_end) next = entry(t + 1);
+      return f;
+    };
+    int ids = entries(w.t0), ids_next = entries(w.t0 + 4);
+    float2 sc = scales(ids), sc_next = make_float2(0.f, 0.f);
+    for (int t = w.t0; t < w.real_end; ++t) {
+      const int q = (t - w.t0) & 3;
+      if (q == 0) {
+        if (t > w.t0) {
+          ids = ids_next;
+          sc = sc_next;
+          ids_next = entries(t + 4);
+        }
+        sc_next = scales(ids_next);
+      }
+      const uint32_t hidden = (__ballot_sync(0xffffffffu, ids < 0) >> (8 * q)) & 0xFFu;
+      // lane j: the tile's j-th block
+      const int jd = __shfl_sync(0xffffffffu, ids, 8 * q + ((lane << (a.block_shift - 4)) & 7));
+      const int id = lane < boxes ? jd : -1;
+      const uint32_t have = __ballot_sync(0xffffffffu, id >= 0);
+      if constexpr (L::kDirect > 0) {
+        // K in the MMA's layout; keys that no row may see become zeros here
+        const uint32_t slot = asked % L::kDirect;
+        if (!(ok = wait_spin_warp(bar(kKFree + slot), ((asked / L::kDirect) & 1u) ^ 1u, ab,
+                                  kStatusProducer)))
+          break;
+        const uint32_t to = sbase + L::kOffK + slot * L::kRawBytes;
+        if (hidden != 0u) {
+          for (int at = 16 * lane; at < L::kRawBytes; at += 512)
+            if ((hidden >> (at / (16 * D))) & 1u) ptx::st_shared_v4(to + at, 0u, 0u, 0u, 0u);
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (lane == 0)
+          ptx::mbar_arrive_expect_tx(bar(kKFull + slot),
+                                     static_cast<uint32_t>(__popc(have) * box_bytes));
+        __syncwarp();
+        if (id >= 0)
+          ptx::tma_load_4d(to + static_cast<uint32_t>(lane * box_bytes), tm_k, bar(kKFull + slot), 0,
+                           0, w.hk, id);
+        ++asked;
+      }
 #pragma unroll
-      for (int is_v = 0; is_v < 2; ++is_v) {
+      for (int is_v = 2 - L::kHalves; is_v < 2; ++is_v) {
         const uint32_t slot = ring % R;
         if (!(ok = wait_spin_warp(bar(kRawFree + slot), ((ring / R) & 1u) ^ 1u, ab,
                                   kStatusProducer)))
@@ -229,10 +292,8 @@ __device__ __forceinline__ void chunk_copy_role(const CUtensorMap* tm_k, const C
         ++ring;
       }
       if (!ok) break;
-      if (lane < 8)
-        s_scale[(count & 15) * 8 + lane] = gid >= 0
-                                               ? make_float4(ks, log2f(vs), 1.f / vs, 0.f)
-                                               : make_float4(1.f, -INFINITY, 0.f, 0.f);
+      if ((lane >> 3) == q)
+        s_scale[(count & 15) * 8 + (lane & 7)] = make_float4(sc.x, log2f(sc.y), ids >= 0 ? 1.f / sc.y : 0.f, 0.f);
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(bar(kCbScaleFull + (count & 15)));
       ++count;
@@ -241,15 +302,21 @@ __device__ __forceinline__ void chunk_copy_role(const CUtensorMap* tm_k, const C
   if (!ok)  // let the copies in flight land before the CTA exits
     for (uint32_t n = ring > R ? ring - R : 0; n < ring; ++n)
       wait_drain(bar(kRawFull + n % R), (n / R) & 1u, ab, kStatusDrain);
+  if constexpr (L::kDirect > 0) {
+    constexpr uint32_t N = L::kDirect;
+    if (!ok)
+      for (uint32_t n = asked > N ? asked - N : 0; n < asked; ++n)
+        wait_drain(bar(kKFull + n % N), (n / N) & 1u, ab, kStatusDrain);
+  }
 }
 
 // ---- converters: warps 12-15. A thread takes 16 codes of a row at a time: 32
 // bytes in two chunks of one of the row's 128-byte panels.
-template <int D>
+template <int D, int PARTS>
 __device__ __forceinline__ void chunk_convert_role(const CacheAttnArgs& a, ChunkWalk w,
                                                    uint8_t* sgen, uint32_t sbase, uint32_t bars,
                                                    const AbortCtx& ab, int warp, int lane) {
-  using L = ChunkLayout<D>;
+  using L = ChunkLayout<D, PARTS>;
   constexpr int S = L::kStages, R = L::kRaw;
   constexpr int kRawFull = kCbKVFull + 2 * S, kRawFree = kRawFull + R;
   constexpr int kLanesPerRow = D / 16;
@@ -271,17 +338,18 @@ __device__ __forceinline__ void chunk_convert_role(const CacheAttnArgs& a, Chunk
   const uint32_t ch = static_cast<uint32_t>(2 * (c & 3)), x7 = static_cast<uint32_t>(r0 & 7);
   const uint32_t to0 = row_at + ((ch ^ x7) << 4), to1 = row_at + (((ch + 1u) ^ x7) << 4);
   unsigned long long* const s_nan = reinterpret_cast<unsigned long long*>(sgen + L::kOffNan);
+  volatile uint32_t* const s_any = reinterpret_cast<volatile uint32_t*>(sgen + L::kOffBar + kChunkSlotAnyNan);
   const uint8_t* const s_hidden = sgen + L::kOffBar + kChunkSlotHidden;
   uint32_t ring = 0, count = 0;  // slots filled, tiles done
   bool ok = true;
   do {
     const int first_seen = keys_seen(
-        a, w.s, static_cast<int>(static_cast<long long>(w.rb) * kChunkRows / a.group));
-    const int halves = 2 * max(0, w.real_end - w.t0);  // K and V of each tile
+        a, w.s, static_cast<int>(static_cast<long long>(w.rb) * a.item_rows / a.group));
+    const int halves = L::kHalves * max(0, w.real_end - w.t0);  // (K and) V of each tile
 #pragma unroll 1
     for (int h = 0; h < halves; ++h, ++ring) {
-      const bool is_v = (h & 1) != 0;
-      const int key0 = (w.t0 + (h >> 1)) * kChunkKeys;
+      const bool is_v = PARTS > 0 || (h & 1) != 0;
+      const int key0 = (w.t0 + h / L::kHalves) * kChunkKeys;
       const uint32_t slot = ring % S, raw = ring % R;
       if (!(ok = wait_bounded_warp(bar(kRawFull + raw), (ring / R) & 1u, ab, kStatusProducer) &&
                  wait_bounded_warp(bar(kCbKVFull + S + slot), ((ring / S) & 1u) ^ 1u, ab,
@@ -311,6 +379,7 @@ __device__ __forceinline__ void chunk_convert_role(const CacheAttnArgs& a, Chunk
                 const uint32_t bad = nan_bytes(v[q]);
                 for (int y = 0; y < 4; ++y)
                   if ((bad >> (8 * y)) & 0x80u) {
+                    *s_any = 1;
                     atomicMax(s_nan + (w.item & 7) * D + 16 * c + 4 * q + y,
                               (static_cast<unsigned long long>(w.item + 1) << 32) |
                                   static_cast<unsigned>(0x7FFFFFFF - key));
@@ -346,97 +415,145 @@ __device__ __forceinline__ void chunk_convert_role(const CacheAttnArgs& a, Chunk
   } while (ok && w.next(a));
 }
 
-// ---- MMA issue: warp 0
+// S[tmem] = Q K^T with Q in PARTS tiles of e4m3 (K-major SW128, one after
+// another) that add up to its rows, and K as the cache holds it.
+template <int D, int PARTS>
+__device__ __forceinline__ void issue_qk_parts(uint32_t d_tmem, uint64_t dq, uint64_t dk) {
+  static_assert(D == 128, "a row is one 128-byte panel");
+  constexpr uint32_t id = ptx::idesc_f8(128, 128);
+#pragma unroll
+  for (int p = 0; p < PARTS; ++p) {
+    uint64_t k = dk;
+#pragma unroll
+    for (int kk = 0; kk < D / 32; ++kk) {
+      ptx::umma_f8_ss_elect(d_tmem, dq, k, id, p + kk > 0 ? 1u : 0u);
+      dq = desc_add(dq, kk + 1 < D / 32 ? 32u : static_cast<uint32_t>(kChunkKeys * D - 96));
+      k = desc_add(k, 32u);
+      asm volatile("" : "+l"(dq), "+l"(k));  // advance in place: three live descriptors
+    }
+  }
+}
+
+// O[tmem] (+)= P V over half `h` of a tile's keys: 64 keys of P in tensor memory.
 template <int D>
+__device__ __forceinline__ void issue_pv_half(uint32_t d_tmem, uint32_t p_tmem, uint64_t dv, int h,
+                                              bool accumulate) {
+  constexpr uint32_t id = ptx::idesc_f16(false, true, 128, D);
+  dv = desc_add(dv, static_cast<uint32_t>(4 * 2048 * h));
+#pragma unroll
+  for (int kk = 0; kk < 4; ++kk) {
+    ptx::umma_f16_ts_elect(d_tmem, p_tmem + 8u * kk, dv, id, accumulate || kk > 0 ? 1u : 0u);
+    dv = desc_add(dv, 2048u);
+    asm volatile("" : "+l"(dv));
+  }
+}
+
+// ---- MMA issue: warp 0
+template <int D, int PARTS>
 __device__ __forceinline__ void chunk_mma_role(const CacheAttnArgs& a, ChunkWalk w, uint32_t sbase,
                                                uint32_t bars, uint32_t tmem, const AbortCtx& ab) {
-  using L = ChunkLayout<D>;
+  using L = ChunkLayout<D, PARTS>;
   constexpr int S = L::kStages;
   auto bar = [&](int i) { return bars + 8u * static_cast<uint32_t>(i); };
-  const uint64_t dQ[2] = {desc_kmajor(sbase + L::kOffQ),
-                          desc_kmajor(sbase + L::kOffQ + L::kTileBytes)};
-  const uint64_t dK0 = desc_kmajor(sbase + L::kOffKV);
+  constexpr int N = PARTS > 0 ? L::kDirect : S;  // slots of K
+  constexpr int kKFull = PARTS > 0 ? kCbKVFull + 2 * S + 2 * L::kRaw : kCbKVFull;
+  const uint64_t dQ[2] = {desc_kmajor(sbase + L::kOffQ), desc_kmajor(sbase + L::kOffQ + L::kQBytes)};
+  const uint64_t dK0 = desc_kmajor(sbase + (PARTS > 0 ? L::kOffK : L::kOffKV));
   const uint64_t dV0 = desc_v(sbase + L::kOffKV);
   const uint32_t tS[2] = {tmem + L::kColS, tmem + L::kColS + 128};
   const uint32_t tO[2] = {tmem + L::kColO, tmem + L::kColO + D};
-  auto off = [](uint32_t idx) { return (idx % S) * static_cast<uint32_t>(L::kTileBytes); };
-  auto kv_wait = [&](uint32_t idx) {
-    return wait_spin_warp(bar(kCbKVFull + idx % S), (idx / S) & 1u, ab, kStatusMma);
+  // K and V of tile t (of all that this CTA reads) as they were filled
+  auto k_at = [](uint32_t t) { return PARTS > 0 ? t : 2u * t; };
+  auto v_at = [](uint32_t t) { return PARTS > 0 ? t : 2u * t + 1u; };
+  auto k_wait = [&](uint32_t t) {
+    return wait_spin_warp(bar(kKFull + k_at(t) % N), (k_at(t) / N) & 1u, ab, kStatusMma);
   };
-  auto kv_free = [&](uint32_t idx) { ptx::umma_commit_elect(bar(kCbKVFull + S + idx % S)); };
-  auto qk = [&](int q, int i, uint32_t idx) {
-    issue_qk_desc<D, false, true>(tS[i], dQ[q], desc_add(dK0, off(idx)));
+  auto v_wait = [&](uint32_t t) {
+    return wait_spin_warp(bar(kCbKVFull + v_at(t) % S), (v_at(t) / S) & 1u, ab, kStatusMma);
+  };
+  auto k_free = [&](uint32_t t) { ptx::umma_commit_elect(bar(kKFull + N + k_at(t) % N)); };
+  auto v_free = [&](uint32_t t) { ptx::umma_commit_elect(bar(kCbKVFull + S + v_at(t) % S)); };
+  auto qk = [&](int q, int i, uint32_t t) {
+    const uint64_t dk = desc_add(
+        dK0, (k_at(t) % N) * static_cast<uint32_t>(PARTS > 0 ? L::kRawBytes : L::kTileBytes));
+    if constexpr (PARTS > 0) issue_qk_parts<D, PARTS>(tS[i], dQ[q], dk);
+    else issue_qk_desc<D, false, true>(tS[i], dQ[q], dk);
     ptx::umma_commit_elect(bar(kCbSFull + i));
   };
-  auto pv = [&](int i, uint32_t idx, bool acc) {
-    issue_pv_ts_desc<D, false, true>(tO[i], tS[i], desc_add(dV0, off(idx)), acc);
+  auto v_desc = [&](uint32_t t) {
+    return desc_add(dV0, (v_at(t) % S) * static_cast<uint32_t>(L::kTileBytes));
   };
-  uint32_t ring = 0, qn[2] = {0u, 0u}, pn[2] = {0u, 0u};
+  auto pv = [&](int i, uint32_t t, bool acc) {
+    issue_pv_ts_desc<D, false, true>(tO[i], tS[i], v_desc(t), acc);
+  };
+  uint32_t done = 0, qn[2] = {0u, 0u}, pn[2] = {0u, 0u}, hn[2] = {0u, 0u};  // tiles, Q, P, P in halves
   bool ok = true;
   do {
     const int n = w.n();
     if (n == 0) continue;
-    const bool pair = w.rows(a) > 128;
+    const bool pair = PARTS == 0 && w.rows(a) > 128;
     ok = wait_spin_warp(bar(kCbQFull + 0), (qn[0]++) & 1u, ab, kStatusMma) &&
-         (!pair || wait_spin_warp(bar(kCbQFull + 1), (qn[1]++) & 1u, ab, kStatusMma));
+         (!(pair || PARTS > 0) ||
+          wait_spin_warp(bar(kCbQFull + 1), (qn[1]++) & 1u, ab, kStatusMma));
     if (!ok) break;
-    // K of tile j is slot ring + 2 j, its V the next one
     if (pair) {
-      if (!(ok = kv_wait(ring))) break;
+      if (!(ok = k_wait(done))) break;
       ptx::tc_fence_after();
-      qk(0, 0, ring);
-      qk(1, 1, ring);
-      kv_free(ring);
+      qk(0, 0, done);
+      qk(1, 1, done);
+      k_free(done);
       for (int j = 0; j < n && ok; ++j) {
-        const uint32_t vj = ring + 2u * j + 1u, kn = vj + 1u;
+        const uint32_t t = done + static_cast<uint32_t>(j);
         const bool more = j + 1 < n;
-        if (!(ok = kv_wait(vj))) break;
+        if (!(ok = v_wait(t))) break;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           if (!(ok = wait_spin_warp(bar(kCbPFull + i), (pn[i]++) & 1u, ab, kStatusMma))) break;
           ptx::tc_fence_after();
-          pv(i, vj, j > 0);
+          pv(i, t, j > 0);
           if (!more) {
             ptx::umma_commit_elect(bar(kCbOFull + i));
             continue;
           }
           if (i == 0) {
-            if (!(ok = kv_wait(kn))) break;
+            if (!(ok = k_wait(t + 1u))) break;
             ptx::tc_fence_after();
           }
-          qk(i, i, kn);
+          qk(i, i, t + 1u);
         }
         if (!ok) break;
-        kv_free(vj);
-        if (more) kv_free(kn);
+        v_free(t);
+        if (more) k_free(t + 1u);
       }
     } else {
       for (int i = 0; i < 2 && i < n && ok; ++i) {
-        if (!(ok = kv_wait(ring + 2u * i))) break;
+        if (!(ok = k_wait(done + i))) break;
         ptx::tc_fence_after();
-        qk(0, i, ring + 2u * i);
-        kv_free(ring + 2u * i);
+        qk(0, i, done + i);
+        k_free(done + i);
       }
       for (int j = 0; j < n && ok; ++j) {
         const int i = j & 1;
-        const uint32_t vj = ring + 2u * j + 1u, kn = vj + 3u;
-        if (!(ok = kv_wait(vj))) break;
-        if (!(ok = wait_spin_warp(bar(kCbPFull + i), (pn[i]++) & 1u, ab, kStatusMma))) break;
+        const uint32_t t = done + static_cast<uint32_t>(j);
+        if (!(ok = v_wait(t))) break;
+        if (!(ok = wait_spin_warp(bar(kCbPSplit + i), (hn[i]++) & 1u, ab, kStatusMma))) break;
         ptx::tc_fence_after();
-        pv(i, vj, j > 1);
-        kv_free(vj);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) issue_pv_half<D>(tO[h], tS[i] + 64u * h, v_desc(t), h, j > 0);
+        ptx::umma_commit_elect(bar(kCbOStep));
+        v_free(t);
         if (j + 2 < n) {
-          if (!(ok = kv_wait(kn))) break;
+          if (!(ok = k_wait(t + 2u))) break;
           ptx::tc_fence_after();
-          qk(0, i, kn);
-          kv_free(kn);
-        } else {
-          ptx::umma_commit_elect(bar(kCbOFull + i));
+          qk(0, i, t + 2u);
+          k_free(t + 2u);
+        } else if (j + 1 == n) {
+          ptx::umma_commit_elect(bar(kCbOFull + 0));
         }
       }
     }
     if (!ok) break;
-    ring += 2u * static_cast<uint32_t>(n);
+    done += static_cast<uint32_t>(n);
   } while (w.next(a));
   ptx::umma_commit_elect(bar(kCbDrain));
   wait_drain(bar(kCbDrain), 0u, ab, kStatusDrain);
@@ -482,203 +599,326 @@ __device__ __forceinline__ ChunkShelf unshelve(uint32_t at) {
 struct RowAt {
   int i, head;
 };
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+  __half2 x, y;
+  __builtin_memcpy(&x, &a, 4);
+  __builtin_memcpy(&y, &b, 4);
+  x = __hsub2(x, y);
+  __builtin_memcpy(&a, &x, 4);
+  return a;
+}
+
 __device__ __forceinline__ RowAt row_at(const CacheAttnArgs& a, const ChunkWalk& w, int r) {
-  const int row = w.rb * kChunkRows + r;  // (T * H is in int range)
+  const int row = w.rb * a.item_rows + r;  // (T * H is in int range)
   const int i = row / a.group;
   return {i, w.hk * a.group + row - i * a.group};
 }
 
-template <int D, bool BF16>
+// The power of two that is 1 / 256 to 1 / 128 of the largest of the magnitudes whose
+// 16-bit patterns `top` bounds (NaN if there is an infinity or NaN among them).
+template <bool BF16>
+__device__ __forceinline__ float e4m3_step(uint32_t top) {
+  const float big = BF16 ? __uint_as_float(top << 16) : unpack_f16(top).x;
+  const int e = max(static_cast<int>(__float_as_uint(big) >> 23) - 127 - 7, -126);
+  const float fac = top == 0u ? 1.f : __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+  return top >= (BF16 ? 0x7F80u : 0x7C00u) ? __int_as_float(0x7FFFFFFF) : fac;
+}
+
+// Chunks e0 .. e1 - 1 (16 elements each) of this thread's query row p as PARTS
+// e4m3 rows at `to` (row r of tiles of kChunkKeys rows) that add up to row / fac,
+// whose largest magnitude is 128 to 256. bf16's 8-bit significands are the sum of
+// two parts, fp16's 11 bits of three, down to elements 2^-16 of the largest one;
+// below, the last part rounds to multiples of 2^-9, 2^-16 of the largest.
+template <int D, bool BF16, int PARTS>
+__device__ __forceinline__ void query_parts(const uint16_t* p, float fac, uint32_t to, int r, int e0,
+                                            int e1) {
+  const float inv = 1.f / fac;
+#pragma unroll 1  // (unrolled, it took longer to fetch than to run)
+  for (int e = e0; e < e1; ++e) {
+    const uint4 u0 = *reinterpret_cast<const uint4*>(p + 16 * e);
+    const uint4 u1 = *reinterpret_cast<const uint4*>(p + 16 * e + 8);
+    uint32_t h[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      float2 f;
+      if constexpr (BF16) f = make_float2(__uint_as_float(h[x] << 16), __uint_as_float(h[x] & 0xFFFF0000u));
+      else f = unpack_f16(h[x]);
+      h[x] = pack_f16(f.x * inv, f.y * inv);
+    }
+#pragma unroll
+    for (int q = 0; q < PARTS; ++q) {
+      uint32_t code[4];
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        const uint16_t c = ptx::f16x2_to_e4m3x2(h[x]);
+        code[x >> 1] = x & 1 ? code[x >> 1] | (static_cast<uint32_t>(c) << 16) : c;
+        if (q + 1 < PARTS) h[x] = sub_f16x2(h[x], ptx::e4m3x2_to_f16x2(c));
+      }
+      ptx::st_shared_v4(to + static_cast<uint32_t>(q * kChunkKeys * D + r * D) +
+                            (static_cast<uint32_t>(e ^ (r & 7)) << 4),
+                        code[0], code[1], code[2], code[3]);
+    }
+  }
+}
+
+// The tiles of one item for a warpgroup: NC = 128, all keys of a tile for the rows
+// of Q tile `wg` (pair mode), or NC = 64, half `wg` of the keys (split mode).
+// S of tile j is in S_wg, or in that half of S_(j mod 2); P goes over it.
+struct TileLoop {
+  uint32_t tl, phase;  // tensor memory of the warp's lanes; parities (chunk_softmax_role)
+  int wg, n, k0;       // tiles of the item, first key
+  uint32_t count;      // tiles before the item
+  int lim, lim0;       // keys that the row and that all rows see
+  float crow;
+  bool idle;
+};
+template <int D, int NC, int PARTS>
+__device__ __forceinline__ bool softmax_tiles(const CacheAttnArgs& a, const TileLoop& x,
+                                              const uint8_t* sgen, uint32_t bars,
+                                              const AbortCtx& ab, float& m_ref, float& l) {
+  using L = ChunkLayout<D, PARTS>;
+  constexpr bool kHalf = NC == 64;
+  constexpr int G = NC / 16;
+  auto bar = [&](int i) { return bars + 8u * static_cast<uint32_t>(i); };
+  const uint32_t tO = x.tl + L::kColO + static_cast<uint32_t>(D * x.wg);
+  const bool one_scale = a.block_shift == 7;  // a tile is one block
+  int k0 = x.k0 + (kHalf ? 64 * x.wg : 0);
+  for (int j = 0; j < x.n; ++j, k0 += kChunkKeys) {
+    const int b = kHalf ? j & 1 : x.wg;
+    const uint32_t tix = x.count + static_cast<uint32_t>(j);
+    const uint32_t tS = x.tl + L::kColS + static_cast<uint32_t>(128 * b + (kHalf ? 64 * x.wg : 0));
+    if (!(wait_bounded_warp(bar(kCbSFull + b),
+                            ((x.phase >> b) ^ static_cast<uint32_t>(kHalf ? j >> 1 : j)) & 1u, ab,
+                            kStatusSoftmax) &&
+          wait_bounded_warp(bar(kCbScaleFull + (tix & 15u)), (tix >> 4) & 1u, ab, kStatusSoftmax)))
+      return false;
+    ptx::tc_fence_after();
+    const uint32_t p_bar = bar(kHalf ? kCbPSplit + b : kCbPFull + x.wg);
+    if (x.idle) {
+      ptx::tc_fence_before();
+      ptx::mbar_arrive(p_bar);
+      continue;
+    }
+    uint32_t sr[NC / 64][2][32];
+    float mx_lo, mx_hi;
+    ptx::tmem_ld64_max(tS, sr[0], mx_lo);
+    if constexpr (kHalf) {
+      ptx::tmem_ld_wait(sr[0][0]);
+      ptx::tmem_ld_wait(sr[0][1]);
+      mx_hi = mx_lo;
+    } else {
+      ptx::tmem_ld64_max(tS + 64u, sr[NC / 64 - 1], mx_hi);
+      ptx::tmem_ld_wait64x2(sr[0], sr[NC / 64 - 1]);
+    }
+    ptx::tmem_ld_wait_f2(mx_lo, mx_hi);
+    float s[NC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) s[c] = __uint_as_float(sr[c >> 6][(c >> 5) & 1][c & 31]);
+    const float4* const sc = reinterpret_cast<const float4*>(sgen + L::kOffScale) +
+                             (tix & 15u) * 8 + (kHalf ? 4 * x.wg : 0);
+    auto scales = [&](int g) {  // {ks, log2 vs, 1 / vs} of a 16-key group
+      const float4 v = sc[g];
+      return make_float3(v.x * x.crow, v.y, v.z);
+    };
+    const bool need_mask = k0 + NC > x.lim0;
+    float m_tile;
+    if (one_scale && !need_mask) {
+      const float3 f = scales(0);
+      m_tile = fmaf(fmaxf(mx_lo, mx_hi), f.x, f.y);
+    } else {
+      if (need_mask) {
+        const int see = x.lim - k0;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) s[c] = c < see ? s[c] : -INFINITY;
+      }
+      m_tile = -INFINITY;
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const float3 f = scales(g);
+        float t0 = fmaxf(s[16 * g], s[16 * g + 1]), t1 = fmaxf(s[16 * g + 2], s[16 * g + 3]);
+#pragma unroll
+        for (int c = 4; c < 16; c += 4) {
+          t0 = ptx::fmax3(t0, s[16 * g + c], s[16 * g + c + 1]);
+          t1 = ptx::fmax3(t1, s[16 * g + c + 2], s[16 * g + c + 3]);
+        }
+        m_tile = fmaxf(m_tile, fmaf(fmaxf(t0, t1), f.x, f.y));
+      }
+    }
+    float alpha = 1.f;
+    if (m_tile > m_ref + 8.f) {
+      alpha = ptx::ex2(m_ref - m_tile);  // (0 for the first visible tile)
+      m_ref = m_tile;
+    }
+    const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
+    l *= alpha;
+    uint32_t pk[NC / 64][32];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const float3 f = scales(g);
+      const float add = f.y + neg;
+      const float2 f2 = make_float2(f.x, f.x), a2 = make_float2(add, add);
+      float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const float2 t = ptx::ffma2(make_float2(s[16 * g + 2 * c], s[16 * g + 2 * c + 1]), f2, a2);
+        const float p0 = ptx::ex2(t.x), p1 = ptx::ex2(t.y);
+        pk[g >> 2][(g & 3) * 8 + c] = pack_f16(p0, p1);
+        if (c & 1) sum1 = ptx::fadd2(sum1, make_float2(p0, p1));
+        else sum0 = ptx::fadd2(sum0, make_float2(p0, p1));
+      }
+      sum0 = ptx::fadd2(sum0, sum1);
+      l = fmaf(sum0.x + sum0.y, f.z, l);
+    }
+    ptx::tmem_st32(tS, pk[0]);
+    if constexpr (!kHalf) ptx::tmem_st32(tS + 32u, pk[NC / 64 - 1]);
+    if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+      // O has to hold the products so far. Pair mode: S_wg's commit came after the
+      // last of them. Split mode: S of this tile was formed before them.
+      if constexpr (kHalf) {
+        if (!wait_bounded_warp(bar(kCbOStep), ((x.phase >> 2) + static_cast<uint32_t>(j - 1)) & 1u, ab,
+                               kStatusSoftmax))
+          return false;
+        ptx::tc_fence_after();
+      }
+      const float2 a2 = make_float2(alpha, alpha);
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        ptx::tmem_ld32(tO + 32u * c, o);
+        ptx::tmem_ld_wait(o);
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          const float2 v =
+              ptx::fmul2(make_float2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), a2);
+          o[e] = __float_as_uint(v.x);
+          o[e + 1] = __float_as_uint(v.y);
+        }
+        ptx::tmem_st32(tO + 32u * c, o);
+      }
+    }
+    ptx::tmem_st_wait();
+    ptx::tc_fence_before();
+    ptx::mbar_arrive(p_bar);
+  }
+  return true;
+}
+
+template <int D, bool BF16, int PARTS>
 __device__ __forceinline__ void chunk_softmax_role(const CacheAttnArgs& a, const ChunkWalk& start,
                                                    int share, uint8_t* sgen, uint32_t sbase,
                                                    uint32_t bars, uint32_t tmem, const AbortCtx& ab,
                                                    int warp, int lane) {
-  using L = ChunkLayout<D>;
+  using L = ChunkLayout<D, PARTS>;
   constexpr int kLanes = D / 8, kRowsPerTurn = 32 / kLanes;  // 16 bytes of a 16-bit row each
   auto bar = [&](int i) { return bars + 8u * static_cast<uint32_t>(i); };
   const int wg = (warp >> 2) - 1;
   const int r = (warp & 3) * 32 + lane;
   const uint32_t tl = ptx::tmem_lane_base(tmem, warp);
   const uint32_t shelf = sbase + L::kOffShelf + static_cast<uint32_t>(warp - 4) * 64u;
-  uint32_t sn = 0, count = 0;  // S tiles taken; tiles before the item
+  uint32_t phase = 0, count = 0;  // parities (bits 0, 1: S_i; 2: O steps); tiles before the item
   shelve(shelf, ChunkShelf{start, 0u, share}, lane);
   for (;;) {
     // ---- an item: Q, and what its tile loop needs
-    int n, step, k0, lim, lim0;  // tiles, step, first key; keys that the row and that all rows see
-    bool idle;
-    float crow = a.scale_log2;
+    int n;
+    bool in_pairs;
+    TileLoop x;
+    x.crow = a.scale_log2;
     {
       const ChunkShelf k = unshelve(shelf);
       const ChunkWalk& w = k.w;
       n = w.n();
       const int rows = w.rows(a);
-      const bool pair = rows > 128;
+      const bool pair = PARTS == 0 && rows > 128;
       const int base = pair ? 128 * wg : 0;  // the tile's first row
-      step = pair ? 1 : 2;
-      k0 = (w.t0 + (pair ? 0 : wg)) * kChunkKeys;
-      lim = keys_seen(a, w.s, row_at(a, w, base + r < rows ? base + r : 0).i);
-      lim0 = keys_seen(a, w.s, row_at(a, w, base).i);
+      in_pairs = pair;
+      x.tl = tl;
+      x.phase = phase;
+      x.wg = wg;
+      x.n = n;
+      x.count = count;
+      x.k0 = w.t0 * kChunkKeys;
+      x.lim = keys_seen(a, w.s, row_at(a, w, base + r < rows ? base + r : 0).i);
+      x.lim0 = keys_seen(a, w.s, row_at(a, w, base).i);
       // (a warp without rows hands P over as it is: its rows of O are not read)
-      idle = base + r - lane >= rows;
+      x.idle = base + r - lane >= rows;
       if (n > 0) {
-        // this thread's row of Q, widened or rescaled to fp16, into the swizzled
-        // layout. (A row for each thread, not 16 lanes to a row, which reads
+        // this thread's row of Q into the swizzled layout. (A row for each thread, not 16 lanes to a row, which reads
         // whole lines but has to loop over the rows: 2048 x 16384 chunk 387 us,
         // drafts 70.6 us; 378 and 68.7 us so. Unrolled, its code alone took
         // longer to fetch than the rows: 415 us.)
         const bool there = base + r < rows;
         const RowAt at = row_at(a, w, there ? base + r : 0);
         const uint16_t* p = static_cast<const uint16_t*>(a.q) + q_offset(a, w.b, w.s, at.i, at.head);
-        uint32_t q[D / 2];
+        float fac;
+        if constexpr (PARTS > 0) {
+          uint32_t top = 0;
+          if (there) {
 #pragma unroll
-        for (int e = 0; e < D / 8; ++e) {
-          uint4 v = make_uint4(0u, 0u, 0u, 0u);
-          if (there) v = *reinterpret_cast<const uint4*>(p + 8 * e);
-          q[4 * e] = v.x;
-          q[4 * e + 1] = v.y;
-          q[4 * e + 2] = v.z;
-          q[4 * e + 3] = v.w;
-        }
-        const float fac = rows_to_f16<D / 2, 1, BF16>(q);
-        if (pair || wg == 0) {
-          const uint32_t to = sbase + L::kOffQ +
-                              static_cast<uint32_t>((pair ? wg : 0) * L::kTileBytes + r * 128);
+            for (int e = 0; e < D / 8; ++e) {
+              const uint4 v = *reinterpret_cast<const uint4*>(p + 8 * e);
+              constexpr uint32_t kAbs = 0x7FFF7FFFu;
+              top = __vmaxu2(__vmaxu2(top, __vmaxu2(v.x & kAbs, v.y & kAbs)),
+                             __vmaxu2(v.z & kAbs, v.w & kAbs));
+            }
+          }
+          fac = e4m3_step<BF16>(max(top & 0xFFFFu, top >> 16));
+          // each warpgroup writes half of the row
+          if (there)
+            query_parts<D, BF16, PARTS>(p, fac, sbase + L::kOffQ, r, wg * (D / 32), (wg + 1) * (D / 32));
+        } else {
+          uint32_t q[D / 2];
 #pragma unroll
-          for (int e = 0; e < D / 8; ++e)
-            ptx::st_shared_v4(to + (e >> 3) * kPanelBytes + (static_cast<uint32_t>((e & 7) ^ (r & 7)) << 4),
-                              q[4 * e], q[4 * e + 1], q[4 * e + 2], q[4 * e + 3]);
+          for (int e = 0; e < D / 8; ++e) {
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (there) v = *reinterpret_cast<const uint4*>(p + 8 * e);
+            q[4 * e] = v.x;
+            q[4 * e + 1] = v.y;
+            q[4 * e + 2] = v.z;
+            q[4 * e + 3] = v.w;
+          }
+          fac = rows_to_f16<D / 2, 1, BF16>(q);
+          if (pair || wg == 0) {
+            const uint32_t to = sbase + L::kOffQ +
+                                static_cast<uint32_t>((pair ? wg : 0) * L::kQBytes + r * 128);
+#pragma unroll
+            for (int e = 0; e < D / 8; ++e)
+              ptx::st_shared_v4(to + (e >> 3) * kPanelBytes +
+                                    (static_cast<uint32_t>((e & 7) ^ (r & 7)) << 4),
+                                q[4 * e], q[4 * e + 1], q[4 * e + 2], q[4 * e + 3]);
+          }
         }
-        crow *= fac;
-        if (pair || wg == 0) {
+        x.crow *= fac;
+        if (PARTS > 0 || pair || wg == 0) {
           ptx::fence_proxy_async_smem();
-          ptx::mbar_arrive(bar(kCbQFull + (pair ? wg : 0)));
+          ptx::mbar_arrive(bar(kCbQFull + wg));
         }
       }
     }
-    const uint32_t tS = tl + L::kColS + 128u * wg;
-    const uint32_t tO = tl + L::kColO + static_cast<uint32_t>(D) * wg;
-    const bool one_scale = a.block_shift == 7;  // a tile is one block
     float m_ref = -INFINITY, l = 0.f;
-    bool first = true, ok = true;
-    for (int j = step == 1 ? 0 : wg; j < n; j += step, k0 += step * kChunkKeys) {
-      const uint32_t tix = count + static_cast<uint32_t>(j);
-      if (!(ok = wait_bounded_warp(bar(kCbSFull + wg), sn & 1u, ab, kStatusSoftmax) &&
-                 wait_bounded_warp(bar(kCbScaleFull + (tix & 15u)), (tix >> 4) & 1u, ab,
-                                   kStatusSoftmax)))
-        break;
-      ++sn;
-      ptx::tc_fence_after();
-      if (idle) {
-        ptx::tc_fence_before();
-        ptx::mbar_arrive(bar(kCbPFull + wg));
-        continue;
-      }
-      uint32_t sr[2][2][32];
-      float mx_lo, mx_hi;
-      ptx::tmem_ld64_max(tS, sr[0], mx_lo);
-      ptx::tmem_ld64_max(tS + 64u, sr[1], mx_hi);
-      ptx::tmem_ld_wait64x2(sr[0], sr[1]);
-      ptx::tmem_ld_wait_f2(mx_lo, mx_hi);
-      float s[128];
-#pragma unroll
-      for (int c = 0; c < 128; ++c) s[c] = __uint_as_float(sr[c >> 6][(c >> 5) & 1][c & 31]);
-      const float4* const sc = reinterpret_cast<const float4*>(sgen + L::kOffScale) + (tix & 15u) * 8;
-      auto scales = [&](int g) {  // {ks, log2 vs, 1 / vs} of a 16-key group
-        const float4 v = sc[g];
-        return make_float3(v.x * crow, v.y, v.z);
-      };
-      const bool need_mask = k0 + kChunkKeys > lim0;
-      float m_tile;
-      if (one_scale && !need_mask) {
-        const float3 f = scales(0);
-        m_tile = fmaf(fmaxf(mx_lo, mx_hi), f.x, f.y);
-      } else {
-        if (need_mask) {
-          const int see = lim - k0;
-#pragma unroll
-          for (int c = 0; c < 128; ++c) s[c] = c < see ? s[c] : -INFINITY;
-        }
-        m_tile = -INFINITY;
-#pragma unroll
-        for (int g = 0; g < 8; ++g) {
-          const float3 f = scales(g);
-          float t0 = fmaxf(s[16 * g], s[16 * g + 1]), t1 = fmaxf(s[16 * g + 2], s[16 * g + 3]);
-#pragma unroll
-          for (int c = 4; c < 16; c += 4) {
-            t0 = ptx::fmax3(t0, s[16 * g + c], s[16 * g + c + 1]);
-            t1 = ptx::fmax3(t1, s[16 * g + c + 2], s[16 * g + c + 3]);
-          }
-          m_tile = fmaxf(m_tile, fmaf(fmaxf(t0, t1), f.x, f.y));
-        }
-      }
-      float alpha = 1.f;
-      if (m_tile > m_ref + 8.f) {
-        alpha = ptx::ex2(m_ref - m_tile);  // (0 for the first visible tile)
-        m_ref = m_tile;
-      }
-      const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
-      l *= alpha;
-      uint32_t pk[2][32];
-#pragma unroll
-      for (int g = 0; g < 8; ++g) {
-        const float3 f = scales(g);
-        const float add = f.y + neg;
-        const float2 f2 = make_float2(f.x, f.x), a2 = make_float2(add, add);
-        float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const float2 t = ptx::ffma2(make_float2(s[16 * g + 2 * c], s[16 * g + 2 * c + 1]), f2, a2);
-          const float p0 = ptx::ex2(t.x), p1 = ptx::ex2(t.y);
-          pk[g >> 2][(g & 3) * 8 + c] = pack_f16(p0, p1);
-          if (c & 1) sum1 = ptx::fadd2(sum1, make_float2(p0, p1));
-          else sum0 = ptx::fadd2(sum0, make_float2(p0, p1));
-        }
-        sum0 = ptx::fadd2(sum0, sum1);
-        l = fmaf(sum0.x + sum0.y, f.z, l);
-      }
-      ptx::tmem_st32(tS, pk[0]);
-      ptx::tmem_st32(tS + 32u, pk[1]);
-      // O_i holds the products so far: S_i's commit came after the last of them
-      if (!first && __any_sync(0xffffffffu, alpha != 1.f)) {
-        const float2 a2 = make_float2(alpha, alpha);
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
-          ptx::tmem_ld32(tO + 32u * c, o);
-          ptx::tmem_ld_wait(o);
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const float2 v =
-                ptx::fmul2(make_float2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), a2);
-            o[e] = __float_as_uint(v.x);
-            o[e + 1] = __float_as_uint(v.y);
-          }
-          ptx::tmem_st32(tO + 32u * c, o);
-        }
-      }
-      ptx::tmem_st_wait();
-      ptx::tc_fence_before();
-      ptx::mbar_arrive(bar(kCbPFull + wg));
-      first = false;
+    if (PARTS == 0 && in_pairs) {
+      if (!softmax_tiles<D, 128, PARTS>(a, x, sgen, bars, ab, m_ref, l)) return;
+      phase ^= n & 1 ? 3u : 0u;
+    } else {
+      if (!softmax_tiles<D, 64, PARTS>(a, x, sgen, bars, ab, m_ref, l)) return;
+      phase ^= static_cast<uint32_t>((((n + 1) >> 1) & 1) | (n & 2) | ((n & 1) << 2));
     }
-    if (!ok) return;
 
     // ---- epilogue
     ChunkShelf k = unshelve(shelf);
     ChunkWalk& w = k.w;
     const int rows = w.rows(a);
-    const bool pair = rows > 128;
+    const bool pair = PARTS == 0 && rows > 128;
     const int base = pair ? 128 * wg : 0;
     const bool there = base + r < rows;
-    const bool works = n > 0 && (pair || n > wg);  // this warpgroup had tiles
+    const bool works = n > 0;
     const bool begins = w.t0 == 0, ends = w.t1 == w.tiles;
     float* part = nullptr;
     if (!begins || !ends)
-      part = a.parts + (2LL * blockIdx.x + (begins ? 1 : 0)) * partial_floats(kChunkRows, D);
+      part = a.parts + (2LL * blockIdx.x + (begins ? 1 : 0)) * partial_floats(a.item_rows, D);
     if (!ends && begins && wg == 0 && r == 0)
       a.join[blockIdx.x] =
           join_item(w.b, w.hk, w.rb, rows, 1 + (w.tiles - w.t1 + k.share - 1) / k.share);
-    const bool two = !pair && n > 1;  // results of two warpgroups
+    const bool two = !pair;  // results of two warpgroups
     float* const s_m = reinterpret_cast<float*>(sgen + L::kOffStats);
     if (two && wg == 1) {
       s_m[r] = m_ref;
@@ -697,9 +937,7 @@ __device__ __forceinline__ void chunk_softmax_role(const CacheAttnArgs& a, const
           !wait_bounded_warp(bar(kCbOFull + wg), (k.flags >> wg) & 1u, ab, kStatusEpilogue))
         return;
       if (two) {
-        if (!(wait_bounded_warp(bar(kCbOFull + 1), (k.flags >> 1) & 1u, ab, kStatusEpilogue) &&
-              wait_bounded_warp(bar(kCbStats), (k.flags >> 2) & 1u, ab, kStatusEpilogue)))
-          return;
+        if (!wait_bounded_warp(bar(kCbStats), (k.flags >> 2) & 1u, ab, kStatusEpilogue)) return;
         const float m1 = s_m[r], l1 = s_m[128 + r];
         const float top = fmaxf(m_ref, m1);
         f0 = m_ref == -INFINITY ? 0.f : ptx::ex2(m_ref - top);
@@ -708,7 +946,7 @@ __device__ __forceinline__ void chunk_softmax_role(const CacheAttnArgs& a, const
         m_ref = top;
       }
       ptx::tc_fence_after();
-      const bool none = m_ref == -INFINITY;
+      const bool none = no_weight(m_ref, l);
       if (part == nullptr) {
         const float inv = none ? 0.f : 1.f / l;
         f0 *= inv;
@@ -719,13 +957,14 @@ __device__ __forceinline__ void chunk_softmax_role(const CacheAttnArgs& a, const
               none ? -INFINITY : (m_ref + log2f(l)) * 0.69314718055994531f;
         }
       } else if (there) {
-        part[kChunkRows * D + base + r] = m_ref;
-        part[kChunkRows * D + kChunkRows + base + r] = l;
+        part[a.item_rows * D + base + r] = m_ref;
+        part[a.item_rows * D + a.item_rows + base + r] = l;
       }
-      const uint32_t sQ = sbase + L::kOffQ + static_cast<uint32_t>((pair ? wg : 0) * L::kTileBytes);
+      const uint32_t sQ = sbase + L::kOffQ + static_cast<uint32_t>((pair ? wg : 0) * L::kQBytes);
       const uint32_t tO0 = tl + L::kColO + static_cast<uint32_t>(D) * wg;
       const unsigned long long* nan =
           reinterpret_cast<const unsigned long long*>(sgen + L::kOffNan) + (w.item & 7) * D;
+      const bool any_nan = *reinterpret_cast<const volatile uint32_t*>(sgen + L::kOffBar + kChunkSlotAnyNan) != 0u;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         float v[32];
@@ -745,12 +984,14 @@ __device__ __forceinline__ void chunk_softmax_role(const CacheAttnArgs& a, const
 #pragma unroll
           for (int e = 0; e < 32; ++e) v[e] = 0.f;
         }
+        if (any_nan) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const unsigned long long u = nan[32 * c + e];
-          if (static_cast<int>(u >> 32) == w.item + 1 &&
-              0x7FFFFFFF - static_cast<int>(u & 0xFFFFFFFFu) < lim)
-            v[e] = __int_as_float(0x7FFFFFFF);
+          for (int e = 0; e < 32; ++e) {
+            const unsigned long long u = nan[32 * c + e];
+            if (static_cast<int>(u >> 32) == w.item + 1 &&
+                0x7FFFFFFF - static_cast<int>(u & 0xFFFFFFFFu) < x.lim)
+              v[e] = __int_as_float(0x7FFFFFFF);
+          }
         }
         if (part == nullptr) {
           // through the Q tile, whose products are done: the rows' chunks, swizzled
@@ -765,7 +1006,7 @@ __device__ __forceinline__ void chunk_softmax_role(const CacheAttnArgs& a, const
         } else if (there) {
           // partial results column by column: neighbouring rows are neighbours
 #pragma unroll
-          for (int e = 0; e < 32; ++e) part[(32 * c + e) * kChunkRows + base + r] = v[e];
+          for (int e = 0; e < 32; ++e) part[(32 * c + e) * a.item_rows + base + r] = v[e];
         }
         __syncwarp();
       }
@@ -790,18 +1031,18 @@ __device__ __forceinline__ void chunk_softmax_role(const CacheAttnArgs& a, const
       if (!wait_bounded_warp(bar(kCbMerged), (k.flags >> 2) & 1u, ab, kStatusEpilogue)) return;
       ptx::tc_fence_after();
     }
-    if (n > 0) k.flags ^= 1u | (pair || n > 1 ? 2u : 0u) | (two ? 4u : 0u);
+    k.flags ^= (n > 0 ? 1u | (pair ? 2u : 0u) : 0u) | (two ? 4u : 0u);
     count += static_cast<uint32_t>(n);
     if (!w.next(a)) return;
     shelve(shelf, k, lane);
   }
 }
 
-template <int D, bool BF16>
+template <int D, bool BF16, int PARTS>
 __global__ void __launch_bounds__(kChunkThreads, 1)
     fa_cache_chunk_kernel(const __grid_constant__ CUtensorMap tm_k,
                           const __grid_constant__ CUtensorMap tm_v, const CacheAttnArgs a) {
-  using L = ChunkLayout<D>;
+  using L = ChunkLayout<D, PARTS>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = ptx::smem_u32(smem_raw);
   const uint32_t sbase = (raw + 1023u) & ~1023u;
@@ -827,6 +1068,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     ptx::mbar_init(bar(kCbStats), 128);
     ptx::mbar_init(bar(kCbMerged), 128);
     ptx::mbar_init(bar(kCbDrain), 1);
+    ptx::mbar_init(bar(kCbPSplit), 256);
+    ptx::mbar_init(bar(kCbPSplit + 1), 256);
+    ptx::mbar_init(bar(kCbOStep), 1);
     for (int i = 0; i < 16; ++i) ptx::mbar_init(bar(kCbScaleFull + i), 1);
     for (int i = 0; i < 8; ++i) ptx::mbar_init(bar(kCbVDone + i), 4);
     for (int i = 0; i < L::kStages; ++i) {
@@ -837,7 +1081,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       ptx::mbar_init(bar(kCbKVFull + 2 * L::kStages + i), 1);
       ptx::mbar_init(bar(kCbKVFull + 2 * L::kStages + L::kRaw + i), 4);
     }
+    for (int i = 0; i < 2 * L::kDirect; ++i)
+      ptx::mbar_init(bar(kCbKVFull + 2 * L::kStages + 2 * L::kRaw + i), 1);
     *abort_flag = 0u;
+    *reinterpret_cast<uint32_t*>(sgen + L::kOffBar + kChunkSlotAnyNan) = 0u;
     ptx::fence_mbar_init();
     a.join[blockIdx.x] = JoinItem{0, 0, 0, 0};
   }
@@ -908,15 +1155,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   const int wgrp = warp >> 2;
   if (wgrp == 0) {
     ptx::setmaxnreg_dec<kChunkRegsMma>();
-    if (warp == 0) chunk_mma_role<D>(a, w, sbase, bars, tmem, ab);
-    else if (warp == 1) chunk_copy_role<D>(&tm_k, &tm_v, a, w, sgen, sbase, bars, ab, lane);
+    if (warp == 0) chunk_mma_role<D, PARTS>(a, w, sbase, bars, tmem, ab);
+    else if (warp == 1) chunk_copy_role<D, PARTS>(&tm_k, &tm_v, a, w, sgen, sbase, bars, ab, lane);
   } else if (wgrp < 3) {
     ptx::setmaxnreg_inc<kChunkRegsSoftmax>();
-    chunk_softmax_role<D, BF16>(a, w, static_cast<int>(share), sgen, sbase, bars, tmem, ab, warp,
+    chunk_softmax_role<D, BF16, PARTS>(a, w, static_cast<int>(share), sgen, sbase, bars, tmem, ab, warp,
                                 lane);
   } else {
     ptx::setmaxnreg_dec<kChunkRegsConvert>();
-    chunk_convert_role<D>(a, w, sgen, sbase, bars, ab, warp, lane);
+    chunk_convert_role<D, PARTS>(a, w, sgen, sbase, bars, ab, warp, lane);
   }
   __syncwarp();
   ptx::tc_fence_before();

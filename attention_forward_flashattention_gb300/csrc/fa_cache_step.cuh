@@ -195,6 +195,10 @@ __device__ __forceinline__ float rows_to_f16(uint32_t (&w)[N]) {
   }
 }
 
+// Whether a row with the reference m and the sum l saw no key. (The maximum of
+// scores that are all NaN is -inf too, but their sum is NaN: that row is NaN.)
+__device__ __forceinline__ bool no_weight(float m, float l) { return m == -INFINITY && l == 0.f; }
+
 // Shared memory (all of it dynamic: a static array would be padded to the
 // ring's alignment).
 template <int D, int NT>
@@ -690,7 +694,7 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas(NT))
               part[kRows * D + kRows + rr] = sum;
             }
           } else {
-            const bool none = top == -INFINITY;
+            const bool none = no_weight(top, sum);
             const float inv = none ? 0.f : 1.f / sum;
             const int h = now.hk * a.group + j_q;
             *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) +
@@ -753,7 +757,7 @@ __device__ __forceinline__ void join_columns(const CacheAttnArgs& a, const JoinI
       for (int c = 0; c < kCols; ++c)
         o[c] = fmaf(__ldcg(q + (warp * kCols + c) * max_rows), f, o[c]);
     }
-    const float inv = m == -INFINITY ? 0.f : 1.f / l;
+    const float inv = no_weight(m, l) ? 0.f : 1.f / l;
 #pragma unroll
     for (int c = 0; c < kCols; ++c) s_rows[lane * kPitch + warp * kCols + c] = o[c] * inv;
   }
@@ -775,7 +779,7 @@ __device__ __forceinline__ void join_columns(const CacheAttnArgs& a, const JoinI
     const int i = static_cast<int>(row / a.group);
     const int h = it.hk * a.group + static_cast<int>(row - static_cast<long long>(i) * a.group);
     a.lse[lse_index(a, it.b, s, i, h)] =
-        m == -INFINITY ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+        no_weight(m, l) ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
   }
 }
 
@@ -849,7 +853,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2)
       }
     }
     if (r < rows && k == 0) {
-      const bool none = m == -INFINITY;
+      const bool none = no_weight(m, l);
       const float inv = none ? 0.f : 1.f / l;
       const long long row = static_cast<long long>(it.rb) * max_rows + r;
       const int i = static_cast<int>(row / a.group);

@@ -192,9 +192,11 @@ def test_append_old_scale_that_is_no_power_of_two():
 # ------------------------------------------------------------ attention
 
 def attention_case(lens, counts, H, heads, bs, d, dtype, causal, layout="head", uniform=False,
-                   seed=0, spoil=None, scale=None, q_mult=1.0, width=None, q_layout="thd"):
+                   seed=0, spoil=None, scale=None, q_mult=1.0, width=None, q_layout="thd",
+                   q_floor=0.0):
     """Runs fa_fwd_cache and compares it with the 64-bit implementation.
-    spoil(k codes, v codes, table): changes what the call must not see."""
+    spoil(k codes, v codes, table): changes what the call must not see. q_floor:
+    rounding of a query element, relative to the largest one of its row."""
     import torch
     rng = np.random.default_rng(seed)
     B = len(lens)
@@ -216,6 +218,10 @@ def attention_case(lens, counts, H, heads, bs, d, dtype, causal, layout="head", 
     scale = d ** -0.5 if scale is None else scale
     ref = U.attend(qv, codes_of(cache.k), codes_of(cache.v), ks.astype(np.float64),
                    vs.astype(np.float64), table, lens, cu, bs, scale, causal)
+    if q_floor:   # of a score: q_floor max |q| sum |k|
+        most = (np.abs(U.CODE_VALUES[codes_of(cache.k)]).sum(-1) * ks[:, :, None]).max()
+        far = ref[3] + scale * q_floor * np.abs(qv).max(-1) * most
+        ref = (ref[0], ref[1], ref[2], far, ref[4])
     if spoil is not None:
         spoil(cache, table, ids[at:])
     if uniform:
@@ -415,6 +421,58 @@ def test_wide_values_and_scales():
         else:
             assert np.all(np.abs(got - ref[0]) <= tol_o)
         assert np.all(np.abs(lse.double().cpu().numpy() - ref[1]) <= tol_l)
+
+
+@pytest.mark.parametrize("bs", [16, 32, 64, 128])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("causal", [True, False])
+def test_up_to_128_rows_on_average(bs, dtype, causal):
+    """Drafts beside pieces of more rows than one item holds, single tokens and
+    sequences without rows, 68 rows of a K / V head on average."""
+    lens = [900, 127, 0, 300, 64, 1290, 5, 33]
+    counts = [70, 5, 2, 33, 0, 17, 1, 8]
+    attention_case(lens, counts, 8, 2, bs, 128, dtype, causal, seed=bs)
+    attention_case([400, 129, 31], [20, 20, 20], 6, 1, bs, 128, dtype, causal, uniform=True, seed=bs + 1)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("n,top", [(20, 1.0), (20, 60.0), (20, 2.0 ** -12), (150, 60.0), (3, 60.0)])
+def test_queries_of_wide_range(dtype, n, top):
+    """Elements of a query that lie 2^20 apart: the small ones may be rounded to
+    2^-17 of the largest (half of the last part's smallest step, 2^-10, of a row
+    whose largest element is at least 2^7)."""
+    mult = top * np.exp2(-np.linspace(0, 20, 128)[np.random.default_rng(n).permutation(128)])
+    attention_case([n + 100, n, n + 259], [n] * 3, 6, 1, 32, 128, dtype, True, q_mult=mult,
+                   q_floor=2.0 ** -17)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("n,d,keys", [(24, 128, 253), (12, 64, 253), (24, 64, 253), (150, 128, 253),
+                                      (12, 128, 6000), (24, 128, 6000), (150, 128, 6000)])
+def test_queries_without_a_value(dtype, n, d, keys):
+    """Zero rows see the mean of V; rows with an infinity or NaN give NaN, and the
+    others are what they are without them."""
+    import torch
+    rng = np.random.default_rng(5)
+    H, bs = 2, 32
+    P = -(-keys // bs)
+    cache = make_cache(P, 2 if n == 12 else 1, bs, d, "head", rng)
+    table, lens = ints(rng.permutation(P)[None]), ints([keys])
+    q = torch.from_numpy(rng.standard_normal((n, H, d))).to(DEV).to(tdt(dtype))
+    clean, cl = fa.attention_forward_cache(q, cache, table, lens, ints([0, n]))
+    q[3] = 0
+    q[7, 0, 5], q[9, 1, 40], q[11, 0, d - 1] = float("inf"), float("nan"), -float("inf")
+    o, lse = fa.attention_forward_cache(q, cache, table, lens, ints([0, n]))
+    bad = torch.zeros(n, H, dtype=torch.bool, device=DEV)
+    bad[7, 0] = bad[9, 1] = bad[11, 0] = True
+    assert torch.isnan(o[bad]).all() and not torch.isfinite(lse[bad]).any()
+    good = ~bad
+    good[3] = False
+    assert torch.equal(o[good], clean[good]) and torch.equal(lse[good], cl[good])
+    seen = keys - n + 4
+    want = np.log(seen)
+    most = seen * 2.0 ** -24 + 2.0 ** -20 + 8 * 2.0 ** -24 * (want + 64)   # (attend_tolerance's)
+    assert np.all(np.abs(lse[3].cpu().numpy() - want) <= most)
 
 
 def test_long_sequences_split_and_joined():
