@@ -110,7 +110,8 @@ enum ChunkBar : int {
   kCbKVFull = 38,
 };
 constexpr int kChunkSlotTmem = 496, kChunkSlotAbort = 500, kChunkSlotStart = 504;
-constexpr int kChunkSlotAnyNan = 528, kChunkSlotHidden = 520;  // [raw] bytes: bit g: 16-key group g is hidden
+constexpr int kChunkSlotHidden = 520;  // [raw] bytes: bit g: 16-key group g is hidden
+constexpr int kChunkSlotAnyNan = 528;  // not 0: a converter has noted NaN
 
 // Keys that query token i of a sequence sees.
 __device__ __forceinline__ int keys_seen(const CacheAttnArgs& a, const SeqRows& s, int i) {
@@ -120,9 +121,8 @@ __device__ __forceinline__ int keys_seen(const CacheAttnArgs& a, const SeqRows& 
 // Row blocks of a sequence, and the tiles that one of them reads (counted: at
 // least one, so that rows without keys are written).
 __device__ __forceinline__ int chunk_row_blocks(const CacheAttnArgs& a, const SeqRows& s) {
-  return takes_seq(a, s) ? static_cast<int>(
-                               (static_cast<long long>(s.count) * a.group + a.item_rows - 1) / a.item_rows)
-                         : 0;
+  const long long rows = static_cast<long long>(s.count) * a.group;
+  return takes_seq(a, s) ? static_cast<int>((rows + a.item_rows - 1) / a.item_rows) : 0;
 }
 __device__ __forceinline__ int chunk_real_tiles(const CacheAttnArgs& a, const SeqRows& s, int rb) {
   const long long last = min((rb + 1LL) * a.item_rows, static_cast<long long>(s.count) * a.group) - 1;
@@ -293,7 +293,8 @@ __device__ __forceinline__ void chunk_copy_role(const CUtensorMap* tm_k, const C
       }
       if (!ok) break;
       if ((lane >> 3) == q)
-        s_scale[(count & 15) * 8 + (lane & 7)] = make_float4(sc.x, log2f(sc.y), ids >= 0 ? 1.f / sc.y : 0.f, 0.f);
+        s_scale[(count & 15) * 8 + (lane & 7)] =
+            make_float4(sc.x, log2f(sc.y), ids >= 0 ? 1.f / sc.y : 0.f, 0.f);
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(bar(kCbScaleFull + (count & 15)));
       ++count;
@@ -338,7 +339,8 @@ __device__ __forceinline__ void chunk_convert_role(const CacheAttnArgs& a, Chunk
   const uint32_t ch = static_cast<uint32_t>(2 * (c & 3)), x7 = static_cast<uint32_t>(r0 & 7);
   const uint32_t to0 = row_at + ((ch ^ x7) << 4), to1 = row_at + (((ch + 1u) ^ x7) << 4);
   unsigned long long* const s_nan = reinterpret_cast<unsigned long long*>(sgen + L::kOffNan);
-  volatile uint32_t* const s_any = reinterpret_cast<volatile uint32_t*>(sgen + L::kOffBar + kChunkSlotAnyNan);
+  volatile uint32_t* const s_any =
+      reinterpret_cast<volatile uint32_t*>(sgen + L::kOffBar + kChunkSlotAnyNan);
   const uint8_t* const s_hidden = sgen + L::kOffBar + kChunkSlotHidden;
   uint32_t ring = 0, count = 0;  // slots filled, tiles done
   bool ok = true;
@@ -641,8 +643,10 @@ __device__ __forceinline__ void query_parts(const uint16_t* p, float fac, uint32
 #pragma unroll
     for (int x = 0; x < 8; ++x) {
       float2 f;
-      if constexpr (BF16) f = make_float2(__uint_as_float(h[x] << 16), __uint_as_float(h[x] & 0xFFFF0000u));
-      else f = unpack_f16(h[x]);
+      if constexpr (BF16)
+        f = make_float2(__uint_as_float(h[x] << 16), __uint_as_float(h[x] & 0xFFFF0000u));
+      else
+        f = unpack_f16(h[x]);
       h[x] = pack_f16(f.x * inv, f.y * inv);
     }
 #pragma unroll
@@ -842,10 +846,10 @@ __device__ __forceinline__ void chunk_softmax_role(const CacheAttnArgs& a, const
       // (a warp without rows hands P over as it is: its rows of O are not read)
       x.idle = base + r - lane >= rows;
       if (n > 0) {
-        // this thread's row of Q into the swizzled layout. (A row for each thread, not 16 lanes to a row, which reads
-        // whole lines but has to loop over the rows: 2048 x 16384 chunk 387 us,
-        // drafts 70.6 us; 378 and 68.7 us so. Unrolled, its code alone took
-        // longer to fetch than the rows: 415 us.)
+        // this thread's row of Q into the swizzled layout. (A row for each thread,
+        // not 16 lanes to a row, which reads whole lines but has to loop over the
+        // rows: 2048 x 16384 chunk 387 us, 378 so. Unrolled, that loop's code alone
+        // took longer to fetch than the rows: 415 us.)
         const bool there = base + r < rows;
         const RowAt at = row_at(a, w, there ? base + r : 0);
         const uint16_t* p = static_cast<const uint16_t*>(a.q) + q_offset(a, w.b, w.s, at.i, at.head);
@@ -864,7 +868,8 @@ __device__ __forceinline__ void chunk_softmax_role(const CacheAttnArgs& a, const
           fac = e4m3_step<BF16>(max(top & 0xFFFFu, top >> 16));
           // each warpgroup writes half of the row
           if (there)
-            query_parts<D, BF16, PARTS>(p, fac, sbase + L::kOffQ, r, wg * (D / 32), (wg + 1) * (D / 32));
+            query_parts<D, BF16, PARTS>(p, fac, sbase + L::kOffQ, r, wg * (D / 32),
+                                        (wg + 1) * (D / 32));
         } else {
           uint32_t q[D / 2];
 #pragma unroll
@@ -964,7 +969,8 @@ __device__ __forceinline__ void chunk_softmax_role(const CacheAttnArgs& a, const
       const uint32_t tO0 = tl + L::kColO + static_cast<uint32_t>(D) * wg;
       const unsigned long long* nan =
           reinterpret_cast<const unsigned long long*>(sgen + L::kOffNan) + (w.item & 7) * D;
-      const bool any_nan = *reinterpret_cast<const volatile uint32_t*>(sgen + L::kOffBar + kChunkSlotAnyNan) != 0u;
+      const bool any_nan = *reinterpret_cast<const volatile uint32_t*>(sgen + L::kOffBar +
+                                                                       kChunkSlotAnyNan) != 0u;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         float v[32];

@@ -149,8 +149,12 @@ fa_status fa_cache_append(const void* k, const void* v, const fa_strides* stride
  * Scores, softmax sums and O are formed in fp32 from the exact products of
  * 16-bit queries and 8-bit codes; the weights are rounded to fp16 (relative
  * 2^-11 at most) for the product with V, whatever `dtype` is, but kept in two
- * such parts for FA_DTYPE_FP16 and up to 16 rows to a K / V head. V scales of
- * one sequence may differ by a factor of up to 2^100.
+ * such parts for FA_DTYPE_FP16 and up to 16 rows to a K / V head. With d = 128
+ * and 17 to 128 rows to a K / V head (on average over the sequences) query
+ * elements below 2^-6 of their row's largest (bf16: 2^-9) may be rounded, by
+ * 2^-17 of that largest one at most. A query row that holds an infinity or NaN
+ * gives NaN wherever its scores are. V scales of one sequence may differ by a
+ * factor of up to 2^100.
  * Up to three launches (a kernel for sequences of up to 16 rows to a K / V
  * head, one for more, and one that joins what they split), by the sizes that
  * the host knows. Deterministic: the same call gives the same bits.
