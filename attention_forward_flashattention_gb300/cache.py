@@ -159,8 +159,8 @@ def cache_plan(lens, new_lens, block_table, free_blocks, free_pos, n_tokens: int
     lens[b]: writes the block table entries that they open and returns (slots
     [n_tokens], cu_new [B + 1], kv_lens [B], free_next [1]), int32. n_tokens is
     the number of rows to plan, at least the sum of new_lens (slots behind the
-    last token are -1). Requests that cannot be served keep their length and
-    get slots -1 (see fa_cache.h)."""
+    last token are -1), parts of one allocation. Requests that cannot be served
+    keep their length and get slots -1 (see fa_cache.h)."""
     r = (_native or _module()).cache_plan(lens, new_lens, block_table, free_blocks, free_pos, None,
                                           n_tokens, block, stream)
     if type(r) is int:
