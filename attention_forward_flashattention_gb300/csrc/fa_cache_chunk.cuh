@@ -40,8 +40,8 @@
 //
 // What bounds it. Pair mode: the chain S - softmax - P V - S of each Q tile, as in
 // the forward kernel of whole matrices; tensor memory is full, so S has no second
-// buffer. 2048 tokens behind 14336 others, 32 heads of d 128 on 8: 375 us, 1.37
-// PFLOP/s (71 % of a matrix product's burst rate), tensor pipe active 61 %. Split
+// buffer. 2048 tokens behind 14336 others, 32 heads of d 128 on 8: 369 us, 1.40
+// PFLOP/s (72 % of a matrix product's burst rate), tensor pipe active 61 %. Split
 // mode: 16 x 40 rows, 4 K / V heads, 8192 keys: 59 us (with all of K widened, too,
 // and whole tiles for each warpgroup 69 us); a KV tile takes 2400 cycles, 1700 of
 // them the MMAs (shared-memory traffic, 208 KB a tile) and 1700 a

@@ -735,6 +735,10 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas(NT))
 // by the time of that search, 3 us.)
 constexpr int kJoinThreads = 256;
 constexpr int kJoinRows = 32;
+// Blocks on an SM. Their loads from L2 are what takes time: four in 64 registers
+// each, 2048 x 16384 chunk 369.5 us, chunks beside single tokens 38.8; two in 128,
+// 374.5 and 40.2; five in 48, 371 and 39.1.
+constexpr int kJoinBlocks = 4;
 
 // The chunk kernel's partial results lie column by column ([D][max_rows], then m
 // and l): a lane takes a row, a warp D / 8 of its columns, and the joined rows
@@ -789,7 +793,7 @@ __device__ __forceinline__ void join_columns(const CacheAttnArgs& a, const JoinI
 }
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kJoinThreads, 2)
+__global__ void __launch_bounds__(kJoinThreads, kJoinBlocks)
     fa_cache_join_kernel(const CacheAttnArgs a, const JoinSides sides) {
   constexpr int kWarps = kJoinThreads / 32, kPer = D / 32;
   __shared__ float s_rows[kJoinRows * (D + 4)];
