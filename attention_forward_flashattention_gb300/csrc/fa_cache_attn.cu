@@ -35,8 +35,13 @@ AttnPlan plan_attn(int B, int T, int group, bool ragged) {
     p.chunk = true;
   } else {
     // a batch of single tokens and longer pieces, in a mixture that only the
-    // device knows: each sequence goes to the kernel of its size
-    p.nt = 2;
+    // device knows: each sequence goes to the kernel of its size. Single tokens are
+    // faster on the instance of 8 rows; pieces of 9 to 16 rows, two items there, are
+    // slower. So it is taken where no draft of up to four tokens has so many rows, or
+    // one of two tokens alone. D 128, us on 8 rows / on 16, beside chunks of 300 to 512
+    // tokens: 63 single tokens, 8 query heads to a K / V head 117 / 125, 4 heads
+    // 151 / 157; 60 drafts of two tokens, 8 heads 134 / 130, of three, 4 heads 227 / 173.
+    p.nt = group <= 2 || (group > 4 && group <= 8) ? 1 : 2;
     p.chunk = true;
     p.upto = kStepMaxRows;
   }

@@ -283,6 +283,15 @@ def test_mixed_batches(d, dtype, H, heads, bs):
     attention_case(lens, counts[::-1], H, heads, bs, d, dtype, False, seed=d + H + 1)
 
 
+@pytest.mark.parametrize("group", [1, 2, 3, 4, 5, 8, 9])
+@pytest.mark.parametrize("d,dtype", [(128, "fp16"), (64, "bf16")])
+def test_mixed_batches_of_few_rows(group, d, dtype):
+    """Pieces of every number of rows around 8 and 16 beside a chunk."""
+    counts = sorted({n for r in (1, 7, 8, 9, 15, 16, 17) for n in (r // group, -(-r // group)) if n})
+    lens = [40 * n + 3 for n in counts] + [170, 0]
+    attention_case(lens, counts + [150, 1], 2 * group, 2, 32, d, dtype, True, seed=group)
+
+
 @pytest.mark.parametrize("lens,counts", [([3, 0, 40], [10, 1, 45]), ([1], [300])])
 def test_rows_before_the_first_key(lens, counts):
     """More query rows than keys: the first rows see nothing."""
