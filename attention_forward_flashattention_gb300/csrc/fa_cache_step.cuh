@@ -31,7 +31,7 @@
 //
 // Measured, all launches: two sequences of 131071 keys, 32 heads on 8, d 128: 95 us
 // (5.7 TB/s, 85 % of a copy's rate); 96 sequences of up to 16384 keys, the same
-// heads: 236 us (5.8 TB/s); four of 4096 keys, 16 heads: 22.8 us, 3 of them the
+// heads: 236 us (5.8 TB/s); four of 4096 keys, 16 heads: 21.4 us, 3 of them the
 // join. What bounds it stands at step_ctas.
 #pragma once
 
@@ -62,6 +62,22 @@ __host__ __device__ constexpr int step_keys(int d) { return kStepTileBytes / d; 
 
 // Floats of a partial result of `rows` rows: O, m, l.
 __host__ __device__ constexpr int partial_floats(int rows, int d) { return rows * (d + 2); }
+
+// The first sequence from b on that a launch computes, or -1. Called by whole
+// warps, which look at 32 sequences at a time: a large batch may have many of the
+// other launch's, or without rows, in a row. (The chunk kernel, whose sequences
+// are the long ones, looks at them one by one: there the search's code alone
+// cost 5 %.)
+__device__ __forceinline__ int next_taken(const CacheAttnArgs& a, int b) {
+  if (a.cu_q == nullptr) return -1;  // all sequences alike
+  const int lane = static_cast<int>(threadIdx.x & 31);
+  for (; b < a.B; b += 32) {
+    const bool taken = b + lane < a.B && takes_seq(a, seq_rows(a, b + lane));
+    const uint32_t mask = __ballot_sync(0xffffffffu, taken);
+    if (mask != 0u) return b + __ffs(static_cast<int>(mask)) - 1;
+  }
+  return -1;
+}
 
 // Position of a CTA's share in the list of tiles. An item with no keys counts
 // as one (empty) tile, so that its rows are written.
@@ -105,7 +121,7 @@ struct StepWalk {
     left = n;
     t1 = static_cast<int>(min(static_cast<long long>(tiles), t0 + left));
   }
-  // To the next item; false if the share ends.
+  // To the next item; false if the share ends. Called by whole warps.
   __device__ __forceinline__ bool next(const CacheAttnArgs& a, int rows, bool whole) {
     left -= t1 - t0;
     if (left <= 0) return false;
@@ -113,10 +129,13 @@ struct StepWalk {
       rb = 0;
       if (++hk == a.Hkv) {
         hk = 0;
-        do {
-          ++b;
+        ++b;
+        load(a, rows, whole);
+        if (n_rb == 0) {
+          b = next_taken(a, b + 1);
+          if (b < 0) return false;  // (no tiles are left then)
           load(a, rows, whole);
-        } while (n_rb == 0);  // ends: tiles are left
+        }
       }
     }
     t0 = 0;
