@@ -316,7 +316,7 @@ def test_codes_and_blocks_out_of_sight(n, H, heads, d):
     attention_case([n + 50, n, n + 200], [n] * 3, H, heads, 32, d, "fp16", True, spoil=spoil)
 
 
-@pytest.mark.parametrize("n,H", [(3, 2), (20, 8), (150, 2)])
+@pytest.mark.parametrize("n,H", [(3, 2), (20, 4), (20, 8), (150, 2)])
 @pytest.mark.parametrize("d", [64, 128])
 def test_nan_reaches_the_rows_that_see_it(n, H, d):
     """A key whose V holds NaN in one column: the rows that see the key get NaN
@@ -441,7 +441,9 @@ def test_up_to_128_rows_on_average(bs, dtype, causal):
     lens = [900, 127, 0, 300, 64, 1290, 5, 33]
     counts = [70, 5, 2, 33, 0, 17, 1, 8]
     attention_case(lens, counts, 8, 2, bs, 128, dtype, causal, seed=bs)
-    attention_case([400, 129, 31], [20, 20, 20], 6, 1, bs, 128, dtype, causal, uniform=True, seed=bs + 1)
+    attention_case([400, 129, 31], [20, 20, 20], 6, 1, bs, 128, dtype, causal, uniform=True,
+                   seed=bs + 1)
+    attention_case([0, 60, 0, 7, 200], [20, 20, 33, 30, 25], 2, 2, bs, 128, dtype, causal, seed=bs + 2)
 
 
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
@@ -647,7 +649,7 @@ def test_serving_loop_on_streams_and_twice():
         assert torch.equal(c.v_scales, c0.v_scales)
 
 
-@pytest.mark.parametrize("n,H,heads,d", [(1, 8, 2, 128), (40, 4, 1, 64)])
+@pytest.mark.parametrize("n,H,heads,d", [(1, 8, 2, 128), (40, 4, 1, 64), (5, 16, 2, 128)])
 def test_graph_replays_a_step(n, H, heads, d):
     """One step captured (plan, append, attention), replayed on new lengths and
     values, against direct calls."""
@@ -845,3 +847,34 @@ def test_binding_refusals():
     fa.cache_append(x[:0], x[:0], i3[:0], c)
     o, lse = fa.attention_forward_cache(q[:0], c, tab, lens, ints([0, 0, 0, 0]))
     assert o.shape == (0, 4, 64) and lse.shape == (0, 4)
+
+
+def test_drafts_on_streams_and_at_a_largest_batch():
+    """Drafts of 40 rows at once on several streams, bit for bit what they give alone;
+    and 3000 sequences, of which every fifth has rows."""
+    import torch
+    rng = np.random.default_rng(21)
+    H, heads, d, bs, B = 16, 2, 128, 32, 6
+    lens = rng.integers(5, 900, B)
+    need = -(-lens // bs)
+    P = int(need.sum())
+    cache = make_cache(P, heads, bs, d, "head", rng)
+    table = np.full((B, int(need.max())), -1)
+    ids, at = rng.permutation(P), 0
+    for b in range(B):
+        table[b, :need[b]] = ids[at:at + need[b]]
+        at += need[b]
+    tab, ln, cu = ints(table), ints(lens), ints(np.arange(B + 1) * 5)
+    qs = [torch.randn(5 * B, H, d, device=DEV).to(tdt(t)) for t in ("fp16", "bf16") * 3]
+    alone = [fa.attention_forward_cache(q, cache, tab, ln, cu) for q in qs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in qs]
+    for _ in range(3):
+        got = [fa.attention_forward_cache(q, cache, tab, ln, cu, stream=st)
+               for q, st in zip(qs, streams)]
+        torch.cuda.synchronize()
+        for (o, lse), (o1, l1) in zip(got, alone):
+            assert torch.equal(o, o1) and torch.equal(lse, l1)
+    counts = np.where(np.arange(3000) % 5 == 0, np.arange(3000) % 23, 0)
+    lens = np.where(counts > 0, counts + np.arange(3000) % 40, np.arange(3000) % 2)
+    attention_case(list(lens), list(counts), 2, 1, 32, 128, "bf16", True, seed=4)
