@@ -749,7 +749,8 @@ __device__ __forceinline__ bool softmax_tiles(const CacheAttnArgs& a, const Tile
       }
     }
     float alpha = 1.f;
-    if (m_tile > m_ref + 8.f) {
+    if (m_tile > m_ref + kWeightMost) {
+      m_tile -= kWeightLift;
       alpha = ptx::ex2(m_ref - m_tile);  // (0 for the first visible tile)
       m_ref = m_tile;
     }
@@ -766,7 +767,7 @@ __device__ __forceinline__ bool softmax_tiles(const CacheAttnArgs& a, const Tile
       for (int c = 0; c < 8; ++c) {
         const float2 t = ptx::ffma2(make_float2(s[16 * g + 2 * c], s[16 * g + 2 * c + 1]), f2, a2);
         const float p0 = ptx::ex2(t.x), p1 = ptx::ex2(t.y);
-        pk[g >> 2][(g & 3) * 8 + c] = pack_f16(p0, p1);
+        pk[g >> 2][(g & 3) * 8 + c] = pack_weights(p0, p1);
         if (c & 1) sum1 = ptx::fadd2(sum1, make_float2(p0, p1));
         else sum0 = ptx::fadd2(sum0, make_float2(p0, p1));
       }

@@ -21,9 +21,15 @@
 // ks, vs of the key's block,
 //     e_j = c ks (q . k8_j) + log2 vs,   P'_j = 2^(e_j - m),
 //     O = sum P'_j v8_j / sum (P'_j / vs),   LSE = ln 2 (m + log2 sum (P'_j / vs)),
-// so V is used as stored, and the reference m follows the weights as they meet
-// V: a block of large values does not push another one's weights below fp16.
-// m moves (and O, l are rescaled) only when an e_j exceeds it by more than 8.
+// so V is used as stored. P' goes into the product as fp16, whose values have 11
+// bits from 2^-14 on, and below that a step of 2^-24; l and the reference m are
+// fp32. So that little of a small weight is lost, m is kept kWeightLift below
+// the e that it was taken from, near the top of fp16's range: with W = max w_j
+// vs_j (w the softmax weights), w vs is off by at most 2^-11 of itself (half a step
+// of 11 bits), or, where it is below 2^-22 W, by 2^-33 W. m moves (and O, l are
+// rescaled) only when an e_j exceeds it by more than kWeightMost.
+// Not m at the largest e itself: there a weight of 2^-14 W loses bits and one of
+// 2^-25 W all, which l, the sum of the unrounded weights, would still count.
 //
 // Splitting: the items' tiles form one list, cut into equal shares for the
 // persistent CTAs (two or three on each SM). A share that begins or ends inside an item
@@ -56,6 +62,14 @@ __host__ __device__ constexpr int step_ctas(int nt) { return nt == 1 ? 3 : 2; }
 __host__ __device__ constexpr int step_stages(int nt) { return nt == 1 ? 2 : 3; }
 constexpr int kStepTileBytes = 4096;  // of K, and of V
 constexpr int kStepMaxRows = 16;      // rows of an item: 8 NT, NT = 1 or 2
+
+// P' = 2^(e - m) is at most fp16's largest power of two, and m is taken so far
+// below the largest e. The closer the two, the more of small weights is kept, and
+// the oftener m moves: us of the chunk kernel with m 0 / 7 / 8 / 9 / 11 below, P' at
+// most 2^8 / 2^15 ..: 2048 x 16384 chunk 371.4 / 371.9 / 373.3 / 374.4 / 376.8, drafts
+// 59.5 / 59.7 / 59.7 / 59.8 / 60.6 (few rows: no difference).
+constexpr float kWeightMost = 15.f;
+constexpr float kWeightLift = 8.f;
 
 // Keys of a tile.
 __host__ __device__ constexpr int step_keys(int d) { return kStepTileBytes / d; }
@@ -187,6 +201,14 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
 
 // Two fp32 values as fp16, lo in the low half.
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) { return pack2<false>(lo, hi); }
+
+// Two weights as fp16. Where scores are so large that the exponent's fp32 steps are
+// whole numbers, one may pass fp16's range: it becomes the largest number, not infinity.
+__device__ __forceinline__ uint32_t pack_weights(float lo, float hi) {
+  uint32_t u;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %2, %1;" : "=r"(u) : "f"(lo), "f"(hi));
+  return u;
+}
 
 __device__ __forceinline__ float2 unpack_f16(uint32_t w) {
   __half2 h;
@@ -538,7 +560,7 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas(NT))
       bool grow = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
-        grow = grow || top[nt][0] > m[nt][0] + 8.f || top[nt][1] > m[nt][1] + 8.f;
+        grow = grow || top[nt][0] > m[nt][0] + kWeightMost || top[nt][1] > m[nt][1] + kWeightMost;
       if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -547,7 +569,7 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas(NT))
             float v = top[nt][h];
 #pragma unroll
             for (int x = 4; x < 32; x <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, x));
-            const float ref = fmaxf(m[nt][h], v);
+            const float ref = fmaxf(m[nt][h], v - kWeightLift);
             const float keep = ref == -INFINITY ? 1.f : ptx::ex2(m[nt][h] - ref);
             m[nt][h] = ref;
             l[nt][h] *= keep;
@@ -573,7 +595,7 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas(NT))
           const float p2 = ptx::ex2(s[u][nt][2] - n0), p3 = ptx::ex2(s[u][nt][3] - n1);
           l[nt][0] = fmaf(p0 + p2, iv[u], l[nt][0]);
           l[nt][1] = fmaf(p1 + p3, iv[u], l[nt][1]);
-          const uint32_t h0 = pack_f16(p0, p1), h1 = pack_f16(p2, p3);
+          const uint32_t h0 = pack_weights(p0, p1), h1 = pack_weights(p2, p3);
           p[u][nt][0] = transpose_8x8(h0);
           p[u][nt][1] = transpose_8x8(h1);
           if constexpr (!BF16) {

@@ -147,9 +147,13 @@ fa_status fa_cache_append(const void* k, const void* v, const fa_strides* stride
  *               aligned; overwritten, and not to be used by another call at
  *               the same time. Nothing is kept in it between calls.
  * Scores, softmax sums and O are formed in fp32 from the exact products of
- * 16-bit queries and 8-bit codes; the weights are rounded to fp16 (relative
- * 2^-11 at most) for the product with V, whatever `dtype` is, but kept in two
- * such parts for FA_DTYPE_FP16 and up to 16 rows to a K / V head. With d = 128
+ * 16-bit queries and 8-bit codes. For the product with V, whatever `dtype` is,
+ * the weights w_j = exp(score) times V's scale are rounded to fp16's 11 bits: by
+ * at most 2^-11 of themselves, or by 2^-33 W where they are below 2^-22 W, W the
+ * largest of them in the row. (So a column of O that lives on keys far below the
+ * row's largest, or on blocks of a far smaller V scale, is off by up to 2^-33 W
+ * sum |code| / sum w.) For FA_DTYPE_FP16 and up to 16 rows to a K / V head they
+ * are kept in two such parts: 2^-22 of themselves, or 2^-33 W. With d = 128
  * and 17 to 128 rows to a K / V head (on average over the sequences) query
  * elements below 2^-6 of their row's largest (bf16: 2^-9) may be rounded, by
  * 2^-17 of that largest one at most. A query row that holds an infinity or NaN

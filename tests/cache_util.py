@@ -152,3 +152,73 @@ def attend_tolerance(ref, eps, keys):
     lf = np.where(np.isfinite(L), np.abs(L), 0.0)
     tol_l = far + keys * 2.0 ** -24 + 2.0 ** -20 + 8 * 2.0 ** -24 * (lf + 64)
     return tol_o, tol_l
+
+
+def attend_columns(q, k, v, ks, vs, table, kv_lens, cu, bs, scale, causal, eps, two_parts=False,
+                   q_floor=0.0):
+    """float64 attention with bounds on the error of every single result, from the
+    terms that it is made of. Arguments as in attend; eps: of the results' type;
+    two_parts: weights kept as two fp16 values; q_floor: rounding of a query
+    element, relative to the largest one of its row. Returns (O, LSE, tol_O, tol_LSE).
+
+    With w_j = exp(s_j), W = max w_j vs_j and L = sum w_j:
+    - a weight's relative error r_j: the score's fp32 sum, (d + 3) 2^-24 scale
+      sum |k q| and q_floor's share; the fp32 exponent c s + log2 vs - m, 2^-23 of
+      the magnitudes that it is formed of, and 2^-22 of log2 vs; 2^-20 for the
+      exponential and the scales' reciprocal. It enters numerator and L.
+    - its rounding for the product with V: 2^-11 of itself (two parts: 2^-22), or
+      2^-33 W where that is more (both kernels' references lie 2^-8 or more below the
+      largest weight, and fp16's half step below its normal range is 2^-25).
+    - the fp32 sums over the keys: 2^-24 for each of them in numerator and L, 2^-14
+      at most (a share of the keys is summed by itself, by MMAs of 16 keys).
+    - O is rounded to its type once; fp16 has a fixed step of 2^-24 below 2^-14."""
+    T, H, d = q.shape
+    P, heads = ks.shape
+    g = H // heads
+    O, tol_o = np.zeros((T, H, d)), np.full((T, H, d), 1e-300)
+    L, tol_l = np.full((T, H), -np.inf), np.zeros((T, H))
+    width = table.shape[1] * bs
+    part = 2.0 ** -22 if two_parts else 2.0 ** -11
+    for b, length in enumerate(kv_lens):
+        length = min(max(int(length), 0), width)
+        n = cu[b + 1] - cu[b]
+        at = np.arange(length)
+        ids = table[b, at // bs] if length else np.zeros(0, dtype=np.int64)
+        seen = (ids >= 0) & (ids < P)
+        safe = np.where(seen, ids, 0)
+        for h in range(heads):
+            kk = CODE_VALUES[k[safe, h, at % bs]] * ks[safe, h][:, None]
+            vc = CODE_VALUES[v[safe, h, at % bs]]
+            sv = vs[safe, h]
+            for i in range(n):
+                lim = min(length, length - n + i + 1) if causal else length
+                keep = np.flatnonzero(seen[:max(lim, 0)])
+                if keep.size == 0:
+                    continue
+                kj, vj, sj = kk[keep], vc[keep], sv[keep]
+                lv = np.log2(sj)
+                sums = min(keep.size * 2.0 ** -24, 2.0 ** -14)
+                for j in range(g):
+                    t, head = cu[b] + i, h * g + j
+                    x = q[t, head]
+                    s = kj @ x * scale
+                    e = s * math.log2(math.e) + lv
+                    r = ((d + 3) * 2.0 ** -24 * scale * (np.abs(kj) @ np.abs(x))
+                         + q_floor * scale * np.abs(x).max() * np.abs(kj).sum(-1)
+                         + math.log(2) * (2.0 ** -23 * (np.abs(e) + np.abs(lv) + np.abs(e.max()) + 11)
+                                          + 2.0 ** -22 * np.abs(lv))
+                         + 2.0 ** -20)
+                    w = np.exp(s - s.max())
+                    tot = w.sum()
+                    u = w * sj                       # what a code is multiplied by
+                    O[t, head] = u @ vj / tot
+                    L[t, head] = s.max() + math.log(tot)
+                    rl = (w * np.expm1(r)).sum() / tot + sums
+                    du = np.maximum(u * part, 2.0 ** -33 * u.max()) + u * (np.expm1(r) + sums)
+                    tol_o[t, head] += (du @ np.abs(vj) / tot + np.abs(O[t, head]) * rl) * (1 + eps)
+                    tol_o[t, head] += np.abs(O[t, head]) * eps / 2
+                    # LSE = ln 2 (m + log2 l): fp32, and log2's own error
+                    tol_l[t, head] = rl + 2.0 ** -22 * (np.abs(L[t, head]) + np.abs(e.max()) + 64)
+    if eps == 2.0 ** -10:
+        tol_o += 2.0 ** -25
+    return O, L, tol_o, tol_l

@@ -1,0 +1,127 @@
+"""The block cache's attention judged result by result: every element of O
+against a bound made of that element's own terms (cache_util.attend_columns), so
+that weights far below a row's largest one, lost partial results and wrong
+columns show beside large neighbours."""
+import numpy as np
+import pytest
+
+import attention_forward_flashattention_gb300 as fa
+import cache_util as U
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+# rows to the one K / V head, head dimension: the step kernel's two instances, and
+# the chunk kernel on items of 128 rows (d = 128: queries in 8-bit parts; d = 64) and 256
+KERNELS = [(1, 64), (1, 128), (12, 64), (12, 128), (24, 64), (24, 128), (150, 64), (150, 128)]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    import torch
+    torch.cuda.init()
+    fa.build.build()
+    fa.load_library()
+
+
+def ints(v):
+    import torch
+    return torch.tensor(np.asarray(v), dtype=torch.int32, device=DEV)
+
+
+def tdt(name):
+    import torch
+    return torch.float16 if name == "fp16" else torch.bfloat16
+
+
+def to_cache(k, v, ks, vs):
+    import torch
+    return fa.Cache(*(torch.from_numpy(np.ascontiguousarray(x)).to(DEV) for x in (k, v)),
+                    *(torch.from_numpy(np.asarray(x, dtype=np.float32)).to(DEV) for x in (ks, vs)))
+
+
+def two_parts(rows, dtype):
+    """Whether a call of so many rows to a K / V head keeps its weights in two fp16 parts."""
+    return dtype == "fp16" and rows <= 16
+
+
+def compare(q, cache, table, lens, cu, causal=True, scale=None, dtype="bf16", two=False, q_floor=0.0):
+    """Runs the call and judges every element of O and LSE. q: CUDA tensor [T, H, d]."""
+    import torch
+    d, bs = q.shape[2], cache.k.shape[2]
+    scale = d ** -0.5 if scale is None else scale
+    o, lse = fa.attention_forward_cache(q, cache, ints(table), ints(lens), ints(cu), causal, scale)
+    assert fa.fa_check(0) == fa.FA_OK
+    host = [c.view(torch.uint8).cpu().numpy() for c in cache[:2]]
+    O, L, tol_o, tol_l = U.attend_columns(
+        q.double().cpu().numpy(), *host, *(s.double().cpu().numpy() for s in cache[2:]),
+        np.asarray(table), lens, cu, bs, scale, causal, torch.finfo(tdt(dtype)).eps, two, q_floor)
+    got, gl = o.double().cpu().numpy(), lse.double().cpu().numpy()
+    empty = np.isneginf(L)
+    assert np.array_equal(np.isneginf(gl), empty) and np.all(got[empty] == 0)
+    err = np.abs(got - O)
+    assert np.all(err <= tol_o), f"O: {np.max(err / tol_o):.2f} of the bound"
+    le = np.abs(gl - L)[~empty] / tol_l[~empty]
+    assert np.all(le <= 1), f"LSE: {np.max(le):.2f} of the bound"
+    return o, lse
+
+
+def codes(values, shape):
+    return U.encode(np.broadcast_to(np.asarray(values, dtype=np.float64), shape))
+
+
+# ------------------------------------------------------------ weights far below the largest one
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("n,d", KERNELS)
+@pytest.mark.parametrize("apart", [8, 18, 24, 26])
+def test_small_scale_block_beside_a_large_one(n, d, dtype, apart):
+    """Two blocks of 16 keys that follow each other eight times, with equal scores, V
+    scales 2^apart and 1. Columns below 32 are zero in the block of the large scale:
+    there O is half of the other block's 256, although its weights are 2^-apart of
+    the large ones."""
+    import torch
+    bs = 16
+    k = np.zeros((2, 1, bs, d), np.uint8)
+    big = np.where(np.arange(d) < 32, 0.0, 1.0)
+    v = np.stack([codes(big, (1, bs, d)), codes(256.0, (1, bs, d))])
+    cache = to_cache(k, v, np.ones((2, 1)), [[2.0 ** apart / (4096.0 if dtype == "fp16" else 1.0)],
+                                             [1.0 / (4096.0 if dtype == "fp16" else 1.0)]])
+    q = torch.randn(n, 1, d, device=DEV).to(tdt(dtype))
+    o, _ = compare(q, cache, [[0, 1] * 8], [256], [0, n], False, dtype=dtype, two=two_parts(n, dtype))
+    assert torch.all(o[:, :, :32] != 0)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("n,d", KERNELS)
+@pytest.mark.parametrize("nats", [10.0, 18.0])
+def test_many_small_weights_beside_one_large(n, d, dtype, nats):
+    """20000 keys of V = 1 and one, `nats` ahead of them, of V = 0: O is the share
+    of the many, 20000 e^-nats / (1 + 20000 e^-nats)."""
+    import torch
+    bs, keys = 64, 20001
+    P = -(-keys // bs)
+    k = np.zeros((P, 1, bs, d), np.uint8)
+    v = codes(1.0, (P, 1, bs, d)).copy()
+    k[P // 2, 0, 7, 0] = U.encode(np.array([1.0]))[0]
+    v[P // 2, 0, 7] = 0
+    cache = to_cache(k, v, np.ones((P, 1)), np.ones((P, 1)))
+    q = torch.zeros(n, 1, d, device=DEV, dtype=tdt(dtype))
+    q[:, :, 0] = nats
+    compare(q, cache, np.arange(P)[None], [keys], [0, n], False, 1.0, dtype, two_parts(n, dtype))
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("n,d", KERNELS)
+def test_random_values_column_by_column(n, d, dtype):
+    """Normal values, sharp scores, scales 2^-12 to 1 apart, ragged keys."""
+    import torch
+    rng = np.random.default_rng(n + d)
+    bs, keys = 32, n + 603
+    P = -(-keys // bs)
+    k, v = (U.encode(rng.standard_normal((P, 1, bs, d)) * 64) for _ in range(2))
+    cache = to_cache(k, v, np.exp2(rng.integers(-7, -4, (P, 1))), np.exp2(rng.integers(-12, 1, (P, 1))))
+    q = torch.from_numpy(rng.standard_normal((n, 1, d)) * 2).to(DEV).to(tdt(dtype))
+    floor = 2.0 ** -17 if d == 128 and 16 < n <= 128 else 0.0
+    compare(q, cache, rng.permutation(P)[None], [keys], [0, n], True, None, dtype,
+            two_parts(n, dtype), floor)
