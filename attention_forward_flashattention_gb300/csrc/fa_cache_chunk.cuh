@@ -665,6 +665,17 @@ __device__ __forceinline__ void query_parts(const uint16_t* p, float fac, uint32
   }
 }
 
+// Whether row limit `lim` leaves a key of a block that exists in the share's tiles.
+__device__ __forceinline__ bool meets_a_key(const CacheAttnArgs& a, const ChunkWalk& w, int lim) {
+  const long long end = min(static_cast<long long>(lim), 1LL * w.real_end * kChunkKeys);
+  const int32_t* const table = a.table + static_cast<long long>(w.b) * a.table_width;
+  for (long long key = 1LL * w.t0 * kChunkKeys; key < end; key += 1LL << a.block_shift) {
+    const int id = __ldg(table + (key >> a.block_shift));
+    if (id >= 0 && id < a.num_blocks) return true;
+  }
+  return false;
+}
+
 // The tiles of one item for a warpgroup: NC = 128, all keys of a tile for the rows
 // of Q tile `wg` (pair mode), or NC = 64, half `wg` of the keys (split mode).
 // S of tile j is in S_wg, or in that half of S_(j mod 2); P goes over it.
@@ -882,6 +893,7 @@ __device__ __forceinline__ void chunk_softmax_role(const CacheAttnArgs& a, const
             q[4 * e + 2] = v.z;
             q[4 * e + 3] = v.w;
           }
+          if constexpr (!BF16) inf_to_nan<D / 2>(q);
           fac = rows_to_f16<D / 2, 1, BF16>(q);
           if (pair || wg == 0) {
             const uint32_t to = sbase + L::kOffQ +
@@ -893,7 +905,10 @@ __device__ __forceinline__ void chunk_softmax_role(const CacheAttnArgs& a, const
                                 q[4 * e], q[4 * e + 1], q[4 * e + 2], q[4 * e + 3]);
           }
         }
-        x.crow *= fac;
+        // (so that c ks does not underflow to 0, and -inf times it to NaN, for a hidden
+        // key: at 2^-80 the scores are nothing, S being 2^32 at most. A row without a
+        // value has NaN in Q, and a factor that leaves its hidden keys hidden.)
+        x.crow = fmaxf(x.crow * fac, 0x1p-80f);
         if (PARTS > 0 || pair || wg == 0) {
           ptx::fence_proxy_async_smem();
           ptx::mbar_arrive(bar(kCbQFull + wg));
@@ -952,6 +967,12 @@ __device__ __forceinline__ void chunk_softmax_role(const CacheAttnArgs& a, const
         m_ref = top;
       }
       ptx::tc_fence_after();
+      // scores of NaN, which a row without a value has against the zeros of hidden
+      // blocks too
+      if (l != l && !meets_a_key(a, w, x.lim)) {
+        m_ref = -INFINITY;
+        l = 0.f;
+      }
       const bool none = no_weight(m_ref, l);
       if (part == nullptr) {
         const float inv = none ? 0.f : 1.f / l;

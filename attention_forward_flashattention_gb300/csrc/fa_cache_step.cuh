@@ -219,7 +219,9 @@ __device__ __forceinline__ float2 unpack_f16(uint32_t w) {
 // N packed pairs of a query row, as fp16 values of `fac` (returned), a power of
 // two that brings the row into fp16's range (bf16 queries; 1 for fp16): the
 // conversion loses nothing that fp32 sums of the products would keep. kShare:
-// lanes xor 1 .. kShare / 2 hold the other parts of the row.
+// lanes xor 1 .. kShare / 2 hold the other parts of the row. A bf16 row with an
+// infinity becomes NaN: its scores might all be -inf, which looks like a row
+// without keys. (fp16: inf_to_nan.)
 template <int N, int kShare, bool BF16>
 __device__ __forceinline__ float rows_to_f16(uint32_t (&w)[N]) {
   if constexpr (!BF16) {
@@ -233,11 +235,23 @@ __device__ __forceinline__ float rows_to_f16(uint32_t (&w)[N]) {
     // exponent of the row's largest magnitude less 14, within normal fp32
     const int e = (m == 0u || m >= 0x7F80u) ? 0 : max(static_cast<int>(m >> 7) - 127 - 14, -126);
     const float fac = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-    const float inv = 1.f / fac;
+    const float inv = m >= 0x7F80u ? __int_as_float(0x7FFFFFFF) : 1.f / fac;
 #pragma unroll
     for (int i = 0; i < N; ++i)
       w[i] = pack_f16(__uint_as_float(w[i] << 16) * inv, __uint_as_float(w[i] & 0xFFFF0000u) * inv);
     return fac;
+  }
+}
+
+// Infinities among N packed pairs of fp16 values become NaN: w 0 + w.
+template <int N>
+__device__ __forceinline__ void inf_to_nan(uint32_t (&w)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    __half2 h;
+    __builtin_memcpy(&h, &w[i], 4);
+    h = __hfma2(h, __half2half2(__ushort_as_half(0)), h);
+    __builtin_memcpy(&w[i], &h, 4);
   }
 }
 
@@ -487,6 +501,13 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas(NT))
       if (used + 1 < fired) load_scales(used + 1);
       if (alive) alive = wait_bounded_warp(bars + 8u * slot, (used / kStages) & 1u, ab,
                                            kStatusSoftmax);
+      if constexpr (!BF16) {
+        // (here and not where Q is loaded: there it would wait for the rows)
+        if (tile == now.first(whole) + warp) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) inf_to_nan<kQWords>(q[nt]);
+        }
+      }
       const uint32_t sk = ring + static_cast<uint32_t>(slot * 2 * kStepTileBytes);
       const uint32_t sv = sk + kStepTileBytes;
       const int key0 = tile * KT;

@@ -156,9 +156,10 @@ fa_status fa_cache_append(const void* k, const void* v, const fa_strides* stride
  * are kept in two such parts: 2^-22 of themselves, or 2^-33 W. With d = 128
  * and 17 to 128 rows to a K / V head (on average over the sequences) query
  * elements below 2^-6 of their row's largest (bf16: 2^-9) may be rounded, by
- * 2^-17 of that largest one at most. A query row that holds an infinity or NaN
- * gives NaN wherever its scores are. V scales of one sequence may differ by a
- * factor of up to 2^100.
+ * 2^-17 of that largest one at most. Where scale * max |q| of a row is below
+ * 2^-64, its scores may be off by up to 2^-48 of the K scale. A query row that
+ * holds an infinity or NaN gives NaN if it sees a key. V scales of one sequence
+ * may differ by a factor of up to 2^100.
  * Up to three launches (a kernel for sequences of up to 16 rows to a K / V
  * head, one for more, and one that joins what they split), by the sizes that
  * the host knows. Deterministic: the same call gives the same bits.

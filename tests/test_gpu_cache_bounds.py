@@ -125,3 +125,69 @@ def test_random_values_column_by_column(n, d, dtype):
     floor = 2.0 ** -17 if d == 128 and 16 < n <= 128 else 0.0
     compare(q, cache, rng.permutation(P)[None], [keys], [0, n], True, None, dtype,
             two_parts(n, dtype), floor)
+
+
+# ------------------------------------------------------------ queries without a value
+
+def small_cache(rng, P, heads, bs, d):
+    k, v = (U.encode(rng.standard_normal((P, heads, bs, d)) * 64) for _ in range(2))
+    return to_cache(k, v, *(np.exp2(rng.integers(-8, -5, (P, heads))) for _ in range(2)))
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("n,d", KERNELS)
+def test_queries_without_a_value_that_see_no_key(n, d, dtype):
+    """More query rows than keys: rows with an infinity or NaN that see no key give
+    O = 0 and LSE = -inf like any other, those that see one give NaN; with all blocks
+    hidden none sees a key. Rows beside them keep their bits."""
+    import torch
+    rng = np.random.default_rng(n + d)
+    keys = max(n - 6, 0)
+    cache = small_cache(rng, 12, 1, 16, d)
+    table = ints(rng.permutation(12)[None])
+    q = torch.from_numpy(rng.standard_normal((n, 1, d))).to(DEV).to(tdt(dtype))
+    clean, cl = fa.attention_forward_cache(q, cache, table, ints([keys]), ints([0, n]))
+    bad = [r for r in (0, 1, 2, 7, 8, n - 1) if r < n]
+    for r, x in zip(bad, [float("nan"), float("inf"), -float("inf")] * 2):
+        q[r, 0, (5 * r) % d] = x
+    o, lse = fa.attention_forward_cache(q, cache, table, ints([keys]), ints([0, n]))
+    sees = torch.arange(n, device=DEV) >= n - keys
+    nan = torch.zeros(n, dtype=torch.bool, device=DEV)
+    nan[bad] = True
+    assert (o[~sees] == 0).all() and torch.isneginf(lse[~sees]).all()
+    assert torch.isnan(o[sees & nan]).all() and not torch.isfinite(lse[sees & nan]).any()
+    assert torch.equal(o[~nan], clean[~nan]) and torch.equal(lse[~nan], cl[~nan])
+    for hidden in (torch.full_like(table, -1), torch.full_like(table, 12)):
+        o, lse = fa.attention_forward_cache(q, cache, hidden, ints([192]), ints([0, n]))
+        assert (o == 0).all() and torch.isneginf(lse).all()
+    assert fa.fa_check(0) == fa.FA_OK
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("n,d", KERNELS)
+def test_infinite_queries_whose_scores_are_all_minus_infinity(n, d, dtype):
+    """An infinity against keys of one sign: every score is -inf, whose softmax has no
+    value (and it is not a row without keys)."""
+    import torch
+    rng = np.random.default_rng(n)
+    cache = small_cache(rng, 30, 1, 32, d)
+    cache.k.fill_(int(U.encode(np.array([-2.0]))[0]))
+    q = torch.from_numpy(rng.standard_normal((n, 1, d))).to(DEV).to(tdt(dtype))
+    q[n // 2, 0, 3] = float("inf")
+    o, lse = fa.attention_forward_cache(q, cache, ints(np.arange(30)[None]), ints([901]), ints([0, n]))
+    bad = torch.arange(n, device=DEV) == n // 2
+    assert torch.isnan(o[bad]).all() and not torch.isfinite(lse[bad]).any()
+    assert torch.isfinite(o[~bad]).all() and torch.isfinite(lse[~bad]).all()
+
+
+@pytest.mark.parametrize("n,d", KERNELS)
+def test_queries_whose_factor_underflows(n, d):
+    """bf16 queries of 2^-120 over K scales of 2^-40: scores of nothing, so O is the
+    mean of the values that a row sees, and hidden keys stay hidden."""
+    import torch
+    rng = np.random.default_rng(n + d)
+    cache = small_cache(rng, 20, 1, 16, d)
+    cache.k_scales.fill_(2.0 ** -40)
+    q = torch.from_numpy(rng.standard_normal((n, 1, d)) * 2.0 ** -120).to(DEV).to(torch.bfloat16)
+    keys = n + 97
+    compare(q, cache, rng.permutation(20)[None], [keys], [0, n], True, None, "bf16")
