@@ -718,8 +718,11 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// log2 x and 1 / x on the MUFU unit, for the scales of V: both errors (2^-22
-// and a unit in the last place) act as a change of the block's weights by as much.
+// log2 x and 1 / x on the MUFU unit, for the scales of V; subnormal x count as 0.
+// The logarithm is off by 2^-22 for x between 1/2 and 2 and by 2^-22 of itself
+// elsewhere (2^-17 for x near 2^-40; exponents of that size have fp32 steps of
+// 2^-18), the reciprocal by a unit in the last place. Either acts as a change of
+// the block's weights by as much, which fp16's 2^-11 covers.
 __device__ __forceinline__ float lg2(float x) {
   float y;
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

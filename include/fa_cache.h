@@ -36,7 +36,8 @@ extern "C" {
 typedef struct fa_cache {
   void* k;                /* e4m3 codes, 16-byte aligned */
   void* v;
-  float* k_scales;        /* [num_blocks][Hkv], contiguous; finite and > 0 where read */
+  float* k_scales;        /* [num_blocks][Hkv], contiguous; 2^-60 to 2^120 where fa_fwd_cache
+                             reads them (outside: 1 / v_scale and sums of it leave fp32's range) */
   float* v_scales;
   int num_blocks;         /* >= 1, times block and times Hkv at most 2^31 - 1 */
   int block;              /* tokens in a block: 16, 32, 64 or 128 */
@@ -159,7 +160,8 @@ fa_status fa_cache_append(const void* k, const void* v, const fa_strides* stride
  * 2^-17 of that largest one at most. Where scale * max |q| of a row is below
  * 2^-64, its scores may be off by up to 2^-48 of the K scale. A query row that
  * holds an infinity or NaN gives NaN if it sees a key. V scales of one sequence
- * may differ by a factor of up to 2^100.
+ * may differ by a factor of up to 2^100; the logarithm of one is off by at most
+ * 2^-22 of itself (or 2^-22), and the weights of its block in proportion.
  * Up to three launches (a kernel for sequences of up to 16 rows to a K / V
  * head, one for more, and one that joins what they split), by the sizes that
  * the host knows. Deterministic: the same call gives the same bits.

@@ -191,3 +191,37 @@ def test_queries_whose_factor_underflows(n, d):
     q = torch.from_numpy(rng.standard_normal((n, 1, d)) * 2.0 ** -120).to(DEV).to(torch.bfloat16)
     keys = n + 97
     compare(q, cache, rng.permutation(20)[None], [keys], [0, n], True, None, "bf16")
+
+
+# ------------------------------------------------------------ the scales' range
+
+@pytest.mark.parametrize("n,d", KERNELS)
+@pytest.mark.parametrize("low,high", [(-60, -55), (-60, 30), (-30, 60), (20, 110), (105, 110)])
+def test_v_scales_at_the_ends_of_their_range(n, d, low, high):
+    """V scales that are no powers of two, at either end of the documented range and up
+    to 2^90 apart; results in bf16, which holds them all."""
+    import torch
+    rng = np.random.default_rng(n + d)
+    bs, P = 16, 40
+    k = U.encode(rng.standard_normal((P, 1, bs, d)) * 64)
+    v = U.encode(rng.standard_normal((P, 1, bs, d)) * 64)
+    vs = np.exp2(rng.uniform(low, high, (P, 1)))
+    vs[3], vs[7] = np.exp2(low) * 1.01, np.exp2(high) * 0.99
+    cache = to_cache(k, v, np.exp2(rng.uniform(-8, -5, (P, 1))), vs)
+    q = torch.from_numpy(rng.standard_normal((n, 1, d))).to(DEV).to(torch.bfloat16)
+    floor = 2.0 ** -17 if d == 128 and 16 < n <= 128 else 0.0
+    compare(q, cache, rng.permutation(P)[None], [bs * P - 5], [0, n], True, None, "bf16", False, floor)
+
+
+@pytest.mark.parametrize("n,d", KERNELS)
+@pytest.mark.parametrize("e", [-60, -31, 50])
+def test_k_scales_at_the_ends_of_their_range(n, d, e):
+    """K scales near 2^e, and queries that bring the scores back to ordinary sizes."""
+    import torch
+    rng = np.random.default_rng(n + d)
+    bs, P = 32, 20
+    k, v = (U.encode(rng.standard_normal((P, 1, bs, d)) * 64) for _ in range(2))
+    cache = to_cache(k, v, np.exp2(e + rng.uniform(0, 2, (P, 1))), np.ones((P, 1)))
+    q = torch.from_numpy(rng.standard_normal((n, 1, d)) * 2.0 ** (-e - 7)).to(DEV).to(torch.bfloat16)
+    floor = 2.0 ** -17 if d == 128 and 16 < n <= 128 else 0.0
+    compare(q, cache, rng.permutation(P)[None], [bs * P - 5], [0, n], True, None, "bf16", False, floor)
