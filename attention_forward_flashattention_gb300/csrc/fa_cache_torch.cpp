@@ -285,7 +285,8 @@ PyObject* attention_forward_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int32_t* p_table = index(table, dev, B, width, "block_table");
   const int32_t* p_kv = index(tensor(a[3], "kv_lens"), dev, B, -1, "kv_lens");
   const int32_t* p_cu = ragged ? index(tensor(a[4], "cu_q"), dev, B + 1, -1, "cu_q") : nullptr;
-  const bool causal = PyObject_IsTrue(a[6]) == 1;
+  const int causal = PyObject_IsTrue(a[6]);
+  if (causal < 0) throw python_error();
   double scale = 1.0 / std::sqrt(static_cast<double>(c.d));
   if (a[7] != Py_None) {
     scale = PyFloat_AsDouble(a[7]);
@@ -331,7 +332,7 @@ PyObject* attention_forward_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
     fa_status rc;
     Py_BEGIN_ALLOW_THREADS;
     rc = fa_fwd_cache(q.data_ptr(), &c, p_table, width, p_kv, p_cu, o.data_ptr(),
-                      static_cast<float*>(lse.data_ptr()), B, T, H, st, causal ? 1 : 0,
+                      static_cast<float*>(lse.data_ptr()), B, T, H, st, causal,
                       static_cast<float>(scale), dt, ws.data_ptr(), ws_bytes, cs.stream);
     Py_END_ALLOW_THREADS;
     if (rc != FA_OK) return status(rc);

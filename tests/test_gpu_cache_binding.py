@@ -1,0 +1,44 @@
+"""Arguments that the block cache's torch calls have to refuse, and calls of nothing."""
+import numpy as np
+import pytest
+
+import attention_forward_flashattention_gb300 as fa
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    import torch
+    torch.cuda.init()
+    fa.build.build()
+    fa.load_library()
+
+
+def ints(v):
+    import torch
+    return torch.tensor(np.asarray(v), dtype=torch.int32, device=DEV)
+
+
+def test_causal_without_a_truth_value_is_an_error():
+    """The error that its truth test raises reaches the caller, and nothing is enqueued."""
+    import torch
+
+    class Odd:
+        def __bool__(self):
+            raise KeyError("no truth here")
+
+    c = fa.cache_empty(4, 2, 16, 64, device=DEV)
+    q = torch.zeros(3, 4, 64, dtype=torch.float16, device=DEV)
+    tab, lens = ints(np.zeros((3, 2))), ints([1, 1, 1])
+    o, lse = torch.full_like(q, 7.0), torch.full((3, 4), 7.0, device=DEV)
+    ws = torch.empty(fa.fa_fwd_cache_workspace_size(3, 3, 4, 2, 64), dtype=torch.uint8, device=DEV)
+    with pytest.raises(RuntimeError):
+        fa.attention_forward_cache(q, c, tab, lens, causal=torch.tensor([True, False]))
+    with pytest.raises(KeyError):
+        fa.attention_forward_cache_into(q, c, tab, lens, o, lse, ws, causal=Odd())
+    torch.cuda.synchronize()
+    assert (o == 7).all() and (lse == 7).all()
+    fa.attention_forward_cache_into(q, c, tab, lens, o, lse, ws, causal=torch.tensor([True]))
+    assert (o == 0).all()
