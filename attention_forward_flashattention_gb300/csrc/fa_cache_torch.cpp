@@ -133,11 +133,14 @@ fa_cache describe(PyObject* o, int dev) {
     return s.dim() == 2 && s.size(0) == k.size(0) && s.size(1) == k.size(1) &&
            s.scalar_type() == at::kFloat && s.is_contiguous();
   };
+  auto codes = [](const at::Tensor& t) {
+    return t.scalar_type() == at::kFloat8_e4m3fn || t.scalar_type() == at::kByte;
+  };
   if (!(k.dim() == 4 && k.sizes() == v.sizes() && k.strides() == v.strides() && k.stride(3) == 1 &&
-        k.element_size() == 1 && v.element_size() == 1 && scales(ks) && scales(vs)))
+        codes(k) && codes(v) && scales(ks) && scales(vs)))
     refuse(PyExc_ValueError,
-           "cache: k, v must be [blocks, heads, block, d] 8-bit tensors of equal strides (1 along "
-           "d) and k_scales, v_scales contiguous float32 [blocks, heads]");
+           "cache: k, v must be [blocks, heads, block, d] float8_e4m3fn or uint8 tensors of equal "
+           "strides (1 along d) and k_scales, v_scales contiguous float32 [blocks, heads]");
   if (!(on(k, dev) && on(v, dev) && on(ks, dev) && on(vs, dev)))
     refuse(PyExc_ValueError, "cache: tensors must be on the same CUDA device as the other arguments");
   fa_cache c{};

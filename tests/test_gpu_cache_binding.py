@@ -42,3 +42,19 @@ def test_causal_without_a_truth_value_is_an_error():
     assert (o == 7).all() and (lse == 7).all()
     fa.attention_forward_cache_into(q, c, tab, lens, o, lse, ws, causal=torch.tensor([True]))
     assert (o == 0).all()
+
+
+def test_codes_of_another_8_bit_type_are_refused():
+    """Codes are e4m3, as float8_e4m3fn or raw bytes: other 8-bit types would be read as it."""
+    import torch
+    c = fa.cache_empty(4, 2, 16, 64, device=DEV)
+    x = torch.zeros(3, 2, 64, dtype=torch.float16, device=DEV)
+    q = torch.zeros(3, 4, 64, dtype=torch.float16, device=DEV)
+    tab, lens = ints(np.zeros((3, 2))), ints([1, 1, 1])
+    for t in (torch.float8_e5m2, torch.float8_e4m3fnuz, torch.int8, torch.bool):
+        for bad in (c._replace(k=c.k.view(t)), c._replace(v=c.v.view(t))):
+            with pytest.raises(ValueError):
+                fa.cache_append(x, x, ints([0, 1, 2]), bad)
+            with pytest.raises(ValueError):
+                fa.attention_forward_cache(q, bad, tab, lens)
+    fa.cache_append(x, x, ints([0, 1, 2]), c._replace(v=c.v.view(torch.uint8)))
