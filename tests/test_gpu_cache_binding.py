@@ -58,3 +58,33 @@ def test_codes_of_another_8_bit_type_are_refused():
             with pytest.raises(ValueError):
                 fa.attention_forward_cache(q, bad, tab, lens)
     fa.cache_append(x, x, ints([0, 1, 2]), c._replace(v=c.v.view(torch.uint8)))
+
+
+def c_cache(cache):
+    P, heads, bs, d = cache.k.shape
+    return fa.FaCache(cache.k.data_ptr(), cache.v.data_ptr(), cache.k_scales.data_ptr(),
+                      cache.v_scales.data_ptr(), P, bs, heads, d, *cache.k.stride()[:3])
+
+
+def test_a_call_of_no_rows():
+    """T = 0 with the workspace that its size asks for succeeds and writes nothing; a
+    workspace of no bytes is refused, as for any other call."""
+    import torch
+    c = fa.cache_empty(4, 2, 16, 64, device=DEV)
+    tab, lens, cu = ints([[0, 1], [2, 3]]), ints([20, 30]), ints([0, 0, 0])
+    q = torch.randn(2, 4, 64, device=DEV).half()
+    o, lse = torch.full_like(q, 7.0), torch.full((2, 4), 7.0, device=DEV)
+    size = fa.fa_fwd_cache_workspace_size(2, 0, 4, 2, 64)
+    ws = torch.empty(max(size, 16), dtype=torch.uint8, device=DEV)
+    strides = ((4 * 64, 64, 4 * 64),) * 2
+
+    def call(cu_q, nbytes):
+        return fa.fa_fwd_cache(q.data_ptr(), c_cache(c), tab.data_ptr(), 2, lens.data_ptr(), cu_q,
+                               o.data_ptr(), lse.data_ptr(), 2, 0, 4, strides, True, 0.125,
+                               fa.FA_DTYPE_FP16, ws.data_ptr(), nbytes)
+
+    for cu_q in (None, cu.data_ptr()):
+        assert call(cu_q, size) == fa.FA_OK
+        assert call(cu_q, 0) == fa.FA_ERR_INVALID_ARG
+    torch.cuda.synchronize()
+    assert (o == 7).all() and (lse == 7).all()
