@@ -225,3 +225,135 @@ def test_k_scales_at_the_ends_of_their_range(n, d, e):
     q = torch.from_numpy(rng.standard_normal((n, 1, d)) * 2.0 ** (-e - 7)).to(DEV).to(torch.bfloat16)
     floor = 2.0 ** -17 if d == 128 and 16 < n <= 128 else 0.0
     compare(q, cache, rng.permutation(P)[None], [bs * P - 5], [0, n], True, None, "bf16", False, floor)
+
+
+# ------------------------------------------------------------ split and joined
+
+def keys_of(rng, P, heads, bs, d):
+    """Codes with values that differ from column to column and along the keys, so that a
+    lost or misplaced share changes every column."""
+    k = U.encode(rng.standard_normal((P, heads, bs, d)) * 32)
+    lift = np.arange(P)[:, None, None, None] / P + np.arange(d) / d
+    v = U.encode((rng.standard_normal((P, heads, bs, d)) * 0.25 + lift) * 64)
+    return k, v
+
+
+SPLIT = [([131071], 1, 8, 2, 128, 128, "bf16"), ([131071], 1, 2, 1, 128, 64, "fp16"),
+         ([70001], 5, 2, 1, 128, 128, "fp16"), ([40003], 3, 2, 1, 16, 64, "fp16"),
+         ([50001, 33], 24, 4, 1, 64, 128, "fp16"), ([50001, 33], 24, 4, 1, 64, 128, "bf16"),
+         ([20011, 0, 513], 160, 2, 2, 32, 64, "bf16"), ([60007], 6, 16, 2, 32, 64, "bf16")]
+
+
+@pytest.mark.parametrize("lens,n,H,heads,bs,d,dtype", SPLIT)
+def test_joined_means(lens, n, H, heads, bs, d, dtype):
+    """Queries of zero: every visible key weighs 1, so O is the mean of their values and
+    LSE the logarithm of their number. The weights are exact powers of two, so only
+    O's own rounding and the fp32 sums are left: a share's, of at most 2^11 keys by MMAs
+    of 16 (2^7 steps of 2^-23), and the join's over at most 2^9 shares, below 2^-12."""
+    import torch
+    rng = np.random.default_rng(n + d)
+    need = [-(-x // bs) for x in lens]
+    P = sum(need)
+    k, v = keys_of(rng, P, heads, bs, d)
+    cache = to_cache(k, v, np.full((P, heads), 2.0 ** -6), np.full((P, heads), 2.0 ** -7))
+    ids = rng.permutation(P)
+    table = np.zeros((len(lens), max(need)), dtype=np.int64)
+    for b, m in enumerate(need):
+        table[b, :m] = ids[sum(need[:b]):sum(need[:b]) + m]
+    q = torch.zeros(len(lens) * n, H, d, device=DEV, dtype=tdt(dtype))
+    o, lse = fa.attention_forward_cache(q, cache, ints(table), ints(lens),
+                                        ints(np.arange(len(lens) + 1) * n))
+    eps = torch.finfo(q.dtype).eps
+    got, gl = o.double().cpu().numpy(), lse.double().cpu().numpy()
+    for b, L in enumerate(lens):
+        for h in range(heads if L else 0):
+            vv = U.CODE_VALUES[v[table[b, :need[b]], h]].reshape(-1, d)[:L] / 128.0
+            total, size = np.cumsum(vv, 0), np.cumsum(np.abs(vv), 0)
+            for i in range(n):
+                lim = L - n + i + 1
+                rows = got[b * n + i, h * (H // heads):(h + 1) * (H // heads)]
+                if lim <= 0:
+                    assert np.all(rows == 0)
+                    continue
+                ref, mag = total[lim - 1] / lim, size[lim - 1] / lim
+                tol = 2.0 ** -12 * mag + np.abs(ref) * eps / 2 * (1 + 2.0 ** -10) + 2.0 ** -25
+                assert np.all(np.abs(rows - ref) <= tol)
+                le = gl[b * n + i, h * (H // heads):(h + 1) * (H // heads)]
+                assert np.all(np.abs(le - np.log(lim)) <= 2.0 ** -12 + 2.0 ** -16)
+
+
+@pytest.mark.parametrize("lens,n,H,heads,bs,d,dtype", SPLIT)
+def test_joined_column_by_column(lens, n, H, heads, bs, d, dtype):
+    """The same sizes with ordinary queries, every element against its own bound (the
+    first two and the last two query tokens of each sequence)."""
+    import torch
+    rng = np.random.default_rng(n + d + 1)
+    need = [-(-x // bs) for x in lens]
+    P = sum(need)
+    k, v = keys_of(rng, P, heads, bs, d)
+    cache = to_cache(k, v, np.exp2(rng.integers(-8, -5, (P, heads))),
+                     np.exp2(rng.integers(-9, -5, (P, heads))))
+    ids = rng.permutation(P)
+    table = np.zeros((len(lens), max(need)), dtype=np.int64)
+    for b, m in enumerate(need):
+        table[b, :m] = ids[sum(need[:b]):sum(need[:b]) + m]
+    q = torch.from_numpy(rng.standard_normal((len(lens) * n, H, d))).to(DEV).to(tdt(dtype))
+    o, lse = fa.attention_forward_cache(q, cache, ints(table), ints(lens),
+                                        ints(np.arange(len(lens) + 1) * n))
+    rows = n * (H // heads)
+    floor = 2.0 ** -17 if d == 128 and 16 < rows <= 128 else 0.0
+    host = [c.view(torch.uint8).cpu().numpy() for c in cache[:2]]
+    scales = [s.double().cpu().numpy() for s in cache[2:]]
+    eps = torch.finfo(q.dtype).eps
+    for b, L in enumerate(lens):
+        for i in sorted({0, 1, n - 2, n - 1} & set(range(n))):
+            t = b * n + i
+            lim = max(L - n + i + 1, 0)          # the keys that the causal rule leaves this token
+            O, Ls, tol_o, tol_l = U.attend_columns(
+                q[t:t + 1].double().cpu().numpy(), *host, *scales, table[b:b + 1], [lim], [0, 1], bs,
+                d ** -0.5, False, eps, two_parts(rows, dtype), floor)
+            got, gl = o[t].double().cpu().numpy(), lse[t].double().cpu().numpy()
+            if lim == 0:
+                assert np.all(got == 0) and np.all(np.isneginf(gl))
+                continue
+            err = np.abs(got - O[0])
+            assert np.all(err <= tol_o[0]), f"O: {np.max(err / tol_o[0]):.2f} of the bound"
+            assert np.all(np.abs(gl - Ls[0]) <= tol_l[0])
+
+
+# ------------------------------------------------------------ together
+
+@pytest.mark.parametrize("dtype,H,heads,bs,d", [("bf16", 6, 2, 16, 64), ("fp16", 8, 1, 32, 128),
+                                                ("bf16", 16, 2, 64, 128)])
+def test_serving_loop_step_by_step(dtype, H, heads, bs, d):
+    """Plan, append and attention as a serving loop makes them. Every step's plan is
+    compared exactly, the codes and scales that its append leaves exactly, and its
+    attention, element by element, with exact attention over those codes."""
+    import torch
+    rng = np.random.default_rng(d + bs)
+    B, P, width = 4, 40, 12
+    cache = fa.cache_empty(P, heads, bs, d, device=DEV)
+    host = [np.zeros((P, heads, bs, d), np.uint8) for _ in range(2)]
+    scales = [np.ones((P, heads)) for _ in range(2)]
+    htable, hlens, hpos = np.full((B, width), -1, dtype=np.int64), [0] * B, 0
+    hfree = rng.permutation(P)
+    table, free, pos, lens = ints(htable), ints(hfree), ints([0]), ints(hlens)
+    for add in ([37, 5, 64, 0], [1, 1, 1, 1], [1, 0, 2, 30], [3, 1, 1, 1], [1, 25, 1, 2], [1, 1, 1, 1]):
+        T = sum(add)
+        slots, cu, lens, pos = fa.cache_plan(lens, ints(add), table, free, pos, T, bs)
+        hs, hcu, hlens, htable, hpos = U.plan(hlens, add, htable, hfree, hpos, T, bs)
+        assert (slots.tolist(), cu.tolist(), lens.tolist(), pos.tolist()) == (hs, hcu, hlens, [hpos])
+        assert np.array_equal(table.cpu().numpy(), htable)
+        size = np.exp2(rng.integers(-3, 4, (T, heads, 1)))
+        kv = [torch.from_numpy(rng.standard_normal((T, heads, d)) * size).to(DEV).to(tdt(dtype))
+              for _ in range(2)]
+        fa.cache_append(kv[0], kv[1], slots, cache)
+        for i in range(2):
+            host[i], scales[i] = U.append(kv[i].double().cpu().numpy(), hs, host[i], scales[i], bs)
+            assert np.array_equal(cache[i].view(torch.uint8).cpu().numpy(), host[i])
+            assert np.array_equal(cache[i + 2].cpu().numpy().astype(np.float64), scales[i])
+        q = torch.from_numpy(rng.standard_normal((T, H, d))).to(DEV).to(tdt(dtype))
+        rows = [n * (H // heads) for n in add]
+        # (the wider of the bounds where a step's sequences go to different kernels)
+        floor = 2.0 ** -17 if d == 128 and max(rows) > 16 else 0.0
+        compare(q, cache, htable, hlens, hcu, True, None, dtype, two_parts(max(rows), dtype), floor)
