@@ -3,7 +3,9 @@
   _build/libfa_sm103.so    the product: C ABI of include/fa.h and fa_cache.h
   _build/libfa_selftest.so GPU unit tests of the PTX building blocks
   _build/_fa_cache_torch.so  the block cache's calls on torch tensors (host
-                           code, g++, linked against libfa_sm103.so)
+                           code, g++, linked against libfa_sm103.so); left out
+                           where there is no PyTorch, which the libraries do
+                           not need
 
 Translation units are compiled in parallel (one nvcc process each), then
 linked. ptxas resource usage (registers, spills, shared memory) of every
@@ -67,11 +69,29 @@ def torch_path() -> str:
     return os.path.join(OUT, TORCH_NAME)
 
 
-def _torch_dir() -> str:
+def _torch_dir() -> str | None:
+    """PyTorch's folder, None where it is not installed."""
     spec = importlib.util.find_spec("torch")
     if spec is None or not spec.submodule_search_locations:
-        raise RuntimeError("PyTorch not found")
+        return None
     return list(spec.submodule_search_locations)[0]
+
+
+def _torch_stamp() -> str:
+    """What the torch module is built against: it is bound to that PyTorch and
+    this interpreter."""
+    with open(os.path.join(_torch_dir(), "version.py")) as f:
+        return f"{sys.version}\n{_torch_dir()}\n{f.read()}"
+
+
+def _torch_stale() -> bool:
+    if _stale(torch_path(), [TORCH_UNIT]):
+        return True
+    try:
+        with open(torch_path() + ".stamp") as f:
+            return f.read() != _torch_stamp()
+    except OSError:
+        return True
 
 
 def _torch_compile(nvcc: str, obj: str) -> list[str]:
@@ -97,43 +117,55 @@ def _stale(target: str, sources: list[str]) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _start(cmd: list[str], unit: str):
+    """Starts a compiler; what it prints goes to the unit's log."""
+    with open(_log_path(unit), "w") as log:
+        return subprocess.Popen(cmd, stdout=log, stderr=subprocess.STDOUT)
+
+
+def _log_path(unit: str) -> str:
+    return os.path.join(OUT, f"ptxas_{os.path.splitext(unit)[0]}.log")
+
+
+def _raise_failed(units: list[str]) -> None:
+    msgs = []
+    for u in units:
+        with open(_log_path(u)) as f:
+            msgs.append(f"--- {u}\n" + f.read()[-6000:])
+    raise RuntimeError("compilation failed:\n" + "\n".join(msgs))
+
+
 def build(force: bool = False, verbose: bool = False) -> tuple[str, str]:
-    """Compiles the libraries and the torch module if any source is newer;
-    returns the libraries' paths."""
+    """Compiles the libraries and the torch module if any source is newer (the
+    module also if PyTorch is another one); returns the libraries' paths. The
+    libraries are complete before anything about the module can fail."""
     nvcc = nvcc_path()
     os.makedirs(OUT, exist_ok=True)
     jobs = []
     for units, name in ((LIB_UNITS, LIB_NAME), (SELFTEST_UNITS, SELFTEST_NAME)):
         if force or _stale(os.path.join(OUT, name), units):
             jobs.append((units, name))
-    torch_job = force or bool(jobs) or _stale(torch_path(), [TORCH_UNIT])
-    if not torch_job:
+    torch_job = _torch_dir() is not None and (force or bool(jobs) or _torch_stale())
+    if not jobs and not torch_job:
         return lib_path(), selftest_path()
-    procs = []
+    procs, torch_proc, torch_error = [], None, None
     torch_obj = os.path.join(OUT, "fa_cache_torch.o")
-    log = open(os.path.join(OUT, "ptxas_fa_cache_torch.log"), "w")
-    procs.append((TORCH_UNIT, subprocess.Popen(_torch_compile(nvcc, torch_obj), stdout=log,
-                                               stderr=subprocess.STDOUT), log))
+    if torch_job:
+        try:
+            torch_proc = _start(_torch_compile(nvcc, torch_obj), TORCH_UNIT)
+        except OSError as e:
+            torch_error = e
     for units, _ in jobs:
         for u in units:
             obj = os.path.join(OUT, u.replace(".cu", ".o"))
-            log = open(os.path.join(OUT, "ptxas_" + u.replace(".cu", ".log")), "w")
             cmd = [nvcc] + _flags() + ["-c", os.path.join(CSRC, u), "-o", obj]
             if verbose:
                 print(" ".join(cmd), file=sys.stderr)
-            procs.append((u, subprocess.Popen(cmd, stdout=log, stderr=subprocess.STDOUT), log))
-    failed = []
-    for u, p, log in procs:
-        p.wait()
-        log.close()
-        if p.returncode != 0:
-            failed.append(u)
+            procs.append((u, _start(cmd, u)))
+    failed = [u for u, p in procs if p.wait() != 0]
+    torch_failed = torch_proc is not None and torch_proc.wait() != 0
     if failed:
-        msgs = []
-        for u in failed:
-            with open(os.path.join(OUT, f"ptxas_{os.path.splitext(u)[0]}.log")) as f:
-                msgs.append(f"--- {u}\n" + f.read()[-6000:])
-        raise RuntimeError("compilation failed:\n" + "\n".join(msgs))
+        _raise_failed(failed)
     libdir = os.path.join(_cuda_home(nvcc), "lib64")
     for units, name in jobs:
         objs = [os.path.join(OUT, u.replace(".cu", ".o")) for u in units]
@@ -142,9 +174,17 @@ def build(force: bool = False, verbose: bool = False) -> tuple[str, str]:
             "-Xlinker", "-rpath", "-Xlinker", libdir]
         subprocess.run(cmd, check=True)
         os.replace(tmp, os.path.join(OUT, name))
-    tmp = torch_path() + f".tmp{os.getpid()}"
-    subprocess.run(_torch_link(torch_obj, tmp), check=True)
-    os.replace(tmp, torch_path())
+    if torch_error is not None:
+        raise RuntimeError(f"{TORCH_UNIT} not compiled: {torch_error}")
+    if torch_failed:
+        _raise_failed([TORCH_UNIT])
+    if torch_job:
+        tmp = torch_path() + f".tmp{os.getpid()}"
+        subprocess.run(_torch_link(torch_obj, tmp), check=True)
+        os.replace(tmp, torch_path())
+        with open(tmp, "w") as f:
+            f.write(_torch_stamp())
+        os.replace(tmp, torch_path() + ".stamp")
     return lib_path(), selftest_path()
 
 
