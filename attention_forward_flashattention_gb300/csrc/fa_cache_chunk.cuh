@@ -629,8 +629,10 @@ __device__ __forceinline__ float e4m3_step(uint32_t top) {
 // Chunks e0 .. e1 - 1 (16 elements each) of this thread's query row p as PARTS
 // e4m3 rows at `to` (row r of tiles of kChunkKeys rows) that add up to row / fac,
 // whose largest magnitude is 128 to 256. bf16's 8-bit significands are the sum of
-// two parts, fp16's 11 bits of three, down to elements 2^-16 of the largest one;
-// below, the last part rounds to multiples of 2^-9, 2^-16 of the largest.
+// two parts, fp16's 11 bits of three, as long as their last bit is not below e4m3's
+// smallest step, 2^-9: for elements from 2^-9 (bf16) or 2^-6 (fp16) of the largest
+// one on. Of smaller ones the last part is rounded, by 2^-10 at most, 2^-17 of the
+// largest. A row with a few very large elements pays for it with its small ones.
 template <int D, bool BF16, int PARTS>
 __device__ __forceinline__ void query_parts(const uint16_t* p, float fac, uint32_t to, int r, int e0,
                                             int e1) {

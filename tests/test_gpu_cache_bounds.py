@@ -357,3 +357,24 @@ def test_serving_loop_step_by_step(dtype, H, heads, bs, d):
         # (the wider of the bounds where a step's sequences go to different kernels)
         floor = 2.0 ** -17 if d == 128 and max(rows) > 16 else 0.0
         compare(q, cache, htable, hlens, hcu, True, None, dtype, two_parts(max(rows), dtype), floor)
+
+
+# ------------------------------------------------------------ queries of wide range
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("top", [1.0, 60.0, 2.0 ** -10])
+@pytest.mark.parametrize("n", [1, 3, 20, 40])
+def test_elements_of_a_query_far_apart(n, top, dtype):
+    """Elements of a query that lie 2^20 apart, 6 rows to the K / V head. Only where
+    queries are cut into 8-bit parts (17 to 128 rows, on average 18 and 120 here, d 128)
+    may small elements be rounded, by 2^-17 of the row's largest; with 6 rows, or 240,
+    they count as they are."""
+    import torch
+    d, rng = 128, np.random.default_rng(n)
+    apart = top * np.exp2(-np.linspace(0, 20, d)[rng.permutation(d)])
+    cache = small_cache(rng, 40, 1, 32, d)
+    lens, table = [n + 100, n, n + 259], rng.permutation(39).reshape(3, 13)
+    q = torch.from_numpy(rng.standard_normal((3 * n, 6, d)) * apart).to(DEV).to(tdt(dtype))
+    parts = 16 < 6 * n <= 128
+    compare(q, cache, table, lens, [0, n, 2 * n, 3 * n], True, None, dtype, two_parts(6 * n, dtype),
+            2.0 ** -17 if parts else 0.0)
