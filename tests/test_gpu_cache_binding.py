@@ -88,3 +88,26 @@ def test_a_call_of_no_rows():
         assert call(cu_q, 0) == fa.FA_ERR_INVALID_ARG
     torch.cuda.synchronize()
     assert (o == 7).all() and (lse == 7).all()
+
+
+@pytest.mark.parametrize("short", ["rows", "blocks", "none"])
+def test_a_large_plan_that_refuses(short):
+    """A plan of many CTAs whose rows or free blocks run out on the way, with requests
+    that are refused for their own numbers in between."""
+    import cache_util as U
+    rng = np.random.default_rng(7)
+    B, bs, width = 700, 32, 40
+    lens, new = rng.integers(0, 600, B), rng.integers(0, 60, B)
+    lens[100], new[200], lens[300] = -1, -7, width * bs
+    new[300] = 5
+    T = int(np.maximum(new, 0).sum())
+    T = T // 2 + 3 if short == "rows" else T + 9
+    need = int((-(-(lens + np.maximum(new, 0)) // bs) - -(-lens // bs)).sum())
+    free = rng.permutation(1 << 16)[:need // 2 if short == "blocks" else need + 4]
+    table = rng.integers(0, 1 << 16, (B, width))
+    tab = ints(table)
+    got = fa.cache_plan(ints(lens), ints(new), tab, ints(free), ints([2]), T, bs)
+    ref = U.plan(lens.tolist(), new.tolist(), table, free, 2, T, bs)
+    assert [g.tolist() for g in got] == [ref[0], ref[1], ref[2], [ref[4]]]
+    assert np.array_equal(tab.cpu().numpy(), ref[3])
+    assert any(s == -1 for s in ref[0][:T - 9])

@@ -378,3 +378,60 @@ def test_elements_of_a_query_far_apart(n, top, dtype):
     parts = 16 < 6 * n <= 128
     compare(q, cache, table, lens, [0, n, 2 * n, 3 * n], True, None, dtype, two_parts(6 * n, dtype),
             2.0 ** -17 if parts else 0.0)
+
+
+# ------------------------------------------------------------ scores past fp32's whole numbers
+
+@pytest.mark.parametrize("n,d", KERNELS)
+@pytest.mark.parametrize("e", [18, 24, 27, 40])
+def test_scores_of_any_size_choose_the_largest(n, d, e):
+    """One key's score is 2^e (exponents whose fp32 steps are 2^(e - 23)) and the next
+    one an eighth lower: O is the first key's V and LSE its score, to the rounding of
+    the exponent: a weight that passes fp16's range is its largest number, 2^-5 less."""
+    import torch
+    rng = np.random.default_rng(e)
+    P, bs = 10, 32
+    k = np.zeros((P, 1, bs, d), np.uint8)
+    k[:, 0, :, 0] = U.encode(rng.uniform(0.1, 0.875, (P, bs)))
+    k[6, 0, 5, 0] = U.encode(np.array([1.0]))[0]
+    v = U.encode(rng.standard_normal((P, 1, bs, d)))
+    cache = to_cache(k, v, np.ones((P, 1)), np.full((P, 1), 0.37))
+    q = torch.zeros(n, 1, d, device=DEV, dtype=torch.bfloat16)
+    q[:, :, 0] = 2.0 ** e
+    o, lse = fa.attention_forward_cache(q, cache, ints(np.arange(P)[None]), ints([P * bs]), ints([0, n]),
+                                        False, 1.0)
+    want = torch.from_numpy(U.CODE_VALUES[v[6, 0, 5]] * np.float64(np.float32(0.37))).to(DEV)
+    assert ((o.double() - want).abs() <= want.abs() * 2.0 ** -5).all()
+    assert ((lse.double() - 2.0 ** e).abs() <= 2.0 ** (e - 21)).all()
+
+
+# ------------------------------------------------------------ a workspace of two graphs
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_two_graphs_on_one_workspace(dtype):
+    """Two captured calls, one of single tokens and one of a mixture, that share a
+    workspace and are replayed in turn on one stream give the bits of direct calls."""
+    import torch
+    rng = np.random.default_rng(3)
+    cache = small_cache(rng, 120, 2, 32, 128)
+    table, lens = ints(rng.permutation(120).reshape(3, 40)), ints([1270, 33, 900])
+    cus = [ints([0, 1, 2, 3]), ints([0, 1, 61, 66])]
+    qs = [torch.randn(T, 16, 128, device=DEV).to(tdt(dtype)) for T in (3, 66)]
+    want = [fa.attention_forward_cache(q, cache, table, lens, cu) for q, cu in zip(qs, cus)]
+    ws = torch.empty(max(fa.fa_fwd_cache_workspace_size(3, T, 16, 2, 128) for T in (3, 66)),
+                     dtype=torch.uint8, device=DEV)
+    outs = [(torch.empty_like(o), torch.empty_like(lse)) for o, lse in want]
+    torch.cuda.synchronize()
+    graphs = [torch.cuda.CUDAGraph() for _ in qs]
+    for g, q, cu, (o, lse) in zip(graphs, qs, cus, outs):
+        with torch.cuda.graph(g):
+            fa.attention_forward_cache_into(q, cache, table, lens, o, lse, ws, cu)
+    for _ in range(3):
+        for o, lse in outs:
+            o.zero_()
+            lse.zero_()
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for got, ref in zip(outs, want):
+            assert all(torch.equal(a, b) for a, b in zip(got, ref))
