@@ -32,7 +32,9 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kCtasPerSm = 4;  // 64 registers a thread
+// 64 registers a thread: the instances of blocks of 16, 32 and 64 spill 32 to 36
+// bytes at d = 128 (blocks of 32 at d = 64: 4), those of 128 nothing.
+constexpr int kCtasPerSm = 4;
 
 template <bool BF16>
 __device__ __forceinline__ float2 widen(uint32_t w) {

@@ -25,9 +25,14 @@ AttnPlan plan_attn(int B, int T, int group, bool ragged) {
   AttnPlan p;
   const long long most = static_cast<long long>(T) * group;  // rows of a sequence to a K / V head
   if (!ragged || B == 1 || T <= B || most <= kStepMaxRows) {
-    // sequences of one size, of a token each (as a rule), or small in any case. Up to
-    // 16 rows the step kernel: 16 sequences, 4 K / V heads, 8192 keys take 46 us with
-    // 16 rows there; the chunk kernel takes 58 to 66 us for any number from 17 to 64.
+    // sequences of one size, of a token each, or small in any case. Up to 16 rows the
+    // step kernel: 16 sequences, 4 K / V heads, 8192 keys, bf16: a call takes 50 us with
+    // 16 rows there; the chunk kernel takes 60 for any number from 24 to 64.
+    // A ragged batch of at most a token for each sequence need not be one of single
+    // tokens, but the host does not see its lengths. Calls of 256 sequences, 8 query
+    // heads to a K / V head, here / as a mixture: all with one token, 1000 keys, 58 / 64
+    // us (4 heads: 95 / 137); one with 16 tokens behind 8000 keys, the others idle, 31 /
+    // 49; but one with 64 tokens 70 / 37, and with 200 tokens 189 / 62.
     const long long rows = !ragged ? most / B : (T <= B && B > 1 ? group : most);
     p.nt = rows <= 8 ? 1 : (rows <= kStepMaxRows ? 2 : 0);
     p.chunk = p.nt == 0;
@@ -167,9 +172,12 @@ cudaError_t launch_cache_attn(const CacheAttnArgs& a, const fa_cache& c, bool bf
                               float* ws, cudaStream_t stream, bool* mapped) {
   AttnPlan p = plan_attn(a.B, a.T, a.group, a.cu_q != nullptr);
   // Items of 128 rows, K unwidened, where sequences have up to 128 rows to a K / V
-  // head on average. Us with items of 256 rows beside it, bf16 (fp16), 4 K / V heads:
-  // 16 x 24 rows over 8192 keys 58 / 70 (66 / 69), 16 x 64 rows 58 / 70 (59 / 67), 16 x
-  // 128 rows 67 / 77 (69 / 74), one sequence of 4096 rows among 63 of 8 127 / 127 (129 / 127).
+  // head on average. Us of ragged calls with items of 256 rows beside it, bf16 (fp16),
+  // 4 K / V heads, 8192 keys: 16 x 24 rows 70 / 77 (72 / 74), 16 x 64 rows 71 / 77
+  // (72 / 75), 16 x 128 rows 78 / 83 (79 / 80). The average counts the sequences of the
+  // step kernel too, which the host cannot tell from the others: one chunk of 2048
+  // tokens behind 14336 others (behind none) beside 200 single tokens, 8 query heads to
+  // a K / V head, takes 524 / 468 us (308 / 207), one of 512 tokens 116 / 123.
   if (chunk_parts(c.d, bf16) > 0 && static_cast<long long>(a.T) * a.group <= 128LL * a.B)
     p.item_rows = 128;
   *mapped = true;

@@ -40,13 +40,14 @@
 //
 // What bounds it. Pair mode: the chain S - softmax - P V - S of each Q tile, as in
 // the forward kernel of whole matrices; tensor memory is full, so S has no second
-// buffer. 2048 tokens behind 14336 others, 32 heads of d 128 on 8: 369 us, 1.40
+// buffer. 2048 tokens behind 14336 others, 32 heads of d 128 on 8: 371 us, 1.39
 // PFLOP/s (72 % of a matrix product's burst rate), tensor pipe active 61 %. Split
-// mode: 16 x 40 rows, 4 K / V heads, 8192 keys: 59 us (with all of K widened, too,
-// and whole tiles for each warpgroup 69 us); a KV tile takes 2400 cycles, 1700 of
-// them the MMAs (shared-memory traffic, 208 KB a tile) and 1700 a
-// warpgroup's softmax, whose warps stand alone on their schedulers. The other
-// third of the time is the launch, Q, the epilogues and the join.
+// mode: 16 x 40 rows, 4 K / V heads, 8192 keys: 60 us a call of equal sequences, 70
+// a ragged one, whose launch of the step kernel finds nothing to do (9 us less than
+// with all of K widened, too, and whole tiles for each warpgroup); a KV tile takes
+// 2400 cycles, 1700 of them the MMAs (shared-memory traffic, 208 KB a tile) and 1700
+// a warpgroup's softmax, whose warps stand alone on their schedulers. The other
+// third of the 60 us is the launch, Q, the epilogues and the join.
 #pragma once
 
 #include "fa_cache_step.cuh"
@@ -780,6 +781,9 @@ __device__ __forceinline__ bool softmax_tiles(const CacheAttnArgs& a, const Tile
       for (int c = 0; c < 8; ++c) {
         const float2 t = ptx::ffma2(make_float2(s[16 * g + 2 * c], s[16 * g + 2 * c + 1]), f2, a2);
         const float p0 = ptx::ex2(t.x), p1 = ptx::ex2(t.y);
+        // (one fp16 value, for fp16 queries too: a second part, which the step kernel
+        // keeps for them, would double the products with V here. Relative error of
+        // fp16 drafts against 64 bits 2.9e-4, of which rounding O is 2.1e-4.)
         pk[g >> 2][(g & 3) * 8 + c] = pack_weights(p0, p1);
         if (c & 1) sum1 = ptx::fadd2(sum1, make_float2(p0, p1));
         else sum0 = ptx::fadd2(sum0, make_float2(p0, p1));

@@ -35,10 +35,11 @@
 // persistent CTAs (two or three on each SM). A share that begins or ends inside an item
 // writes a partial result (O, m, l), which fa_cache_join_kernel joins in order.
 //
-// Measured, all launches: two sequences of 131071 keys, 32 heads on 8, d 128: 95 us
-// (5.7 TB/s, 85 % of a copy's rate); 96 sequences of up to 16384 keys, the same
-// heads: 236 us (5.8 TB/s); four of 4096 keys, 16 heads: 21.4 us, 3 of them the
-// join. What bounds it stands at step_ctas.
+// Measured, all launches of captured calls (a call by itself takes 1 to 2 us more):
+// two sequences of 131071 keys, 32 heads on 8, d 128: 95 us (5.7 TB/s, 85 % of a
+// copy's rate); 96 sequences of up to 16384 keys, the same heads: 235 us (5.8
+// TB/s); four of 4096 keys, 16 heads: 21.4 us, 3 of them the join. What bounds it
+// stands at step_ctas.
 #pragma once
 
 #include <cuda.h>

@@ -164,7 +164,11 @@ fa_status fa_cache_append(const void* k, const void* v, const fa_strides* stride
  * 2^-22 of itself (or 2^-22), and the weights of its block in proportion.
  * Up to three launches (a kernel for sequences of up to 16 rows to a K / V
  * head, one for more, and one that joins what they split), by the sizes that
- * the host knows. Deterministic: the same call gives the same bits.
+ * the host knows: with cu_q it does not know how the rows are spread. Where all
+ * sequences have the same number of query tokens, the call without cu_q spares a
+ * launch (16 x 5 tokens: 60 us in place of 70). A batch with cu_q and T <= B is
+ * taken for one of single tokens; a long piece in it is computed right, but at a
+ * third of its speed. Deterministic: the same call gives the same bits.
  */
 fa_status fa_fwd_cache(const void* q, const fa_cache* cache, const int32_t* block_table,
                        int table_width, const int32_t* kv_lens, const int32_t* cu_q, void* o,
