@@ -668,15 +668,18 @@ __device__ __forceinline__ void query_parts(const uint16_t* p, float fac, uint32
   }
 }
 
-// Whether row limit `lim` leaves a key of a block that exists in the share's tiles.
-__device__ __forceinline__ bool meets_a_key(const CacheAttnArgs& a, const ChunkWalk& w, int lim) {
-  const long long end = min(static_cast<long long>(lim), 1LL * w.real_end * kChunkKeys);
+// The first key of a block that exists in the share's tiles of the item (2^31 - 1:
+// none). Called by whole warps.
+__device__ __forceinline__ int first_key(const CacheAttnArgs& a, const ChunkWalk& w, int lane) {
   const int32_t* const table = a.table + static_cast<long long>(w.b) * a.table_width;
-  for (long long key = 1LL * w.t0 * kChunkKeys; key < end; key += 1LL << a.block_shift) {
-    const int id = __ldg(table + (key >> a.block_shift));
-    if (id >= 0 && id < a.num_blocks) return true;
+  const long long keys = min(static_cast<long long>(w.s.kv_len), 1LL * w.real_end * kChunkKeys);
+  const int end = static_cast<int>((keys + (1 << a.block_shift) - 1) >> a.block_shift);
+  for (int at = (w.t0 * kChunkKeys) >> a.block_shift; at < end; at += 32) {
+    const int id = at + lane < end ? __ldg(table + at + lane) : -1;
+    const uint32_t there = __ballot_sync(0xffffffffu, id >= 0 && id < a.num_blocks);
+    if (there != 0u) return (at + __ffs(static_cast<int>(there)) - 1) << a.block_shift;
   }
-  return false;
+  return 0x7FFFFFFF;
 }
 
 // The tiles of one item for a warpgroup: NC = 128, all keys of a tile for the rows
@@ -973,11 +976,14 @@ __device__ __forceinline__ void chunk_softmax_role(const CacheAttnArgs& a, const
         m_ref = top;
       }
       ptx::tc_fence_after();
-      // scores of NaN, which a row without a value has against the zeros of hidden
-      // blocks too
-      if (l != l && !meets_a_key(a, w, x.lim)) {
-        m_ref = -INFINITY;
-        l = 0.f;
+      // Scores of NaN, which a row without a value has against the zeros of hidden
+      // blocks too: where it sees no other keys they count for nothing.
+      if (__any_sync(0xffffffffu, l != l)) {
+        const int first = first_key(a, w, lane);
+        if (l != l && x.lim <= first) {
+          m_ref = -INFINITY;
+          l = 0.f;
+        }
       }
       const bool none = no_weight(m_ref, l);
       if (part == nullptr) {

@@ -165,6 +165,31 @@ def test_queries_without_a_value_that_see_no_key(n, d, dtype):
 
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
 @pytest.mark.parametrize("n,d", KERNELS)
+@pytest.mark.parametrize("hidden", [40, 3000])
+def test_queries_without_a_value_over_hidden_blocks(n, d, hidden, dtype):
+    """The first blocks of a sequence are hidden up to a key that only the later rows
+    see past: rows of NaN before it see nothing, those behind it give NaN, also where
+    the hidden keys and the others are other CTAs' shares."""
+    import torch
+    rng = np.random.default_rng(n + d)
+    first, bs = 16 * (hidden // 16), 16
+    keys = first + max(n // 2, 1)                     # row i sees keys - n + i + 1 of them
+    P = -(-keys // bs)
+    cache = small_cache(rng, P, 1, bs, d)
+    table = rng.permutation(P)[None]
+    table[0, :first // bs] = np.where(np.arange(first // bs) % 2, -1, P)
+    q = torch.from_numpy(rng.standard_normal((n, 1, d))).to(DEV).to(tdt(dtype))
+    q[::2, 0, 1] = float("nan")
+    o, lse = fa.attention_forward_cache(q, cache, ints(table), ints([keys]), ints([0, n]))
+    nan = torch.arange(n, device=DEV) % 2 == 0
+    sees = torch.arange(n, device=DEV) + keys - n + 1 > first
+    assert (o[~sees] == 0).all() and torch.isneginf(lse[~sees]).all()
+    assert torch.isnan(o[sees & nan]).all() and not torch.isfinite(lse[sees & nan]).any()
+    assert torch.isfinite(o[sees & ~nan]).all() and torch.isfinite(lse[sees & ~nan]).all()
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("n,d", KERNELS)
 def test_infinite_queries_whose_scores_are_all_minus_infinity(n, d, dtype):
     """An infinity against keys of one sign: every score is -inf, whose softmax has no
     value (and it is not a row without keys)."""
