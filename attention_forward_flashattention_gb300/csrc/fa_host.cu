@@ -64,6 +64,23 @@ EncodeTiledFn encode_fn() {
   return g_encode;
 }
 
+// cuTensorMapEncodeTiled with these arguments. It needs a current context, which a
+// host thread has only once a runtime call has worked on the device (cudaGetDevice
+// does not): a thread whose first such call is one of ours, as autograd's may be,
+// gets it here.
+template <typename... Args>
+bool encode_tiled(Args... args) {
+  const EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  CUresult r = enc(args...);
+  if (r == CUDA_ERROR_INVALID_CONTEXT) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) return false;
+    r = enc(args...);
+  }
+  return r == CUDA_SUCCESS;
+}
+
 // Device facts for the current device; allocates its status word on first use.
 fa_status current_device(int* dev_out, DeviceState** st_out, bool need_status) {
   int dev = 0;
@@ -100,8 +117,6 @@ fa_status current_device(int* dev_out, DeviceState** st_out, bool need_status) {
 // 128-byte swizzle. Rows past N read as zero.
 bool encode_qkv(CUtensorMap* m, const void* ptr, const fa_strides& st, bool bf16, int B, int H,
                 int N, int d, int box_rows) {
-  EncodeTiledFn enc = encode_fn();
-  if (!enc) return false;
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(N),
                               static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(B)};
   const cuuint64_t strides[3] = {static_cast<cuuint64_t>(st.n) * 2u,
@@ -109,10 +124,10 @@ bool encode_qkv(CUtensorMap* m, const void* ptr, const fa_strides& st, bool bf16
                                  static_cast<cuuint64_t>(st.b) * 2u};
   const cuuint32_t box[4] = {64u, static_cast<cuuint32_t>(box_rows), 1u, 1u};
   const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
-  return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+  return encode_tiled(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
              const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 // A 4-D byte tensor (e4m3 codes) {dims[0] (contiguous), dims[1], dims[2],
@@ -120,13 +135,11 @@ bool encode_qkv(CUtensorMap* m, const void* ptr, const fa_strides& st, bool bf16
 // 128-byte swizzle. Elements past dims[0] / dims[1] read as zero.
 bool encode_bytes4(CUtensorMap* m, const void* ptr, const cuuint64_t (&dims)[4],
                    const cuuint64_t (&strides)[3], cuuint32_t box_rows = 128u) {
-  EncodeTiledFn enc = encode_fn();
-  if (!enc) return false;
   const cuuint32_t box[4] = {128u, box_rows, 1u, 1u};
   const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(ptr), dims, strides, box, estr,
+  return encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(ptr), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -145,8 +158,6 @@ __global__ void clock_probe_kernel(uint64_t* out, long long cycles) {
 }  // namespace
 
 bool encode_cache(CUtensorMap* m, const void* codes, const fa_cache& c, int rows, bool swizzle) {
-  EncodeTiledFn enc = encode_fn();
-  if (!enc) return false;
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.d), static_cast<cuuint64_t>(c.block),
                               static_cast<cuuint64_t>(c.Hkv),
                               static_cast<cuuint64_t>(c.num_blocks)};
@@ -155,11 +166,11 @@ bool encode_cache(CUtensorMap* m, const void* codes, const fa_cache& c, int rows
                                  static_cast<cuuint64_t>(c.block_stride)};
   const cuuint32_t box[4] = {static_cast<cuuint32_t>(c.d), static_cast<cuuint32_t>(rows), 1u, 1u};
   const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(codes), dims, strides, box,
+  return encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(codes), dims, strides, box,
              estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
              !swizzle ? CU_TENSOR_MAP_SWIZZLE_NONE
                       : c.d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 fa_status device_facts(int* sm_count, uint32_t** status) {
