@@ -105,8 +105,9 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.fa_version.argtypes = []
         lib.fa_version.restype = i
         if hasattr(lib, "fa_fwd_cache"):
-            from . import cache
+            from . import cache, rope
             cache.bind(lib)
+            rope.bind(lib)
         if path is None:
             _lib = lib
         return lib
@@ -481,3 +482,9 @@ from .cache import (Cache, FaCache, attention_forward_cache,  # noqa: E402,F401
                     attention_forward_cache_into, cache_append, cache_empty, cache_plan,
                     cache_plan_into, fa_cache_append, fa_cache_plan, fa_fwd_cache,
                     fa_fwd_cache_workspace_size)
+
+# ------------------------------------------------------------ norm and rotation (include/fa_rope.h)
+
+from .rope import (FaRope, fa_qk_norm_rope, fa_qk_norm_rope_bwd,  # noqa: E402,F401
+                   fa_qk_norm_rope_bwd_workspace_size, qk_norm_rope, qk_norm_rope_backward,
+                   qk_norm_rope_forward, qk_norm_rope_forward_into, rope_table)

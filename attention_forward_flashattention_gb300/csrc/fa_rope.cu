@@ -1,0 +1,529 @@
+// fa_qk_norm_rope and its gradients (include/fa_rope.h): kernels, argument
+// checks, launches.
+//
+// Every element is read and written once, with some ten operations, so HBM
+// bounds both directions. d / 8 lanes share a row of d elements: a lane holds
+// four elements and the four that they are paired with, so that the rotation
+// needs no other lane and the norm one sum over the lanes. A lane group takes
+// the same token of several heads, one after another in batches of kBatch rows
+// whose loads are under way together: cosines, sines and weights are then read
+// once for all of them.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "fa_cache.cuh"
+#include "fa_check.h"
+#include "fa_rope.h"
+
+namespace fa {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kBatch = 4;  // rows of a lane group under way together
+
+struct RowsOf {  // q or k: its heads, and element strides of each operand
+  const uint16_t* x;
+  const uint16_t* dy;  // backward
+  uint16_t* out;       // y, or dx
+  fa_strides xs, dys, outs;
+  const void* weight;
+  int heads;
+};
+
+struct RopeArgs {
+  RowsOf of[2];  // q, k
+  const float* table;
+  const int32_t* positions;
+  long long positions_b;
+  int n_positions, rotary, interleaved, weights_fp32;
+  int B, N;
+  int per_unit;       // heads that a lane group takes
+  int chunks[2];      // units of a token, of q and of k
+  int heads_inner;    // neighbouring units: chunks of one token, or tokens of one chunk
+  long long units;    // B * N * (chunks[0] + chunks[1])
+  float eps;
+  float* partial;  // backward: [CTAs][2][d]
+};
+
+template <bool BF16>
+__device__ __forceinline__ float2 widen(uint32_t w) {
+  if constexpr (BF16) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  } else {
+    __half2 h;
+    __builtin_memcpy(&h, &w, 4);
+    return __half22float2(h);
+  }
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t narrow(float lo, float hi) {
+  uint32_t w;
+  if constexpr (BF16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    __builtin_memcpy(&w, &v, 4);
+  } else {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    __builtin_memcpy(&w, &v, 4);
+  }
+  return w;
+}
+
+// Eight elements of a row that a lane holds: four and their partners (half a
+// row apart), or four neighbouring pairs.
+struct Eight {
+  uint2 lo, hi;
+};
+template <bool BF16>
+__device__ __forceinline__ void widen8(const Eight& e, float (&f)[8]) {
+  const uint32_t w[4] = {e.lo.x, e.lo.y, e.hi.x, e.hi.y};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = widen<BF16>(w[i]);
+    f[2 * i] = v.x;
+    f[2 * i + 1] = v.y;
+  }
+}
+template <bool BF16>
+__device__ __forceinline__ Eight narrow8(const float (&f)[8]) {
+  return {make_uint2(narrow<BF16>(f[0], f[1]), narrow<BF16>(f[2], f[3])),
+          make_uint2(narrow<BF16>(f[4], f[5]), narrow<BF16>(f[6], f[7]))};
+}
+
+// Where a lane's two fours lie in a row.
+struct Place {
+  int lo, hi;
+  int pair;  // its first pair's cosine, -1: not turned
+};
+template <int D>
+__device__ __forceinline__ Place place_of(const RopeArgs& a, int lane) {
+  const int p = 4 * lane, half = a.rotary >> 1;
+  if (a.interleaved) return {2 * p, 2 * p + 4, p < half ? p : -1};
+  if (p < half) return {p, p + half, p};
+  return {a.rotary + p - half, a.rotary + (D - a.rotary) / 2 + p - half, -1};
+}
+
+// Cosines and sines of a lane's four pairs.
+struct Turn {
+  float4 c, s;
+};
+__device__ __forceinline__ Turn turn_of(const RopeArgs& a, const Place& w, int b, int n) {
+  Turn t{make_float4(1.f, 1.f, 1.f, 1.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+  if (w.pair >= 0) {
+    const int p = min(max(__ldg(a.positions + b * a.positions_b + n), 0), a.n_positions - 1);
+    const float* row = a.table + static_cast<long long>(p) * a.rotary + w.pair;
+    t.c = __ldg(reinterpret_cast<const float4*>(row));
+    t.s = __ldg(reinterpret_cast<const float4*>(row + (a.rotary >> 1)));
+  }
+  return t;
+}
+// Turns the four pairs of f by the angles (kBack: by their opposites).
+template <bool INTERLEAVED, bool kBack>
+__device__ __forceinline__ void rotate(float (&f)[8], const Turn& t) {
+  const float c[4] = {t.c.x, t.c.y, t.c.z, t.c.w}, s[4] = {t.s.x, t.s.y, t.s.z, t.s.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int x = INTERLEAVED ? 2 * i : i, y = INTERLEAVED ? 2 * i + 1 : i + 4;
+    const float u = f[x], v = f[y], sn = kBack ? -s[i] : s[i];
+    f[x] = u * c[i] - v * sn;
+    f[y] = v * c[i] + u * sn;
+  }
+}
+
+template <bool BF16>
+__device__ __forceinline__ void weights_of(const RopeArgs& a, const void* w, const Place& at,
+                                           float (&f)[8]) {
+  if (w == nullptr) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = 1.f;
+  } else if (a.weights_fp32) {
+    const float* p = static_cast<const float*>(w);
+    const float4 x = __ldg(reinterpret_cast<const float4*>(p + at.lo));
+    const float4 y = __ldg(reinterpret_cast<const float4*>(p + at.hi));
+    f[0] = x.x, f[1] = x.y, f[2] = x.z, f[3] = x.w;
+    f[4] = y.x, f[5] = y.y, f[6] = y.z, f[7] = y.w;
+  } else {
+    const uint16_t* p = static_cast<const uint16_t*>(w);
+    widen8<BF16>({__ldg(reinterpret_cast<const uint2*>(p + at.lo)),
+                  __ldg(reinterpret_cast<const uint2*>(p + at.hi))}, f);
+  }
+}
+
+// (plain loads: an output may be its input)
+__device__ __forceinline__ Eight load8(const uint16_t* row, const Place& at) {
+  return {*reinterpret_cast<const uint2*>(row + at.lo), *reinterpret_cast<const uint2*>(row + at.hi)};
+}
+__device__ __forceinline__ void store8(uint16_t* row, const Place& at, const Eight& e) {
+  *reinterpret_cast<uint2*>(row + at.lo) = e.lo;
+  *reinterpret_cast<uint2*>(row + at.hi) = e.hi;
+}
+
+// Sum over the L lanes of a group.
+template <int L>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+struct Unit {
+  int b, n, which, h0, h1;
+};
+__device__ __forceinline__ Unit unit_of(const RopeArgs& a, long long u) {
+  const int chunks = a.chunks[0] + a.chunks[1];
+  const long long tokens = static_cast<long long>(a.B) * a.N;
+  long long token;
+  int chunk;
+  if (a.heads_inner) {
+    token = u / chunks;
+    chunk = static_cast<int>(u - token * chunks);
+  } else {
+    chunk = static_cast<int>(u / tokens);
+    token = u - chunk * tokens;
+  }
+  Unit r;
+  r.b = static_cast<int>(token / a.N);
+  r.n = static_cast<int>(token - static_cast<long long>(r.b) * a.N);
+  r.which = chunk >= a.chunks[0];
+  r.h0 = (chunk - (r.which ? a.chunks[0] : 0)) * a.per_unit;
+  r.h1 = min(r.h0 + a.per_unit, a.of[r.which].heads);
+  return r;
+}
+__device__ __forceinline__ long long row_at(const fa_strides& s, const Unit& u, int h) {
+  return u.b * s.b + h * s.h + u.n * s.n;
+}
+
+template <int D, bool BF16, bool INTERLEAVED>
+__global__ void __launch_bounds__(kThreads) fa_norm_rope_kernel(const RopeArgs a) {
+  constexpr int L = D / 8;
+  const int lane = static_cast<int>(threadIdx.x) % L;
+  const long long u = static_cast<long long>(blockIdx.x) * (kThreads / L) + threadIdx.x / L;
+  // (a group without a unit takes part in the sums)
+  const bool there = u < a.units;
+  const Unit w = unit_of(a, there ? u : 0);
+  const RowsOf& o = a.of[w.which];
+  const Place at = place_of<D>(a, lane);
+  const Turn turn = turn_of(a, at, w.b, w.n);
+  float wt[8];
+  weights_of<BF16>(a, o.weight, at, wt);
+  const int steps = (a.per_unit + kBatch - 1) / kBatch;  // (the same for all groups of a warp)
+  for (int step = 0; step < steps; ++step) {
+    const int h0 = w.h0 + step * kBatch;
+    Eight x[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      x[i] = {make_uint2(0u, 0u), make_uint2(0u, 0u)};
+      if (there && h0 + i < w.h1) x[i] = load8(o.x + row_at(o.xs, w, h0 + i), at);
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      float f[8];
+      widen8<BF16>(x[i], f);
+      float sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum = fmaf(f[e], f[e], sum);
+      const float inv = rsqrtf(fmaf(group_sum<L>(sum), 1.f / D, a.eps));
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = f[e] * inv * wt[e];
+      rotate<INTERLEAVED, false>(f, turn);
+      if (there && h0 + i < w.h1) store8(o.out + row_at(o.outs, w, h0 + i), at, narrow8<BF16>(f));
+    }
+  }
+}
+
+// dx, and each CTA's sum for the weights.
+template <int D, bool BF16, bool INTERLEAVED>
+__global__ void __launch_bounds__(kThreads) fa_norm_rope_bwd_kernel(const RopeArgs a) {
+  constexpr int L = D / 8, kGroups = kThreads / L;
+  __shared__ float s_sum[kGroups][D];
+  const int lane = static_cast<int>(threadIdx.x) % L, group = static_cast<int>(threadIdx.x) / L;
+  const Place at = place_of<D>(a, lane);
+  float dw[2][8] = {};
+  const long long step_units = static_cast<long long>(gridDim.x) * kGroups;
+  for (long long u0 = static_cast<long long>(blockIdx.x) * kGroups; u0 < a.units; u0 += step_units) {
+    const long long u = u0 + group;
+    const bool there = u < a.units;
+    const Unit w = unit_of(a, there ? u : 0);
+    const RowsOf& o = a.of[w.which];
+    const Turn turn = turn_of(a, at, w.b, w.n);
+    float wt[8], add[8] = {};
+    weights_of<BF16>(a, o.weight, at, wt);
+    const int steps = (a.per_unit + kBatch - 1) / kBatch;
+    for (int step = 0; step < steps; ++step) {
+      const int h0 = w.h0 + step * kBatch;
+      Eight x[kBatch], dy[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        x[i] = dy[i] = {make_uint2(0u, 0u), make_uint2(0u, 0u)};
+        if (there && h0 + i < w.h1) {
+          x[i] = load8(o.x + row_at(o.xs, w, h0 + i), at);
+          dy[i] = load8(o.dy + row_at(o.dys, w, h0 + i), at);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        float f[8], t[8];
+        widen8<BF16>(x[i], f);
+        widen8<BF16>(dy[i], t);
+        rotate<INTERLEAVED, true>(t, turn);
+        float sum = 0.f, dot = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          sum = fmaf(f[e], f[e], sum);
+          dot = fmaf(t[e] * wt[e], f[e], dot);
+        }
+        sum = group_sum<L>(sum);
+        dot = group_sum<L>(dot);
+        const float inv = rsqrtf(fmaf(sum, 1.f / D, a.eps));
+        const float mean = dot * inv * (1.f / D);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float n = f[e] * inv;
+          add[e] = fmaf(t[e], n, add[e]);
+          f[e] = inv * fmaf(-n, mean, t[e] * wt[e]);
+        }
+        if (there && h0 + i < w.h1) store8(o.out + row_at(o.outs, w, h0 + i), at, narrow8<BF16>(f));
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      dw[0][e] += w.which ? 0.f : add[e];
+      dw[1][e] += w.which ? add[e] : 0.f;
+    }
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (a.partial == nullptr) return;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s_sum[group][(e < 4 ? at.lo + e : at.hi + e - 4)] = dw[k][e];
+    __syncthreads();
+    for (int c = static_cast<int>(threadIdx.x); c < D; c += kThreads) {
+      float v = 0.f;
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) v += s_sum[g][c];
+      a.partial[(static_cast<long long>(blockIdx.x) * 2 + k) * D + c] = v;
+    }
+  }
+}
+
+// The CTAs' sums together: a CTA for 32 columns of dq_weight or dk_weight, eight
+// warps that each take every eighth part.
+template <int D>
+__global__ void __launch_bounds__(256)
+    fa_norm_rope_join_kernel(const float* partial, int parts, float* dq_weight, float* dk_weight) {
+  __shared__ float s_sum[8][32];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
+  const int col = static_cast<int>(blockIdx.x) * 32 + lane;  // of [2][D]
+  float v = 0.f;
+#pragma unroll 8
+  for (int p = warp; p < parts; p += 8) v += __ldcg(partial + static_cast<long long>(p) * 2 * D + col);
+  s_sum[warp][lane] = v;
+  __syncthreads();
+  if (warp != 0) return;
+#pragma unroll
+  for (int w = 1; w < 8; ++w) v += s_sum[w][lane];
+  float* const out = col < D ? dq_weight : dk_weight;
+  if (out != nullptr) out[col < D ? col : col - D] = v;
+}
+
+constexpr int kBwdCtas = 4;  // on an SM
+
+fa_status check_rope(const fa_rope* r, int d) {
+  if (!r || !r->table || !r->positions) return FA_ERR_INVALID_ARG;
+  if (!aligned(r->table, 16) || !aligned(r->positions, 4) || !aligned(r->q_weight, 16) ||
+      !aligned(r->k_weight, 16))
+    return FA_ERR_INVALID_ARG;
+  if (r->n_positions <= 0 || r->positions_b < 0) return FA_ERR_INVALID_ARG;
+  if (r->rotary_dim < 8 || r->rotary_dim > d || (r->rotary_dim & 7) != 0) return FA_ERR_INVALID_ARG;
+  if (!(std::isfinite(r->eps) && r->eps > 0.f)) return FA_ERR_INVALID_ARG;
+  return FA_OK;
+}
+
+fa_status check_shape(int B, int H, int Hkv, int N, int d, fa_dtype dtype, const fa_strides* strides,
+                      int n_strides) {
+  if (B <= 0 || H <= 0 || Hkv <= 0 || N < 0 || !strides) return FA_ERR_INVALID_ARG;
+  if (dtype != FA_DTYPE_FP16 && dtype != FA_DTYPE_BF16) return FA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  for (int i = 0; i < n_strides; ++i)
+    for (const long long s : {strides[i].b, strides[i].h, strides[i].n}) {
+      const fa_status ss = check_stride(s);
+      if (ss != FA_OK) return ss;
+    }
+  // (each factor is below 2^31, so that no product of two passes 2^63)
+  const long long heads = static_cast<long long>(H) + Hkv, tokens = static_cast<long long>(B) * N;
+  if (heads > 0x7FFFFFFFLL || tokens > 0x7FFFFFFFLL || tokens * heads > 0x7FFFFFFFLL)
+    return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+
+RopeArgs common(const fa_rope& r, int B, int N, int H, int Hkv, const fa_strides& q) {
+  RopeArgs a{};
+  a.of[0].weight = r.q_weight;
+  a.of[1].weight = r.k_weight;
+  a.of[0].heads = H;
+  a.of[1].heads = Hkv;
+  a.table = r.table;
+  a.positions = r.positions;
+  a.positions_b = r.positions_b;
+  a.n_positions = r.n_positions;
+  a.rotary = r.rotary_dim;
+  a.interleaved = r.interleaved != 0;
+  a.weights_fp32 = r.weights_fp32 != 0;
+  a.B = B;
+  a.N = N;
+  a.heads_inner = q.h < q.n;
+  a.eps = r.eps;
+  return a;
+}
+
+// Heads of a unit: as many as leave every SM `groups` lane groups to run.
+void split(RopeArgs& a, int most, long long groups) {
+  const long long tokens = static_cast<long long>(a.B) * a.N;
+  int per = most;
+  auto units = [&](int p) {
+    return tokens * ((a.of[0].heads + p - 1) / p + (a.of[1].heads + p - 1) / p);
+  };
+  while (per > 1 && units(per) < groups) per >>= 1;
+  a.per_unit = per;
+  for (int i = 0; i < 2; ++i) a.chunks[i] = (a.of[i].heads + per - 1) / per;
+  a.units = units(per);
+}
+
+template <int D, bool BF16>
+cudaError_t launch_forward(const RopeArgs& a, cudaStream_t s) {
+  constexpr int kGroups = kThreads / (D / 8);
+  const unsigned grid = static_cast<unsigned>((a.units + kGroups - 1) / kGroups);
+  if (a.interleaved) fa_norm_rope_kernel<D, BF16, true><<<grid, kThreads, 0, s>>>(a);
+  else fa_norm_rope_kernel<D, BF16, false><<<grid, kThreads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <int D, bool BF16>
+cudaError_t launch_backward(const RopeArgs& a, int most, float* dqw, float* dkw, cudaStream_t s) {
+  constexpr int kGroups = kThreads / (D / 8);
+  const long long want = (a.units + kGroups - 1) / kGroups;
+  const unsigned grid = static_cast<unsigned>(want < most ? want : most);
+  if (a.interleaved) fa_norm_rope_bwd_kernel<D, BF16, true><<<grid, kThreads, 0, s>>>(a);
+  else fa_norm_rope_bwd_kernel<D, BF16, false><<<grid, kThreads, 0, s>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || a.partial == nullptr) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(2 * D / 32);
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fa_norm_rope_join_kernel<D>, static_cast<const float*>(a.partial),
+                            static_cast<int>(grid), dqw, dkw);
+}
+
+}  // namespace
+}  // namespace fa
+
+extern "C" {
+
+fa_status fa_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out, int B, int H,
+                          int Hkv, int N, int d, const fa_strides* strides, const fa_rope* rope,
+                          fa_dtype dtype, void* stream) {
+  for (const void* p : {q, k, static_cast<const void*>(q_out), static_cast<const void*>(k_out)})
+    if (!p || !fa::aligned(p, 16)) return FA_ERR_INVALID_ARG;
+  const fa_status cs = fa::check_shape(B, H, Hkv, N, d, dtype, strides, 4);
+  if (cs == FA_ERR_INVALID_ARG) return cs;
+  const fa_status cr = fa::check_rope(rope, d);
+  if (cr != FA_OK) return cr;
+  if (cs != FA_OK) return cs;
+  int sms = 0;
+  const fa_status ds = fa::device_facts(&sms, nullptr);
+  if (ds != FA_OK) return ds;
+  if (N == 0) return FA_OK;
+  fa::RopeArgs a = fa::common(*rope, B, N, H, Hkv, strides[0]);
+  const void* in[2] = {q, k};
+  void* out[2] = {q_out, k_out};
+  for (int i = 0; i < 2; ++i) {
+    a.of[i].x = static_cast<const uint16_t*>(in[i]);
+    a.of[i].out = static_cast<uint16_t*>(out[i]);
+    a.of[i].xs = strides[i];
+    a.of[i].outs = strides[2 + i];
+  }
+  fa::split(a, 8, 2048LL / (d / 8) * sms);
+  (void)cudaGetLastError();
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool bf16 = dtype == FA_DTYPE_BF16;
+  const cudaError_t e = d == 64 ? (bf16 ? fa::launch_forward<64, true>(a, s) : fa::launch_forward<64, false>(a, s))
+                                : (bf16 ? fa::launch_forward<128, true>(a, s) : fa::launch_forward<128, false>(a, s));
+  return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+fa_status fa_qk_norm_rope_bwd_workspace_size(int d, size_t* bytes) {
+  if (!bytes) return FA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  int sms = 0;
+  const fa_status ds = fa::device_facts(&sms, nullptr);
+  if (ds != FA_OK) return ds;
+  *bytes = sizeof(float) * 2 * static_cast<size_t>(d) * static_cast<size_t>(sms * fa::kBwdCtas);
+  return FA_OK;
+}
+
+fa_status fa_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q, const void* k,
+                              void* dq, void* dk, float* dq_weight, float* dk_weight, int B, int H,
+                              int Hkv, int N, int d, const fa_strides* strides, const fa_rope* rope,
+                              fa_dtype dtype, void* workspace, size_t workspace_size, void* stream) {
+  for (const void* p : {dq_out, dk_out, q, k, static_cast<const void*>(dq), static_cast<const void*>(dk)})
+    if (!p || !fa::aligned(p, 16)) return FA_ERR_INVALID_ARG;
+  if (!fa::aligned(dq_weight, 4) || !fa::aligned(dk_weight, 4) || !fa::aligned(workspace, 16))
+    return FA_ERR_INVALID_ARG;
+  const bool sums = dq_weight != nullptr || dk_weight != nullptr;
+  if ((sums && !workspace) || (sums && dq_weight == dk_weight)) return FA_ERR_INVALID_ARG;
+  const fa_status cs = fa::check_shape(B, H, Hkv, N, d, dtype, strides, 6);
+  if (cs == FA_ERR_INVALID_ARG) return cs;
+  const fa_status cr = fa::check_rope(rope, d);
+  if (cr != FA_OK) return cr;
+  if (cs != FA_OK) return cs;
+  size_t need = 0;
+  const fa_status ws = fa_qk_norm_rope_bwd_workspace_size(d, &need);
+  if (ws != FA_OK) return ws;
+  if (sums && workspace_size < need) return FA_ERR_INVALID_ARG;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  (void)cudaGetLastError();
+  if (N == 0) {
+    for (float* w : {dq_weight, dk_weight})
+      if (w && cudaMemsetAsync(w, 0, sizeof(float) * static_cast<size_t>(d), s) != cudaSuccess) return FA_ERR_CUDA;
+    return FA_OK;
+  }
+  int sms = 0;
+  const fa_status ds = fa::device_facts(&sms, nullptr);
+  if (ds != FA_OK) return ds;
+  fa::RopeArgs a = fa::common(*rope, B, N, H, Hkv, strides[2]);
+  const void* x[2] = {q, k};
+  const void* dy[2] = {dq_out, dk_out};
+  void* out[2] = {dq, dk};
+  for (int i = 0; i < 2; ++i) {
+    a.of[i].x = static_cast<const uint16_t*>(x[i]);
+    a.of[i].dy = static_cast<const uint16_t*>(dy[i]);
+    a.of[i].out = static_cast<uint16_t*>(out[i]);
+    a.of[i].dys = strides[i];
+    a.of[i].xs = strides[2 + i];
+    a.of[i].outs = strides[4 + i];
+  }
+  a.partial = sums ? static_cast<float*>(workspace) : nullptr;
+  fa::split(a, 8, 2048LL / (d / 8) * sms);
+  const int most = sms * fa::kBwdCtas;
+  const bool bf16 = dtype == FA_DTYPE_BF16;
+  const cudaError_t e =
+      d == 64 ? (bf16 ? fa::launch_backward<64, true>(a, most, dq_weight, dk_weight, s)
+                      : fa::launch_backward<64, false>(a, most, dq_weight, dk_weight, s))
+              : (bf16 ? fa::launch_backward<128, true>(a, most, dq_weight, dk_weight, s)
+                      : fa::launch_backward<128, false>(a, most, dq_weight, dk_weight, s));
+  return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+}  // extern "C"
