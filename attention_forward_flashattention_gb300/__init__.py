@@ -105,8 +105,9 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.fa_version.argtypes = []
         lib.fa_version.restype = i
         if hasattr(lib, "fa_fwd_cache"):
-            from . import cache, rope
+            from . import cache, draft, rope
             cache.bind(lib)
+            draft.bind(lib)
             rope.bind(lib)
         if path is None:
             _lib = lib
@@ -482,6 +483,12 @@ from .cache import (Cache, FaCache, attention_forward_cache,  # noqa: E402,F401
                     attention_forward_cache_into, cache_append, cache_empty, cache_plan,
                     cache_plan_into, fa_cache_append, fa_cache_plan, fa_fwd_cache,
                     fa_fwd_cache_workspace_size)
+
+# ------------------------------------------------------------ trees of drafted tokens (include/fa_draft.h)
+
+from .draft import (attention_forward_cache_tree,  # noqa: E402,F401
+                    attention_forward_cache_tree_into, cache_tree, cache_tree_into, fa_cache_tree,
+                    fa_fwd_cache_tree)
 
 # ------------------------------------------------------------ norm and rotation (include/fa_rope.h)
 

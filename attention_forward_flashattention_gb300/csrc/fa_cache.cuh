@@ -77,6 +77,8 @@ struct CacheAttnArgs {
   long long block_stride, head_stride, token_stride;
   int B, T, H, Hkv, group, n_uniform, table_width, num_blocks, block_shift;
   int causal;
+  const unsigned long long* masks;  // fa_fwd_cache_tree: [T][words] (causal is 0 then)
+  int words;
   float scale_log2;  // scale * log2(e)
   uint32_t* status;
   // sequences of more than rows_over and at most rows_upto rows to a K / V head
@@ -93,6 +95,9 @@ cudaError_t launch_cache_append(const CacheAppendArgs& a, int block, int d, bool
 // False in *mapped: a tensor map could not be encoded.
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, const fa_cache& c, bool bf16, int sm_count,
                               float* ws, cudaStream_t stream, bool* mapped);
+// The same with a.masks.
+cudaError_t launch_cache_tree_attn(const CacheAttnArgs& a, const fa_cache& c, bool bf16,
+                                   int sm_count, float* ws, cudaStream_t stream, bool* mapped);
 
 // fa_host.cu: a cache's K or V as a 4-D byte map {d, token in block, head,
 // block}; box = `rows` tokens of one head and block, swizzled over its d bytes
@@ -132,6 +137,55 @@ __device__ __forceinline__ SeqRows seq_rows(const CacheAttnArgs& a, int b) {
 __device__ __forceinline__ bool takes_seq(const CacheAttnArgs& a, const SeqRows& s) {
   const long long rows = static_cast<long long>(s.count) * a.group;
   return rows > a.rows_over && rows <= a.rows_upto;
+}
+
+// Trees (fa_fwd_cache_tree). Drafted token c of a sequence is key kv_len - count + c,
+// so keys below that difference, which may be negative, are seen by all rows.
+
+// Word w of the mask of query row `row`.
+__device__ __forceinline__ unsigned long long mask_word(const CacheAttnArgs& a, int row, int w) {
+  return w < a.words ? __ldg(a.masks + static_cast<long long>(row) * a.words + w) : 0ull;
+}
+// Whether row `row` sees a key (row < 0: there is none).
+__device__ __forceinline__ bool tree_sees(const CacheAttnArgs& a, const SeqRows& s, int row,
+                                          int key) {
+  const int c = key - (s.kv_len - s.count);
+  if (row < 0 || key >= s.kv_len) return false;
+  return c < 0 || ((mask_word(a, row, c >> 6) >> (c & 63)) & 1ull) != 0ull;
+}
+// The keys from `key` on that row `row` sees, as the bits of a word.
+__device__ __forceinline__ unsigned long long tree_seen64(const CacheAttnArgs& a, int kv_len,
+                                                          int behind, int row, int key) {
+  const int left = kv_len - key, c = key - behind;
+  if (left <= 0) return 0ull;
+  unsigned long long v = ~0ull;
+  if (c > -64) {
+    const int w = c >> 6, sh = c & 63;  // (c < 0: word -1 is the context, all ones)
+    v = (w < 0 ? ~0ull : mask_word(a, row, w)) >> sh;
+    if (sh != 0) v |= mask_word(a, row, w + 1) << (64 - sh);
+  }
+  return left < 64 ? v & ((1ull << left) - 1ull) : v;
+}
+// The block of a key, -1 if the table lists none.
+__device__ __forceinline__ int block_of(const CacheAttnArgs& a, int b, int key) {
+  const int id = __ldg(a.table + static_cast<long long>(b) * a.table_width + (key >> a.block_shift));
+  return id < a.num_blocks ? id : -1;
+}
+// Whether column `col` of V is NaN in a drafted key that row `row` sees. Only asked
+// where NaN was found among the drafted keys.
+__device__ __forceinline__ bool tree_nan(const CacheAttnArgs& a, int b, int hk, const SeqRows& s,
+                                         int row, int col) {
+  const int behind = s.kv_len - s.count;
+#pragma unroll 1
+  for (int key = max(behind, 0); key < s.kv_len; ++key) {
+    if (!tree_sees(a, s, row, key)) continue;
+    const int id = block_of(a, b, key);
+    if (id < 0) continue;
+    const uint8_t v = a.v[id * a.block_stride + hk * a.head_stride +
+                          (key & ((1 << a.block_shift) - 1)) * a.token_stride + col];
+    if ((v & 0x7F) == 0x7F) return true;
+  }
+  return false;
 }
 
 // Element offsets of query row i of sequence b, head h, in q / o, and its LSE index.

@@ -119,6 +119,12 @@ __device__ __forceinline__ int keys_seen(const CacheAttnArgs& a, const SeqRows& 
   return a.causal ? min(max(s.kv_len - s.count + i + 1, 0), s.kv_len) : s.kv_len;
 }
 
+// Keys that every row of an item sees whose first row is that of query token i.
+template <bool TREE>
+__device__ __forceinline__ int keys_all_see(const CacheAttnArgs& a, const SeqRows& s, int i) {
+  return TREE ? max(s.kv_len - s.count, 0) : keys_seen(a, s, i);
+}
+
 // Row blocks of a sequence, and the tiles that one of them reads (counted: at
 // least one, so that rows without keys are written).
 __device__ __forceinline__ int chunk_row_blocks(const CacheAttnArgs& a, const SeqRows& s) {
@@ -314,7 +320,7 @@ __device__ __forceinline__ void chunk_copy_role(const CUtensorMap* tm_k, const C
 
 // ---- converters: warps 12-15. A thread takes 16 codes of a row at a time: 32
 // bytes in two chunks of one of the row's 128-byte panels.
-template <int D, int PARTS>
+template <int D, int PARTS, bool TREE>
 __device__ __forceinline__ void chunk_convert_role(const CacheAttnArgs& a, ChunkWalk w,
                                                    uint8_t* sgen, uint32_t sbase, uint32_t bars,
                                                    const AbortCtx& ab, int warp, int lane) {
@@ -346,7 +352,7 @@ __device__ __forceinline__ void chunk_convert_role(const CacheAttnArgs& a, Chunk
   uint32_t ring = 0, count = 0;  // slots filled, tiles done
   bool ok = true;
   do {
-    const int first_seen = keys_seen(
+    const int first_seen = keys_all_see<TREE>(
         a, w.s, static_cast<int>(static_cast<long long>(w.rb) * a.item_rows / a.group));
     const int halves = L::kHalves * max(0, w.real_end - w.t0);  // (K and) V of each tile
 #pragma unroll 1
@@ -682,6 +688,19 @@ __device__ __forceinline__ int first_key(const CacheAttnArgs& a, const ChunkWalk
   return 0x7FFFFFFF;
 }
 
+// Whether a row sees a key of a block that exists in the share's tiles of the item,
+// of which `first` is the first one.
+__device__ __forceinline__ bool tree_sees_block(const CacheAttnArgs& a, const ChunkWalk& w, int row,
+                                                int first) {
+  const long long end = min(static_cast<long long>(w.s.kv_len), 1LL * w.real_end * kChunkKeys);
+#pragma unroll 1
+  for (int key = first; key < end; ++key) {
+    if (!tree_sees(a, w.s, row, key)) continue;
+    if (block_of(a, w.b, key) >= 0) return true;
+  }
+  return false;
+}
+
 // The tiles of one item for a warpgroup: NC = 128, all keys of a tile for the rows
 // of Q tile `wg` (pair mode), or NC = 64, half `wg` of the keys (split mode).
 // S of tile j is in S_wg, or in that half of S_(j mod 2); P goes over it.
@@ -689,11 +708,12 @@ struct TileLoop {
   uint32_t tl, phase;  // tensor memory of the warp's lanes; parities (chunk_softmax_role)
   int wg, n, k0;       // tiles of the item, first key
   uint32_t count;      // tiles before the item
-  int lim, lim0;       // keys that the row and that all rows see
+  int lim, lim0;       // keys that the row and that all rows see (TREE: its mask's row; the
+  int kv_len;          // keys before the drafted ones, which may be negative), all keys
   float crow;
   bool idle;
 };
-template <int D, int NC, int PARTS>
+template <int D, int NC, int PARTS, bool TREE>
 __device__ __forceinline__ bool softmax_tiles(const CacheAttnArgs& a, const TileLoop& x,
                                               const uint8_t* sgen, uint32_t bars,
                                               const AbortCtx& ab, float& m_ref, float& l) {
@@ -748,9 +768,20 @@ __device__ __forceinline__ bool softmax_tiles(const CacheAttnArgs& a, const Tile
       m_tile = fmaf(fmaxf(mx_lo, mx_hi), f.x, f.y);
     } else {
       if (need_mask) {
-        const int see = x.lim - k0;
+        if constexpr (TREE) {
 #pragma unroll
-        for (int c = 0; c < NC; ++c) s[c] = c < see ? s[c] : -INFINITY;
+          for (int h = 0; h < NC / 64; ++h) {
+            const unsigned long long v = tree_seen64(a, x.kv_len, x.lim0, x.lim, k0 + 64 * h);
+            const uint32_t part[2] = {static_cast<uint32_t>(v), static_cast<uint32_t>(v >> 32)};
+#pragma unroll
+            for (int c = 0; c < 64; ++c)
+              s[64 * h + c] = (part[c >> 5] >> (c & 31)) & 1u ? s[64 * h + c] : -INFINITY;
+          }
+        } else {
+          const int see = x.lim - k0;
+#pragma unroll
+          for (int c = 0; c < NC; ++c) s[c] = c < see ? s[c] : -INFINITY;
+        }
       }
       m_tile = -INFINITY;
 #pragma unroll
@@ -828,7 +859,7 @@ __device__ __forceinline__ bool softmax_tiles(const CacheAttnArgs& a, const Tile
   return true;
 }
 
-template <int D, bool BF16, int PARTS>
+template <int D, bool BF16, int PARTS, bool TREE>
 __device__ __forceinline__ void chunk_softmax_role(const CacheAttnArgs& a, const ChunkWalk& start,
                                                    int share, uint8_t* sgen, uint32_t sbase,
                                                    uint32_t bars, uint32_t tmem, const AbortCtx& ab,
@@ -862,8 +893,10 @@ __device__ __forceinline__ void chunk_softmax_role(const CacheAttnArgs& a, const
       x.n = n;
       x.count = count;
       x.k0 = w.t0 * kChunkKeys;
-      x.lim = keys_seen(a, w.s, row_at(a, w, base + r < rows ? base + r : 0).i);
-      x.lim0 = keys_seen(a, w.s, row_at(a, w, base).i);
+      const int i_row = row_at(a, w, base + r < rows ? base + r : 0).i;
+      x.lim = TREE ? w.s.first + i_row : keys_seen(a, w.s, i_row);
+      x.lim0 = TREE ? w.s.kv_len - w.s.count : keys_seen(a, w.s, row_at(a, w, base).i);
+      x.kv_len = w.s.kv_len;
       // (a warp without rows hands P over as it is: its rows of O are not read)
       x.idle = base + r - lane >= rows;
       if (n > 0) {
@@ -926,10 +959,10 @@ __device__ __forceinline__ void chunk_softmax_role(const CacheAttnArgs& a, const
     }
     float m_ref = -INFINITY, l = 0.f;
     if (PARTS == 0 && in_pairs) {
-      if (!softmax_tiles<D, 128, PARTS>(a, x, sgen, bars, ab, m_ref, l)) return;
+      if (!softmax_tiles<D, 128, PARTS, TREE>(a, x, sgen, bars, ab, m_ref, l)) return;
       phase ^= n & 1 ? 3u : 0u;
     } else {
-      if (!softmax_tiles<D, 64, PARTS>(a, x, sgen, bars, ab, m_ref, l)) return;
+      if (!softmax_tiles<D, 64, PARTS, TREE>(a, x, sgen, bars, ab, m_ref, l)) return;
       phase ^= static_cast<uint32_t>((((n + 1) >> 1) & 1) | (n & 2) | ((n & 1) << 2));
     }
 
@@ -980,7 +1013,7 @@ __device__ __forceinline__ void chunk_softmax_role(const CacheAttnArgs& a, const
       // blocks too: where it sees no other keys they count for nothing.
       if (__any_sync(0xffffffffu, l != l)) {
         const int first = first_key(a, w, lane);
-        if (l != l && x.lim <= first) {
+        if (l != l && (TREE ? !tree_sees_block(a, w, x.lim, first) : x.lim <= first)) {
           m_ref = -INFINITY;
           l = 0.f;
         }
@@ -1024,7 +1057,19 @@ __device__ __forceinline__ void chunk_softmax_role(const CacheAttnArgs& a, const
 #pragma unroll
           for (int e = 0; e < 32; ++e) v[e] = 0.f;
         }
-        if (any_nan) {
+        if constexpr (TREE) {
+          uint32_t bad = 0;
+          if (any_nan && there) {
+#pragma unroll 1
+            for (int e = 0; e < 32; ++e)
+              if (static_cast<int>(nan[32 * c + e] >> 32) == w.item + 1 &&
+                  tree_nan(a, w.b, w.hk, w.s, x.lim, 32 * c + e))
+                bad |= 1u << e;
+          }
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if ((bad >> e) & 1u) v[e] = __int_as_float(0x7FFFFFFF);
+        } else if (any_nan) {
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
             const unsigned long long u = nan[32 * c + e];
@@ -1078,7 +1123,7 @@ __device__ __forceinline__ void chunk_softmax_role(const CacheAttnArgs& a, const
   }
 }
 
-template <int D, bool BF16, int PARTS>
+template <int D, bool BF16, int PARTS, bool TREE>
 __global__ void __launch_bounds__(kChunkThreads, 1)
     fa_cache_chunk_kernel(const __grid_constant__ CUtensorMap tm_k,
                           const __grid_constant__ CUtensorMap tm_v, const CacheAttnArgs a) {
@@ -1199,11 +1244,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     else if (warp == 1) chunk_copy_role<D, PARTS>(&tm_k, &tm_v, a, w, sgen, sbase, bars, ab, lane);
   } else if (wgrp < 3) {
     ptx::setmaxnreg_inc<kChunkRegsSoftmax>();
-    chunk_softmax_role<D, BF16, PARTS>(a, w, static_cast<int>(share), sgen, sbase, bars, tmem, ab, warp,
-                                lane);
+    chunk_softmax_role<D, BF16, PARTS, TREE>(a, w, static_cast<int>(share), sgen, sbase, bars, tmem, ab,
+                                             warp, lane);
   } else {
     ptx::setmaxnreg_dec<kChunkRegsConvert>();
-    chunk_convert_role<D, PARTS>(a, w, sgen, sbase, bars, ab, warp, lane);
+    chunk_convert_role<D, PARTS, TREE>(a, w, sgen, sbase, bars, ab, warp, lane);
   }
   __syncwarp();
   ptx::tc_fence_before();

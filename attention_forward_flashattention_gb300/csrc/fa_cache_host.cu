@@ -6,6 +6,7 @@
 
 #include "fa_cache.cuh"
 #include "fa_check.h"
+#include "fa_draft.h"
 
 namespace {
 
@@ -13,6 +14,7 @@ using fa::aligned;
 using fa::block_shift;
 using fa::check_cache;
 using fa::check_stride;
+using fa::kMaxWords;
 
 fa_status done(cudaError_t e) { return e == cudaSuccess ? FA_OK : FA_ERR_CUDA; }
 
@@ -115,11 +117,16 @@ fa_status fa_fwd_cache_workspace_size(int B, int T, int H, int Hkv, int d, size_
   return FA_OK;
 }
 
-fa_status fa_fwd_cache(const void* q, const fa_cache* cache, const int32_t* block_table,
-                       int table_width, const int32_t* kv_lens, const int32_t* cu_q, void* o,
-                       float* lse, int B, int T, int H, const fa_strides* strides, int causal,
-                       float scale, fa_dtype dtype, void* workspace, size_t workspace_size,
-                       void* stream) {
+}  // extern "C"
+
+namespace {
+
+// fa_fwd_cache, or with `words` fa_fwd_cache_tree.
+fa_status fwd_cache(const void* q, const fa_cache* cache, const int32_t* block_table,
+                    int table_width, const int32_t* kv_lens, const int32_t* cu_q,
+                    const uint64_t* masks, int words, void* o, float* lse, int B, int T, int H,
+                    const fa_strides* strides, int causal, float scale, fa_dtype dtype,
+                    void* workspace, size_t workspace_size, void* stream) {
   const fa_status cs = check_cache(cache);
   if (cs == FA_ERR_INVALID_ARG) return cs;
   if (!q || !block_table || !kv_lens || !o || !lse || !strides || !workspace)
@@ -132,6 +139,7 @@ fa_status fa_fwd_cache(const void* q, const fa_cache* cache, const int32_t* bloc
   if (B <= 0 || T < 0 || H <= 0 || table_width <= 0 || H % cache->Hkv != 0)
     return FA_ERR_INVALID_ARG;
   if (!cu_q && T % B != 0) return FA_ERR_INVALID_ARG;
+  if (words != 0 && (!masks || !aligned(masks, 8) || words < 0)) return FA_ERR_INVALID_ARG;
   if (cs != FA_OK) return cs;
   for (int i = 0; i < 2; ++i) {
     for (const long long s : {strides[i].n, strides[i].h, cu_q ? 8LL : strides[i].b}) {
@@ -140,7 +148,8 @@ fa_status fa_fwd_cache(const void* q, const fa_cache* cache, const int32_t* bloc
     }
   }
   if (static_cast<long long>(T) * H > 0x7FFFFFFFLL || B > (1 << 20) ||
-      static_cast<long long>(table_width) * cache->block > (1LL << 30))
+      static_cast<long long>(table_width) * cache->block > (1LL << 30) || words > kMaxWords ||
+      static_cast<long long>(T) * words > 0x7FFFFFFFLL)
     return FA_ERR_UNSUPPORTED;
   size_t need = 0;
   const fa_status ws = fa_fwd_cache_workspace_size(B, T, H, cache->Hkv, cache->d, &need);
@@ -180,13 +189,39 @@ fa_status fa_fwd_cache(const void* q, const fa_cache* cache, const int32_t* bloc
   a.num_blocks = cache->num_blocks;
   a.block_shift = block_shift(cache->block);
   a.causal = causal != 0;
+  static_assert(sizeof(unsigned long long) == sizeof(uint64_t), "mask words");
+  a.masks = reinterpret_cast<const unsigned long long*>(masks);
+  a.words = words;
   a.scale_log2 = scale * 1.4426950408889634f;
   (void)cudaGetLastError();
   bool mapped = true;
-  const cudaError_t e = fa::launch_cache_attn(a, *cache, dtype == FA_DTYPE_BF16, sms,
-                                              static_cast<float*>(workspace),
-                                              static_cast<cudaStream_t>(stream), &mapped);
+  const auto launch = words != 0 ? fa::launch_cache_tree_attn : fa::launch_cache_attn;
+  const cudaError_t e = launch(a, *cache, dtype == FA_DTYPE_BF16, sms, static_cast<float*>(workspace),
+                               static_cast<cudaStream_t>(stream), &mapped);
   return mapped ? done(e) : FA_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+fa_status fa_fwd_cache(const void* q, const fa_cache* cache, const int32_t* block_table,
+                       int table_width, const int32_t* kv_lens, const int32_t* cu_q, void* o,
+                       float* lse, int B, int T, int H, const fa_strides* strides, int causal,
+                       float scale, fa_dtype dtype, void* workspace, size_t workspace_size,
+                       void* stream) {
+  return fwd_cache(q, cache, block_table, table_width, kv_lens, cu_q, nullptr, 0, o, lse, B, T, H,
+                   strides, causal, scale, dtype, workspace, workspace_size, stream);
+}
+
+fa_status fa_fwd_cache_tree(const void* q, const fa_cache* cache, const int32_t* block_table,
+                            int table_width, const int32_t* kv_lens, const int32_t* cu_q,
+                            const uint64_t* masks, int words, void* o, float* lse, int B, int T,
+                            int H, const fa_strides* strides, float scale, fa_dtype dtype,
+                            void* workspace, size_t workspace_size, void* stream) {
+  if (words <= 0) return FA_ERR_INVALID_ARG;
+  return fwd_cache(q, cache, block_table, table_width, kv_lens, cu_q, masks, words, o, lse, B, T, H,
+                   strides, 0, scale, dtype, workspace, workspace_size, stream);
 }
 
 }  // extern "C"

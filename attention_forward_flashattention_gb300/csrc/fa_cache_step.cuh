@@ -287,8 +287,9 @@ __device__ __forceinline__ int merge_pair(int r, int g, int i) {
   return (kI * g + (i ^ ((g >> 1) & (kI / 2 - 1)))) ^ (r & 6);
 }
 
-// D: head dimension; BF16: type of q and o; NT: 8-row groups of an item.
-template <int D, bool BF16, int NT>
+// D: head dimension; BF16: type of q and o; NT: 8-row groups of an item; TREE: rows
+// see the drafted keys that their masks tell (fa_fwd_cache_tree).
+template <int D, bool BF16, int NT, bool TREE>
 __global__ void __launch_bounds__(kStepThreads, step_ctas(NT))
     fa_cache_step_kernel(const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_v, const CacheAttnArgs a,
@@ -449,7 +450,7 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas(NT))
     const int row0 = now.rb * kRows;
     const int rows = min(kRows, now.s.count * a.group - row0);
     const int behind = now.s.kv_len - now.s.count;  // causal: row of query i sees behind + i + 1 keys
-    int lim[NT][2];    // keys that rows 8 nt + 2 t and + 1 see
+    int lim[NT][2];    // keys that rows 8 nt + 2 t and + 1 see (TREE: their masks' rows, or -1)
     float cs[NT][2];   // scale log2 e times the row's factor
     uint32_t q[NT][kQWords];
 #pragma unroll
@@ -471,6 +472,7 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas(NT))
       const float fac = rows_to_f16<kQWords, 4, BF16>(q[nt]);
       int sees = 0;
       if (there) sees = a.causal ? min(max(behind + i + 1, 0), now.s.kv_len) : now.s.kv_len;
+      if constexpr (TREE) sees = there ? now.s.first + i : -1;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         lim[nt][h] = __shfl_sync(0xffffffffu, sees, (2 * t + h) * 4);
@@ -478,8 +480,9 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas(NT))
       }
     }
     // keys that every row of the item sees
-    const int all_see = a.causal ? min(max(behind + row0 / a.group + 1, 0), now.s.kv_len)
-                                 : now.s.kv_len;
+    const int all_see = TREE ? min(max(behind, 0), now.s.kv_len)
+                        : a.causal ? min(max(behind + row0 / a.group + 1, 0), now.s.kv_len)
+                                   : now.s.kv_len;
     float o[NT][kMt][4];
     float m[NT][2], l[NT][2];
 #pragma unroll
@@ -570,10 +573,17 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas(NT))
           if (edge) {
             const int ka = key0 + 16 * u + g;
             const bool no = ((hidden >> box) & 1u) != 0u;
-            if (no || ka >= lim[nt][0]) s[u][nt][0] = -INFINITY;
-            if (no || ka >= lim[nt][1]) s[u][nt][1] = -INFINITY;
-            if (no || ka + 8 >= lim[nt][0]) s[u][nt][2] = -INFINITY;
-            if (no || ka + 8 >= lim[nt][1]) s[u][nt][3] = -INFINITY;
+            if constexpr (TREE) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (no || !tree_sees(a, now.s, lim[nt][e & 1], ka + 4 * (e & 2)))
+                  s[u][nt][e] = -INFINITY;
+            } else {
+              if (no || ka >= lim[nt][0]) s[u][nt][0] = -INFINITY;
+              if (no || ka >= lim[nt][1]) s[u][nt][1] = -INFINITY;
+              if (no || ka + 8 >= lim[nt][0]) s[u][nt][2] = -INFINITY;
+              if (no || ka + 8 >= lim[nt][1]) s[u][nt][3] = -INFINITY;
+            }
           }
           top[nt][0] = fmaxf(top[nt][0], fmaxf(s[u][nt][0], s[u][nt][2]));
           top[nt][1] = fmaxf(top[nt][1], fmaxf(s[u][nt][1], s[u][nt][3]));
@@ -751,9 +761,17 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas(NT))
           }
           const int i_q = (row0 + rr) / a.group, j_q = (row0 + rr) - i_q * a.group;
           if (any_nan) {
-            const int sees = a.causal ? min(behind + i_q + 1, now.s.kv_len) : now.s.kv_len;
-            if (s_nan[c] < sees) acc.x = __int_as_float(0x7FFFFFFF);
-            if (s_nan[c + 1] < sees) acc.y = __int_as_float(0x7FFFFFFF);
+            if constexpr (TREE) {
+#pragma unroll 1
+              for (int x = 0; x < 2; ++x)
+                if (s_nan[c + x] < now.s.kv_len &&
+                    tree_nan(a, now.b, now.hk, now.s, now.s.first + i_q, c + x))
+                  (x ? acc.y : acc.x) = __int_as_float(0x7FFFFFFF);
+            } else {
+              const int sees = a.causal ? min(behind + i_q + 1, now.s.kv_len) : now.s.kv_len;
+              if (s_nan[c] < sees) acc.x = __int_as_float(0x7FFFFFFF);
+              if (s_nan[c + 1] < sees) acc.y = __int_as_float(0x7FFFFFFF);
+            }
           }
           if (part != nullptr) {
             *reinterpret_cast<float2*>(part + rr * D + c) = acc;

@@ -5,6 +5,7 @@
 // sequences would spend waiting.
 //
 // Functions return their tensors, or the fa_status of a failed call as an int.
+#include "fa_draft_torch.h"
 #include "fa_rope_torch.h"
 #include "fa_torch.h"
 
@@ -108,8 +109,9 @@ PyObject* cache_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// (q, cache, block_table, kv_lens, cu_q, out, causal, scale, stream); out:
-// None, or (o, lse, workspace). Returns (o, lse).
+// (q, cache, block_table, kv_lens, cu_q, out, causal, scale, stream), or with TREE
+// the masks in place of causal; out: None, or (o, lse, workspace). Returns (o, lse).
+template <bool TREE>
 PyObject* attention_forward_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   count_args(n, 9);
@@ -135,8 +137,23 @@ PyObject* attention_forward_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int32_t* p_table = index(table, dev, B, width, "block_table");
   const int32_t* p_kv = index(tensor(a[3], "kv_lens"), dev, B, -1, "kv_lens");
   const int32_t* p_cu = ragged ? index(tensor(a[4], "cu_q"), dev, B + 1, -1, "cu_q") : nullptr;
-  const int causal = PyObject_IsTrue(a[6]);
-  if (causal < 0) throw python_error();
+  int causal = 0, words = 0;
+  const uint64_t* p_masks = nullptr;
+  if constexpr (TREE) {
+    const at::Tensor& masks = tensor(a[6], "masks");
+    if (!(masks.scalar_type() == at::kLong && on(masks, dev) && masks.is_contiguous() &&
+          (masks.dim() == 2 ? masks.size(0) == T
+                            : !ragged && masks.dim() == 3 && dims == 4 && masks.size(0) == B &&
+                                  masks.size(1) == q.size(2))))
+      refuse(PyExc_ValueError,
+             "masks must be a contiguous int64 tensor [rows, words] on q's device, without cu_q also "
+             "[B, n, words]");
+    words = narrow(masks.size(masks.dim() - 1), "masks: too many words");
+    p_masks = static_cast<const uint64_t*>(masks.data_ptr());
+  } else {
+    causal = PyObject_IsTrue(a[6]);
+    if (causal < 0) throw python_error();
+  }
   double scale = 1.0 / std::sqrt(static_cast<double>(c.d));
   if (a[7] != Py_None) {
     scale = PyFloat_AsDouble(a[7]);
@@ -181,9 +198,15 @@ PyObject* attention_forward_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const size_t ws_bytes = static_cast<size_t>(ws.numel());
     fa_status rc;
     Py_BEGIN_ALLOW_THREADS;
-    rc = fa_fwd_cache(q.data_ptr(), &c, p_table, width, p_kv, p_cu, o.data_ptr(),
-                      static_cast<float*>(lse.data_ptr()), B, T, H, st, causal,
-                      static_cast<float>(scale), dt, ws.data_ptr(), ws_bytes, cs.stream);
+    float* const p_lse = static_cast<float*>(lse.data_ptr());
+    if constexpr (TREE)
+      rc = fa_fwd_cache_tree(q.data_ptr(), &c, p_table, width, p_kv, p_cu, p_masks, words,
+                             o.data_ptr(), p_lse, B, T, H, st, static_cast<float>(scale), dt,
+                             ws.data_ptr(), ws_bytes, cs.stream);
+    else
+      rc = fa_fwd_cache(q.data_ptr(), &c, p_table, width, p_kv, p_cu, o.data_ptr(), p_lse, B, T, H,
+                        st, causal, static_cast<float>(scale), dt, ws.data_ptr(), ws_bytes,
+                        cs.stream);
     Py_END_ALLOW_THREADS;
     if (rc != FA_OK) return status(rc);
   }
@@ -203,7 +226,9 @@ PyCFunction fast() {
 PyMethodDef kMethods[] = {
     {"cache_plan", fast<cache_plan>(), METH_FASTCALL, nullptr},
     {"cache_append", fast<cache_append>(), METH_FASTCALL, nullptr},
-    {"attention_forward_cache", fast<attention_forward_cache>(), METH_FASTCALL, nullptr},
+    {"attention_forward_cache", fast<attention_forward_cache<false>>(), METH_FASTCALL, nullptr},
+    {"attention_forward_cache_tree", fast<attention_forward_cache<true>>(), METH_FASTCALL, nullptr},
+    {"cache_tree", fast<cache_tree>(), METH_FASTCALL, nullptr},
     {"qk_norm_rope", fast<qk_norm_rope>(), METH_FASTCALL, nullptr},
     {"qk_norm_rope_bwd", fast<qk_norm_rope_bwd>(), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};

@@ -7,6 +7,9 @@
 
 namespace fa {
 
+// Words of a mask over drafted tokens, at most.
+constexpr int kMaxWords = 16;
+
 inline bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 inline int block_shift(int block) {

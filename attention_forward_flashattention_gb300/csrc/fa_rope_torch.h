@@ -1,8 +1,6 @@
 // fa_qk_norm_rope and its gradients on torch tensors (see fa_cache_torch.cpp).
 #pragma once
 
-#include <initializer_list>
-
 #include "fa_rope.h"
 #include "fa_torch.h"
 
@@ -90,19 +88,6 @@ void check_qk(const at::Tensor& q, const at::Tensor& k, const HeadsView& vq, con
   if (!(q.dim() == k.dim() && vk.B == vq.B && vk.N == vq.N && vk.d == vq.d &&
         k.scalar_type() == q.scalar_type() && on(k, q.get_device())))
     refuse(PyExc_ValueError, "q and k must be of one dtype and device and differ in their heads only");
-}
-
-PyObject* tuple_of(std::initializer_list<const at::Tensor*> ts) {
-  PyObject* out = PyTuple_New(static_cast<Py_ssize_t>(ts.size()));
-  if (!out) throw python_error();
-  Py_ssize_t i = 0;
-  for (const at::Tensor* t : ts) {
-    PyObject* o = Py_None;
-    if (t != nullptr && t->defined()) o = THPVariable_Wrap(*t);
-    else Py_INCREF(Py_None);
-    PyTuple_SET_ITEM(out, i++, o);
-  }
-  return out;
 }
 
 // (q, k, table, positions, q_weight, k_weight, eps, interleaved, out, stream);

@@ -11,6 +11,7 @@
 #include <c10/cuda/CUDAStream.h>
 
 #include <cmath>
+#include <initializer_list>
 #include <optional>
 
 #include "fa_cache.h"
@@ -158,6 +159,20 @@ fa_cache describe(PyObject* o, int dev) {
 
 void count_args(Py_ssize_t n, Py_ssize_t want) {
   if (n != want) refuse(PyExc_TypeError, "wrong number of arguments");
+}
+
+// The tensors as a tuple, None for one that is not there.
+PyObject* tuple_of(std::initializer_list<const at::Tensor*> ts) {
+  PyObject* out = PyTuple_New(static_cast<Py_ssize_t>(ts.size()));
+  if (!out) throw python_error();
+  Py_ssize_t i = 0;
+  for (const at::Tensor* t : ts) {
+    PyObject* o = Py_None;
+    if (t != nullptr && t->defined()) o = THPVariable_Wrap(*t);
+    else Py_INCREF(Py_None);
+    PyTuple_SET_ITEM(out, i++, o);
+  }
+  return out;
 }
 
 }  // namespace
