@@ -105,9 +105,10 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.fa_version.argtypes = []
         lib.fa_version.restype = i
         if hasattr(lib, "fa_fwd_cache"):
-            from . import cache, draft, rope
+            from . import cache, draft, pages, rope
             cache.bind(lib)
             draft.bind(lib)
+            pages.bind(lib)
             rope.bind(lib)
         if path is None:
             _lib = lib
@@ -489,6 +490,11 @@ from .cache import (Cache, FaCache, attention_forward_cache,  # noqa: E402,F401
 from .draft import (attention_forward_cache_tree,  # noqa: E402,F401
                     attention_forward_cache_tree_into, cache_tree, cache_tree_into, fa_cache_tree,
                     fa_fwd_cache_tree)
+
+# ------------------------------------------------------------ upkeep of the block cache (include/fa_pages.h)
+
+from .pages import (cache_copy, cache_fork, cache_keep, cache_release,  # noqa: E402,F401
+                    fa_cache_copy, fa_cache_fork, fa_cache_keep, fa_cache_release)
 
 # ------------------------------------------------------------ norm and rotation (include/fa_rope.h)
 

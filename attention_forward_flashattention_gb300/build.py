@@ -32,14 +32,16 @@ SELFTEST_NAME = "libfa_selftest.so"
 LIB_UNITS = ["fa_host.cu", "fa_fwd_d64.cu", "fa_fwd_d128.cu", "fa_fwd_fp8.cu", "fa_fwd_pair.cu",
              "fa_bwd_d64.cu", "fa_bwd_d128.cu", "fa_noalloc.cu", "fa_pipeline.cu",
              "fa_cache_host.cu", "fa_cache_plan.cu", "fa_cache_append.cu", "fa_cache_attn.cu",
-             "fa_cache_tree.cu", "fa_rope.cu"]
+             "fa_cache_tree.cu", "fa_pages.cu", "fa_rope.cu"]
 SELFTEST_UNITS = ["selftest.cu"]
 TORCH_NAME = "_fa_cache_torch.so"
 TORCH_UNIT = "fa_cache_torch.cpp"
 HEADERS = ["ptx.cuh", "fa_common.cuh", "fa_kernel.cuh", "fa_launch.cuh", "fa_pair.cuh", "fa_bwd.cuh",
            "fa_bwd_launch.cuh", "fa_dispatch.h", "fa_cache.cuh", "fa_cache_step.cuh", "fa_cache_chunk.cuh",
-           "fa_cache_launch.cuh", "fa_check.h", "fa_torch.h", "fa_rope_torch.h", "fa_draft_torch.h"]
-PUBLIC_HEADERS = ["fa.h", "fa_cache.h", "fa_draft.h", "fa_rope.h"]
+           "fa_cache_launch.cuh",
+           "fa_cache_scale.cuh", "fa_check.h", "fa_torch.h", "fa_rope_torch.h", "fa_draft_torch.h",
+           "fa_pages_torch.h"]
+PUBLIC_HEADERS = ["fa.h", "fa_cache.h", "fa_draft.h", "fa_pages.h", "fa_rope.h"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -25,7 +25,7 @@
 #include <cuda_fp16.h>
 
 #include "fa_cache.cuh"
-#include "ptx.cuh"
+#include "fa_cache_scale.cuh"
 
 namespace fa {
 namespace {
@@ -82,12 +82,6 @@ __device__ __forceinline__ float scale_for(float x) {
   e = max(e, kCacheMinScaleExp);
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
-// The smallest power of two that is not below x (a positive normal number).
-__device__ __forceinline__ float pow2_above(float x) {
-  const uint32_t u = __float_as_uint(x);
-  return __uint_as_float((u + 0x7FFFFFu) & 0xFF800000u);
-}
-
 // Codes of 8 values times f; kOdd: infinities and NaN among them become NaN
 // (inf * 0 is NaN, a finite value plus its product with 0 is itself).
 template <bool BF16, bool kOdd>
@@ -102,12 +96,6 @@ __device__ __forceinline__ uint2 encode8(uint4 x, float f) {
   }
   return make_uint2(ptx::pack4_e4m3(v[0], v[1], v[2], v[3]),
                     ptx::pack4_e4m3(v[4], v[5], v[6], v[7]));
-}
-
-// Four codes times f, rounded to codes again.
-__device__ __forceinline__ uint32_t rescale4(uint32_t c, float f) {
-  const float2 lo = ptx::e4m3x2_to_f32(c & 0xFFFFu), hi = ptx::e4m3x2_to_f32(c >> 16);
-  return ptx::pack4_e4m3(lo.x * f, lo.y * f, hi.x * f, hi.y * f);
 }
 
 // BLOCK: tokens in a block. D: head dimension. A team takes `planes` of the 2 Hkv

@@ -6,6 +6,7 @@
 //
 // Functions return their tensors, or the fa_status of a failed call as an int.
 #include "fa_draft_torch.h"
+#include "fa_pages_torch.h"
 #include "fa_rope_torch.h"
 #include "fa_torch.h"
 
@@ -229,6 +230,10 @@ PyMethodDef kMethods[] = {
     {"attention_forward_cache", fast<attention_forward_cache<false>>(), METH_FASTCALL, nullptr},
     {"attention_forward_cache_tree", fast<attention_forward_cache<true>>(), METH_FASTCALL, nullptr},
     {"cache_tree", fast<cache_tree>(), METH_FASTCALL, nullptr},
+    {"cache_keep", fast<cache_keep>(), METH_FASTCALL, nullptr},
+    {"cache_release", fast<cache_release>(), METH_FASTCALL, nullptr},
+    {"cache_fork", fast<cache_fork>(), METH_FASTCALL, nullptr},
+    {"cache_copy", fast<cache_copy>(), METH_FASTCALL, nullptr},
     {"qk_norm_rope", fast<qk_norm_rope>(), METH_FASTCALL, nullptr},
     {"qk_norm_rope_bwd", fast<qk_norm_rope_bwd>(), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
