@@ -23,7 +23,10 @@ namespace fa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBatch = 4;  // rows of a lane group under way together
+constexpr int kFwdBatch = 4;  // rows of a lane group under way together
+constexpr int kFwdCtas = 4;   // on an SM
+constexpr int kBwdBatch = 4;
+constexpr int kBwdCtas = 2;
 
 struct RowsOf {  // q or k: its heads, and element strides of each operand
   const uint16_t* x;
@@ -41,12 +44,13 @@ struct RopeArgs {
   long long positions_b;
   int n_positions, rotary, interleaved, weights_fp32;
   int B, N;
-  int per_unit;       // heads that a lane group takes
-  int chunks[2];      // units of a token, of q and of k
-  int heads_inner;    // neighbouring units: chunks of one token, or tokens of one chunk
-  long long units;    // B * N * (chunks[0] + chunks[1])
+  int per_unit;        // heads that a lane group takes
+  int chunks[2];       // units of a token, of q and of k
+  int heads_inner;     // neighbouring units: chunks of one token, or tokens of one chunk
+  long long units[2];  // B * N * chunks
+  int ctas[2];         // the first ones take q's units, the others k's
   float eps;
-  float* partial;  // backward: [CTAs][2][d]
+  float* partial;  // backward: [CTAs][d]
 };
 
 template <bool BF16>
@@ -170,56 +174,65 @@ __device__ __forceinline__ float group_sum(float v) {
 }
 
 struct Unit {
-  int b, n, which, h0, h1;
+  int b, n, h0, h1;  // token, heads h0 .. h1 - 1
 };
-__device__ __forceinline__ Unit unit_of(const RopeArgs& a, long long u) {
-  const int chunks = a.chunks[0] + a.chunks[1];
-  const long long tokens = static_cast<long long>(a.B) * a.N;
+__device__ __forceinline__ Unit unit_of(const RopeArgs& a, int which, long long u) {
+  const int chunks = a.chunks[which];
   long long token;
   int chunk;
   if (a.heads_inner) {
     token = u / chunks;
     chunk = static_cast<int>(u - token * chunks);
   } else {
+    const long long tokens = static_cast<long long>(a.B) * a.N;
     chunk = static_cast<int>(u / tokens);
     token = u - chunk * tokens;
   }
   Unit r;
   r.b = static_cast<int>(token / a.N);
   r.n = static_cast<int>(token - static_cast<long long>(r.b) * a.N);
-  r.which = chunk >= a.chunks[0];
-  r.h0 = (chunk - (r.which ? a.chunks[0] : 0)) * a.per_unit;
-  r.h1 = min(r.h0 + a.per_unit, a.of[r.which].heads);
+  r.h0 = chunk * a.per_unit;
+  r.h1 = min(r.h0 + a.per_unit, a.of[which].heads);
   return r;
 }
 __device__ __forceinline__ long long row_at(const fa_strides& s, const Unit& u, int h) {
   return u.b * s.b + h * s.h + u.n * s.n;
 }
+// Rows h0 .. h0 + N - 1 of a unit, zeros for those that it does not have.
+template <int N>
+__device__ __forceinline__ void load_rows(const uint16_t* x, const fa_strides& s, const Unit& u,
+                                          bool there, int h0, const Place& at, Eight (&e)[N]) {
+  const uint16_t* row = x + row_at(s, u, h0);
+#pragma unroll
+  for (int i = 0; i < N; ++i, row += s.h) {
+    e[i] = {make_uint2(0u, 0u), make_uint2(0u, 0u)};
+    if (there && h0 + i < u.h1) e[i] = load8(row, at);
+  }
+}
 
 template <int D, bool BF16, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads) fa_norm_rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, kFwdCtas) fa_norm_rope_kernel(const RopeArgs a) {
   constexpr int L = D / 8;
   const int lane = static_cast<int>(threadIdx.x) % L;
-  const long long u = static_cast<long long>(blockIdx.x) * (kThreads / L) + threadIdx.x / L;
+  const int which = static_cast<int>(blockIdx.x) >= a.ctas[0];
+  const long long u = static_cast<long long>(static_cast<int>(blockIdx.x) - (which ? a.ctas[0] : 0)) *
+                          (kThreads / L) + threadIdx.x / L;
   // (a group without a unit takes part in the sums)
-  const bool there = u < a.units;
-  const Unit w = unit_of(a, there ? u : 0);
-  const RowsOf& o = a.of[w.which];
+  const bool there = u < a.units[which];
+  const Unit w = unit_of(a, which, there ? u : 0);
+  const RowsOf& o = a.of[which];
   const Place at = place_of<D>(a, lane);
+  Eight x[kFwdBatch];
+  // (the rows first: the table waits for the positions)
+  load_rows(o.x, o.xs, w, there, w.h0, at, x);
   const Turn turn = turn_of(a, at, w.b, w.n);
   float wt[8];
   weights_of<BF16>(a, o.weight, at, wt);
-  const int steps = (a.per_unit + kBatch - 1) / kBatch;  // (the same for all groups of a warp)
-  for (int step = 0; step < steps; ++step) {
-    const int h0 = w.h0 + step * kBatch;
-    Eight x[kBatch];
+  for (int h0 = w.h0; h0 < w.h0 + a.per_unit; h0 += kFwdBatch) {  // (as often for all groups)
+    if (h0 > w.h0) load_rows(o.x, o.xs, w, there, h0, at, x);
+    uint16_t* out = o.out + row_at(o.outs, w, h0);
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      x[i] = {make_uint2(0u, 0u), make_uint2(0u, 0u)};
-      if (there && h0 + i < w.h1) x[i] = load8(o.x + row_at(o.xs, w, h0 + i), at);
-    }
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
+    for (int i = 0; i < kFwdBatch; ++i, out += o.outs.h) {
       float f[8];
       widen8<BF16>(x[i], f);
       float sum = 0.f;
@@ -229,42 +242,40 @@ __global__ void __launch_bounds__(kThreads) fa_norm_rope_kernel(const RopeArgs a
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[e] = f[e] * inv * wt[e];
       rotate<INTERLEAVED, false>(f, turn);
-      if (there && h0 + i < w.h1) store8(o.out + row_at(o.outs, w, h0 + i), at, narrow8<BF16>(f));
+      if (there && h0 + i < w.h1) store8(out, at, narrow8<BF16>(f));
     }
   }
 }
 
-// dx, and each CTA's sum for the weights.
+// dx, and each CTA's sum for the weights of q or k.
 template <int D, bool BF16, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads) fa_norm_rope_bwd_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, kBwdCtas) fa_norm_rope_bwd_kernel(const RopeArgs a) {
   constexpr int L = D / 8, kGroups = kThreads / L;
   __shared__ float s_sum[kGroups][D];
   const int lane = static_cast<int>(threadIdx.x) % L, group = static_cast<int>(threadIdx.x) / L;
+  const int which = static_cast<int>(blockIdx.x) >= a.ctas[0];
+  const int cta = static_cast<int>(blockIdx.x) - (which ? a.ctas[0] : 0);
+  const RowsOf& o = a.of[which];
   const Place at = place_of<D>(a, lane);
-  float dw[2][8] = {};
-  const long long step_units = static_cast<long long>(gridDim.x) * kGroups;
-  for (long long u0 = static_cast<long long>(blockIdx.x) * kGroups; u0 < a.units; u0 += step_units) {
+  float wt[8], dw[8] = {};
+  weights_of<BF16>(a, o.weight, at, wt);
+  const long long step_units = static_cast<long long>(a.ctas[which]) * kGroups;
+  for (long long u0 = static_cast<long long>(cta) * kGroups; u0 < a.units[which]; u0 += step_units) {
     const long long u = u0 + group;
-    const bool there = u < a.units;
-    const Unit w = unit_of(a, there ? u : 0);
-    const RowsOf& o = a.of[w.which];
+    const bool there = u < a.units[which];
+    const Unit w = unit_of(a, which, there ? u : 0);
+    Eight x[kBwdBatch], dy[kBwdBatch];
+    load_rows(o.x, o.xs, w, there, w.h0, at, x);
+    load_rows(o.dy, o.dys, w, there, w.h0, at, dy);
     const Turn turn = turn_of(a, at, w.b, w.n);
-    float wt[8], add[8] = {};
-    weights_of<BF16>(a, o.weight, at, wt);
-    const int steps = (a.per_unit + kBatch - 1) / kBatch;
-    for (int step = 0; step < steps; ++step) {
-      const int h0 = w.h0 + step * kBatch;
-      Eight x[kBatch], dy[kBatch];
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        x[i] = dy[i] = {make_uint2(0u, 0u), make_uint2(0u, 0u)};
-        if (there && h0 + i < w.h1) {
-          x[i] = load8(o.x + row_at(o.xs, w, h0 + i), at);
-          dy[i] = load8(o.dy + row_at(o.dys, w, h0 + i), at);
-        }
+    for (int h0 = w.h0; h0 < w.h0 + a.per_unit; h0 += kBwdBatch) {
+      if (h0 > w.h0) {
+        load_rows(o.x, o.xs, w, there, h0, at, x);
+        load_rows(o.dy, o.dys, w, there, h0, at, dy);
       }
+      uint16_t* out = o.out + row_at(o.outs, w, h0);
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
+      for (int i = 0; i < kBwdBatch; ++i, out += o.outs.h) {
         float f[8], t[8];
         widen8<BF16>(x[i], f);
         widen8<BF16>(dy[i], t);
@@ -282,32 +293,23 @@ __global__ void __launch_bounds__(kThreads) fa_norm_rope_bwd_kernel(const RopeAr
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float n = f[e] * inv;
-          add[e] = fmaf(t[e], n, add[e]);
+          dw[e] = fmaf(t[e], n, dw[e]);
           f[e] = inv * fmaf(-n, mean, t[e] * wt[e]);
         }
-        if (there && h0 + i < w.h1) store8(o.out + row_at(o.outs, w, h0 + i), at, narrow8<BF16>(f));
+        if (there && h0 + i < w.h1) store8(out, at, narrow8<BF16>(f));
       }
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      dw[0][e] += w.which ? 0.f : add[e];
-      dw[1][e] += w.which ? add[e] : 0.f;
     }
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (a.partial == nullptr) return;
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    __syncthreads();
+  for (int e = 0; e < 8; ++e) s_sum[group][(e < 4 ? at.lo + e : at.hi + e - 4)] = dw[e];
+  __syncthreads();
+  for (int c = static_cast<int>(threadIdx.x); c < D; c += kThreads) {
+    float v = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) s_sum[group][(e < 4 ? at.lo + e : at.hi + e - 4)] = dw[k][e];
-    __syncthreads();
-    for (int c = static_cast<int>(threadIdx.x); c < D; c += kThreads) {
-      float v = 0.f;
-#pragma unroll
-      for (int g = 0; g < kGroups; ++g) v += s_sum[g][c];
-      a.partial[(static_cast<long long>(blockIdx.x) * 2 + k) * D + c] = v;
-    }
+    for (int g = 0; g < kGroups; ++g) v += s_sum[g][c];
+    a.partial[static_cast<long long>(blockIdx.x) * D + c] = v;
   }
 }
 
@@ -315,24 +317,26 @@ __global__ void __launch_bounds__(kThreads) fa_norm_rope_bwd_kernel(const RopeAr
 // warps that each take every eighth part.
 template <int D>
 __global__ void __launch_bounds__(256)
-    fa_norm_rope_join_kernel(const float* partial, int parts, float* dq_weight, float* dk_weight) {
+    fa_norm_rope_join_kernel(const float* partial, int parts_q, int parts_k, float* dq_weight,
+                             float* dk_weight) {
   __shared__ float s_sum[8][32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
-  const int col = static_cast<int>(blockIdx.x) * 32 + lane;  // of [2][D]
+  const bool of_k = blockIdx.x >= D / 32;
+  const int col = (static_cast<int>(blockIdx.x) - (of_k ? D / 32 : 0)) * 32 + lane;
+  const int parts = of_k ? parts_k : parts_q;
+  const float* const from = partial + (of_k ? static_cast<long long>(parts_q) * D : 0) + col;
   float v = 0.f;
 #pragma unroll 8
-  for (int p = warp; p < parts; p += 8) v += __ldcg(partial + static_cast<long long>(p) * 2 * D + col);
+  for (int p = warp; p < parts; p += 8) v += __ldcg(from + static_cast<long long>(p) * D);
   s_sum[warp][lane] = v;
   __syncthreads();
   if (warp != 0) return;
 #pragma unroll
   for (int w = 1; w < 8; ++w) v += s_sum[w][lane];
-  float* const out = col < D ? dq_weight : dk_weight;
-  if (out != nullptr) out[col < D ? col : col - D] = v;
+  float* const out = of_k ? dk_weight : dq_weight;
+  if (out != nullptr) out[col] = v;
 }
-
-constexpr int kBwdCtas = 4;  // on an SM
 
 fa_status check_rope(const fa_rope* r, int d) {
   if (!r || !r->table || !r->positions) return FA_ERR_INVALID_ARG;
@@ -386,29 +390,35 @@ RopeArgs common(const fa_rope& r, int B, int N, int H, int Hkv, const fa_strides
 void split(RopeArgs& a, int most, long long groups) {
   const long long tokens = static_cast<long long>(a.B) * a.N;
   int per = most;
-  auto units = [&](int p) {
-    return tokens * ((a.of[0].heads + p - 1) / p + (a.of[1].heads + p - 1) / p);
-  };
-  while (per > 1 && units(per) < groups) per >>= 1;
+  auto units = [&](int i, int p) { return tokens * ((a.of[i].heads + p - 1) / p); };
+  while (per > 1 && units(0, per) + units(1, per) < groups) per >>= 1;
   a.per_unit = per;
-  for (int i = 0; i < 2; ++i) a.chunks[i] = (a.of[i].heads + per - 1) / per;
-  a.units = units(per);
+  for (int i = 0; i < 2; ++i) {
+    a.chunks[i] = (a.of[i].heads + per - 1) / per;
+    a.units[i] = units(i, per);
+  }
 }
 
 template <int D, bool BF16>
-cudaError_t launch_forward(const RopeArgs& a, cudaStream_t s) {
+cudaError_t launch_forward(RopeArgs a, cudaStream_t s) {
   constexpr int kGroups = kThreads / (D / 8);
-  const unsigned grid = static_cast<unsigned>((a.units + kGroups - 1) / kGroups);
+  for (int i = 0; i < 2; ++i) a.ctas[i] = static_cast<int>((a.units[i] + kGroups - 1) / kGroups);
+  const unsigned grid = static_cast<unsigned>(a.ctas[0]) + static_cast<unsigned>(a.ctas[1]);
   if (a.interleaved) fa_norm_rope_kernel<D, BF16, true><<<grid, kThreads, 0, s>>>(a);
   else fa_norm_rope_kernel<D, BF16, false><<<grid, kThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 
 template <int D, bool BF16>
-cudaError_t launch_backward(const RopeArgs& a, int most, float* dqw, float* dkw, cudaStream_t s) {
+cudaError_t launch_backward(RopeArgs a, int most, float* dqw, float* dkw, cudaStream_t s) {
   constexpr int kGroups = kThreads / (D / 8);
-  const long long want = (a.units + kGroups - 1) / kGroups;
-  const unsigned grid = static_cast<unsigned>(want < most ? want : most);
+  // CTAs that run at once, shared out by the units of q and k
+  const long long want[2] = {(a.units[0] + kGroups - 1) / kGroups, (a.units[1] + kGroups - 1) / kGroups};
+  const long long share = (most * a.units[1] + (a.units[0] + a.units[1]) / 2) / (a.units[0] + a.units[1]);
+  const long long k = share < 1 ? 1 : share > most - 1 ? most - 1 : share;
+  a.ctas[1] = static_cast<int>(want[1] < k ? want[1] : k);
+  a.ctas[0] = static_cast<int>(want[0] < most - k ? want[0] : most - k);
+  const unsigned grid = static_cast<unsigned>(a.ctas[0] + a.ctas[1]);
   if (a.interleaved) fa_norm_rope_bwd_kernel<D, BF16, true><<<grid, kThreads, 0, s>>>(a);
   else fa_norm_rope_bwd_kernel<D, BF16, false><<<grid, kThreads, 0, s>>>(a);
   const cudaError_t e = cudaGetLastError();
@@ -423,7 +433,7 @@ cudaError_t launch_backward(const RopeArgs& a, int most, float* dqw, float* dkw,
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, fa_norm_rope_join_kernel<D>, static_cast<const float*>(a.partial),
-                            static_cast<int>(grid), dqw, dkw);
+                            a.ctas[0], a.ctas[1], dqw, dkw);
 }
 
 }  // namespace
@@ -469,7 +479,7 @@ fa_status fa_qk_norm_rope_bwd_workspace_size(int d, size_t* bytes) {
   int sms = 0;
   const fa_status ds = fa::device_facts(&sms, nullptr);
   if (ds != FA_OK) return ds;
-  *bytes = sizeof(float) * 2 * static_cast<size_t>(d) * static_cast<size_t>(sms * fa::kBwdCtas);
+  *bytes = sizeof(float) * static_cast<size_t>(d) * static_cast<size_t>(sms * fa::kBwdCtas);
   return FA_OK;
 }
 
