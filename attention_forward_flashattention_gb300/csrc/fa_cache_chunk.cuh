@@ -58,6 +58,10 @@ constexpr int kChunkThreads = 512;
 constexpr int kChunkRows = 256;
 constexpr int kChunkKeys = 128;
 constexpr int kChunkMinShare = 2;  // tiles
+// Trees: tiles' time that an item takes beside its own (Q, the first scores, the last
+// products, the epilogue), which counts in the list, and the fewest tiles for which
+// an item is cut.
+constexpr int kTreeLead = 12, kTreePiece = 4;
 // Registers a thread after setmaxnreg (sum 512 = 4 x 128): MMA and copy
 // warpgroup, each softmax warpgroup, converters.
 constexpr uint32_t kChunkRegsMma = 64, kChunkRegsSoftmax = 184, kChunkRegsConvert = 80;
@@ -113,6 +117,7 @@ enum ChunkBar : int {
 constexpr int kChunkSlotTmem = 496, kChunkSlotAbort = 500, kChunkSlotStart = 504;
 constexpr int kChunkSlotHidden = 520;  // [raw] bytes: bit g: 16-key group g is hidden
 constexpr int kChunkSlotAnyNan = 528;  // not 0: a converter has noted NaN
+constexpr int kChunkSlotMoved = 536;   // trees: how far the share's two ends were moved
 
 // Keys that query token i of a sequence sees.
 __device__ __forceinline__ int keys_seen(const CacheAttnArgs& a, const SeqRows& s, int i) {
@@ -135,16 +140,30 @@ __device__ __forceinline__ int chunk_real_tiles(const CacheAttnArgs& a, const Se
   const long long last = min((rb + 1LL) * a.item_rows, static_cast<long long>(s.count) * a.group) - 1;
   return (keys_seen(a, s, static_cast<int>(last / a.group)) + kChunkKeys - 1) / kChunkKeys;
 }
-// Tiles of one head of a sequence.
+// Tiles of one head of a sequence, as they count.
+template <bool TREE>
 __device__ __forceinline__ long long chunk_head_tiles(const CacheAttnArgs& a, const SeqRows& s) {
   const int n = chunk_row_blocks(a, s);
-  if (!a.causal) return static_cast<long long>(n) * max(1, (s.kv_len + kChunkKeys - 1) / kChunkKeys);
+  if (!a.causal)
+    return static_cast<long long>(n) *
+           (max(1, (s.kv_len + kChunkKeys - 1) / kChunkKeys) + (TREE ? kTreeLead : 0));
   long long sum = 0;
   for (int rb = 0; rb < n; ++rb) sum += max(1, chunk_real_tiles(a, s, rb));
   return sum;
 }
 
+// Trees: the place of a cut x counted tiles behind an item's start, `tiles` of them in
+// the item, the last kTreeLead of which are not real. An item is not cut into
+// pieces of less than `piece` tiles.
+__device__ __forceinline__ int tree_piece(long long share) {
+  return share < 4 * kTreePiece ? max(static_cast<int>(share) / 4, 1) : kTreePiece;
+}
+__device__ __forceinline__ int tree_cut(int x, int tiles, int piece) {
+  return x < piece ? 0 : x > tiles - kTreeLead - piece ? tiles : x;
+}
+
 // A CTA's share, item by item (every role walks a copy of its own).
+template <bool TREE>
 struct ChunkWalk {
   int b, hk, rb, n_rb;
   int tiles;     // counted tiles of the item
@@ -156,9 +175,14 @@ struct ChunkWalk {
 
   __device__ __forceinline__ void item_tiles(const CacheAttnArgs& a) {
     const int real = chunk_real_tiles(a, s, rb);
-    tiles = max(1, real);
+    tiles = max(1, real) + (TREE ? kTreeLead : 0);
     t1 = static_cast<int>(min(static_cast<long long>(tiles), t0 + left));
     real_end = min(t1, real);
+  }
+  // Parts of the item, which begins here and is cut into shares.
+  __device__ __forceinline__ int parts(int share) const {
+    const int end = TREE ? tiles - kTreeLead - tree_piece(share) + 1 : tiles;
+    return 1 + (end - t1 + share - 1) / share;
   }
   __device__ __forceinline__ void start(const CacheAttnArgs& a, int b_, int hk_, int rb_, int t0_,
                                         long long n) {
@@ -171,6 +195,7 @@ struct ChunkWalk {
     s = seq_rows(a, b);
     n_rb = chunk_row_blocks(a, s);
     item_tiles(a);
+    if (TREE && t0 == tiles) next(a);  // (the cut was moved to the item's end)
   }
   __device__ __forceinline__ bool next(const CacheAttnArgs& a) {
     left -= t1 - t0;
@@ -201,10 +226,10 @@ struct ChunkWalk {
 
 // ---- copies: warp 1. Lane j < 128 / block handles the j-th block of a tile,
 // lane g < 8 the scales of the g-th 16-key group.
-template <int D, int PARTS>
+template <int D, int PARTS, bool TREE>
 __device__ __forceinline__ void chunk_copy_role(const CUtensorMap* tm_k, const CUtensorMap* tm_v,
-                                                const CacheAttnArgs& a, ChunkWalk w, uint8_t* sgen,
-                                                uint32_t sbase, uint32_t bars, const AbortCtx& ab,
+                                                const CacheAttnArgs& a, ChunkWalk<TREE> w,
+                                                uint8_t* sgen, uint32_t sbase, uint32_t bars, const AbortCtx& ab,
                                                 int lane) {
   using L = ChunkLayout<D, PARTS>;
   constexpr int R = L::kRaw;
@@ -321,7 +346,7 @@ __device__ __forceinline__ void chunk_copy_role(const CUtensorMap* tm_k, const C
 // ---- converters: warps 12-15. A thread takes 16 codes of a row at a time: 32
 // bytes in two chunks of one of the row's 128-byte panels.
 template <int D, int PARTS, bool TREE>
-__device__ __forceinline__ void chunk_convert_role(const CacheAttnArgs& a, ChunkWalk w,
+__device__ __forceinline__ void chunk_convert_role(const CacheAttnArgs& a, ChunkWalk<TREE> w,
                                                    uint8_t* sgen, uint32_t sbase, uint32_t bars,
                                                    const AbortCtx& ab, int warp, int lane) {
   using L = ChunkLayout<D, PARTS>;
@@ -458,9 +483,9 @@ __device__ __forceinline__ void issue_pv_half(uint32_t d_tmem, uint32_t p_tmem, 
 }
 
 // ---- MMA issue: warp 0
-template <int D, int PARTS>
-__device__ __forceinline__ void chunk_mma_role(const CacheAttnArgs& a, ChunkWalk w, uint32_t sbase,
-                                               uint32_t bars, uint32_t tmem, const AbortCtx& ab) {
+template <int D, int PARTS, bool TREE>
+__device__ __forceinline__ void chunk_mma_role(const CacheAttnArgs& a, ChunkWalk<TREE> w,
+                                               uint32_t sbase, uint32_t bars, uint32_t tmem, const AbortCtx& ab) {
   using L = ChunkLayout<D, PARTS>;
   constexpr int S = L::kStages;
   auto bar = [&](int i) { return bars + 8u * static_cast<uint32_t>(i); };
@@ -572,14 +597,16 @@ __device__ __forceinline__ void chunk_mma_role(const CacheAttnArgs& a, ChunkWalk
 
 // What a softmax warp needs between its tile loops only, kept in shared memory
 // meanwhile (16 words a warp): the loop holds 128 scores in registers.
+template <bool TREE>
 struct ChunkShelf {
-  ChunkWalk w;
+  ChunkWalk<TREE> w;
   uint32_t flags;  // parities: bits 0-1 items with O_i, bit 2 split items
   int share;
 };
-static_assert(sizeof(ChunkWalk) == 56 && sizeof(ChunkShelf) == 64, "16 words");
+static_assert(sizeof(ChunkWalk<true>) == 56 && sizeof(ChunkShelf<true>) == 64, "16 words");
 
-__device__ __forceinline__ void shelve(uint32_t at, const ChunkShelf& k, int lane) {
+template <bool TREE>
+__device__ __forceinline__ void shelve(uint32_t at, const ChunkShelf<TREE>& k, int lane) {
   uint32_t u[16];
   __builtin_memcpy(u, &k, 64);
   if (lane == 0) {
@@ -588,7 +615,8 @@ __device__ __forceinline__ void shelve(uint32_t at, const ChunkShelf& k, int lan
   }
   __syncwarp();
 }
-__device__ __forceinline__ ChunkShelf unshelve(uint32_t at) {
+template <bool TREE>
+__device__ __forceinline__ ChunkShelf<TREE> unshelve(uint32_t at) {
   uint32_t u[16];
 #pragma unroll
   for (int i = 0; i < 16; i += 4) {
@@ -599,7 +627,7 @@ __device__ __forceinline__ ChunkShelf unshelve(uint32_t at) {
     u[i + 3] = v.w;
   }
   __syncwarp();
-  ChunkShelf k;
+  ChunkShelf<TREE> k;
   __builtin_memcpy(&k, u, 64);
   return k;
 }
@@ -617,7 +645,8 @@ __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
   return a;
 }
 
-__device__ __forceinline__ RowAt row_at(const CacheAttnArgs& a, const ChunkWalk& w, int r) {
+template <bool TREE>
+__device__ __forceinline__ RowAt row_at(const CacheAttnArgs& a, const ChunkWalk<TREE>& w, int r) {
   const int row = w.rb * a.item_rows + r;  // (T * H is in int range)
   const int i = row / a.group;
   return {i, w.hk * a.group + row - i * a.group};
@@ -676,7 +705,8 @@ __device__ __forceinline__ void query_parts(const uint16_t* p, float fac, uint32
 
 // The first key of a block that exists in the share's tiles of the item (2^31 - 1:
 // none). Called by whole warps.
-__device__ __forceinline__ int first_key(const CacheAttnArgs& a, const ChunkWalk& w, int lane) {
+template <bool TREE>
+__device__ __forceinline__ int first_key(const CacheAttnArgs& a, const ChunkWalk<TREE>& w, int lane) {
   const int32_t* const table = a.table + static_cast<long long>(w.b) * a.table_width;
   const long long keys = min(static_cast<long long>(w.s.kv_len), 1LL * w.real_end * kChunkKeys);
   const int end = static_cast<int>((keys + (1 << a.block_shift) - 1) >> a.block_shift);
@@ -690,8 +720,8 @@ __device__ __forceinline__ int first_key(const CacheAttnArgs& a, const ChunkWalk
 
 // Whether a row sees a key of a block that exists in the share's tiles of the item,
 // of which `first` is the first one.
-__device__ __forceinline__ bool tree_sees_block(const CacheAttnArgs& a, const ChunkWalk& w, int row,
-                                                int first) {
+__device__ __forceinline__ bool tree_sees_block(const CacheAttnArgs& a, const ChunkWalk<true>& w,
+                                                int row, int first) {
   const long long end = min(static_cast<long long>(w.s.kv_len), 1LL * w.real_end * kChunkKeys);
 #pragma unroll 1
   for (int key = first; key < end; ++key) {
@@ -860,7 +890,7 @@ __device__ __forceinline__ bool softmax_tiles(const CacheAttnArgs& a, const Tile
 }
 
 template <int D, bool BF16, int PARTS, bool TREE>
-__device__ __forceinline__ void chunk_softmax_role(const CacheAttnArgs& a, const ChunkWalk& start,
+__device__ __forceinline__ void chunk_softmax_role(const CacheAttnArgs& a, const ChunkWalk<TREE>& start,
                                                    int share, uint8_t* sgen, uint32_t sbase,
                                                    uint32_t bars, uint32_t tmem, const AbortCtx& ab,
                                                    int warp, int lane) {
@@ -872,7 +902,7 @@ __device__ __forceinline__ void chunk_softmax_role(const CacheAttnArgs& a, const
   const uint32_t tl = ptx::tmem_lane_base(tmem, warp);
   const uint32_t shelf = sbase + L::kOffShelf + static_cast<uint32_t>(warp - 4) * 64u;
   uint32_t phase = 0, count = 0;  // parities (bits 0, 1: S_i; 2: O steps); tiles before the item
-  shelve(shelf, ChunkShelf{start, 0u, share}, lane);
+  shelve(shelf, ChunkShelf<TREE>{start, 0u, share}, lane);
   for (;;) {
     // ---- an item: Q, and what its tile loop needs
     int n;
@@ -880,8 +910,8 @@ __device__ __forceinline__ void chunk_softmax_role(const CacheAttnArgs& a, const
     TileLoop x;
     x.crow = a.scale_log2;
     {
-      const ChunkShelf k = unshelve(shelf);
-      const ChunkWalk& w = k.w;
+      const ChunkShelf<TREE> k = unshelve<TREE>(shelf);
+      const ChunkWalk<TREE>& w = k.w;
       n = w.n();
       const int rows = w.rows(a);
       const bool pair = PARTS == 0 && rows > 128;
@@ -967,8 +997,8 @@ __device__ __forceinline__ void chunk_softmax_role(const CacheAttnArgs& a, const
     }
 
     // ---- epilogue
-    ChunkShelf k = unshelve(shelf);
-    ChunkWalk& w = k.w;
+    ChunkShelf<TREE> k = unshelve<TREE>(shelf);
+    ChunkWalk<TREE>& w = k.w;
     const int rows = w.rows(a);
     const bool pair = PARTS == 0 && rows > 128;
     const int base = pair ? 128 * wg : 0;
@@ -980,7 +1010,7 @@ __device__ __forceinline__ void chunk_softmax_role(const CacheAttnArgs& a, const
       part = a.parts + (2LL * blockIdx.x + (begins ? 1 : 0)) * partial_floats(a.item_rows, D);
     if (!ends && begins && wg == 0 && r == 0)
       a.join[blockIdx.x] =
-          join_item(w.b, w.hk, w.rb, rows, 1 + (w.tiles - w.t1 + k.share - 1) / k.share);
+          join_item(w.b, w.hk, w.rb, rows, w.parts(k.share));
     const bool two = !pair;  // results of two warpgroups
     float* const s_m = reinterpret_cast<float*>(sgen + L::kOffStats);
     if (two && wg == 1) {
@@ -1013,7 +1043,9 @@ __device__ __forceinline__ void chunk_softmax_role(const CacheAttnArgs& a, const
       // blocks too: where it sees no other keys they count for nothing.
       if (__any_sync(0xffffffffu, l != l)) {
         const int first = first_key(a, w, lane);
-        if (l != l && (TREE ? !tree_sees_block(a, w, x.lim, first) : x.lim <= first)) {
+        bool sees = x.lim > first;
+        if constexpr (TREE) sees = l != l && tree_sees_block(a, w, x.lim, first);
+        if (l != l && !sees) {
           m_ref = -INFINITY;
           l = 0.f;
         }
@@ -1137,6 +1169,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   volatile uint32_t* abort_flag =
       reinterpret_cast<volatile uint32_t*>(sgen + L::kOffBar + kChunkSlotAbort);
   int* const s_start = reinterpret_cast<int*>(sgen + L::kOffBar + kChunkSlotStart);  // b, hk, rb, t0
+  int* const s_moved = reinterpret_cast<int*>(sgen + L::kOffBar + kChunkSlotMoved);
   long long* const s_scan = reinterpret_cast<long long*>(sgen);  // (before Q)
   const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
   const AbortCtx ab{abort_flag, a.status};
@@ -1181,7 +1214,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   const int run = (a.B + kChunkThreads - 1) / kChunkThreads;
   const int b0 = min(tid * run, a.B), b1 = min(b0 + run, a.B);
   long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += a.Hkv * chunk_head_tiles(a, seq_rows(a, b));
+  for (int b = b0; b < b1; ++b) mine += a.Hkv * chunk_head_tiles<TREE>(a, seq_rows(a, b));
   long long upto = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -1203,28 +1236,49 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
   }
-  if (u0 >= upto - mine && u0 < upto) {
+  // the item that u counted tiles from the list's start lie in, and how far behind its start
+  auto locate = [&](long long u, int (&at_item)[4]) {
     long long at = upto - mine, head_tiles;
     int b = b0;
     SeqRows s;
     for (;; ++b) {
       s = seq_rows(a, b);
-      head_tiles = chunk_head_tiles(a, s);
-      if (u0 < at + a.Hkv * head_tiles) break;
+      head_tiles = chunk_head_tiles<TREE>(a, s);
+      if (u < at + a.Hkv * head_tiles) break;
       at += a.Hkv * head_tiles;
     }
-    const int hk = static_cast<int>((u0 - at) / head_tiles);
-    long long rest = u0 - at - hk * head_tiles;
-    int rb = 0;
+    const int hk = static_cast<int>((u - at) / head_tiles);
+    long long rest = u - at - hk * head_tiles;
+    int rb = 0, n;
     for (;; ++rb) {
-      const int n = max(1, chunk_real_tiles(a, s, rb));
+      n = max(1, chunk_real_tiles(a, s, rb)) + (TREE ? kTreeLead : 0);
       if (rest < n) break;
       rest -= n;
     }
-    s_start[0] = b;
-    s_start[1] = hk;
-    s_start[2] = rb;
-    s_start[3] = static_cast<int>(rest);
+    at_item[0] = b;
+    at_item[1] = hk;
+    at_item[2] = rb;
+    at_item[3] = static_cast<int>(rest);
+    return n;
+  };
+  if (u0 >= upto - mine && u0 < upto) {
+    int it[4];
+    const int n = locate(u0, it);
+    s_start[0] = it[0];
+    s_start[1] = it[1];
+    s_start[2] = it[2];
+    s_start[3] = TREE ? tree_cut(it[3], n, tree_piece(share)) : it[3];
+    if constexpr (TREE) s_moved[0] = s_start[3] - it[3];
+  }
+  if constexpr (TREE) {
+    if (u1 == total ? tid == 0 : u1 >= upto - mine && u1 < upto) {
+      int it[4];
+      s_moved[1] = 0;
+      if (u1 < total) {
+        const int n = locate(u1, it);
+        s_moved[1] = tree_cut(it[3], n, tree_piece(share)) - it[3];
+      }
+    }
   }
   if (warp == 0) {
     ptx::tmem_alloc(ptx::smem_u32(tmem_slot), L::kTmemCols);
@@ -1234,14 +1288,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  ChunkWalk w;
-  w.start(a, s_start[0], s_start[1], s_start[2], s_start[3], u1 - u0);
+  ChunkWalk<TREE> w;
+  // (trees: a share whose ends were moved to one place has no tiles)
+  const long long len = TREE ? u1 + s_moved[1] - u0 - s_moved[0] : u1 - u0;
+  if (len > 0) w.start(a, s_start[0], s_start[1], s_start[2], s_start[3], len);
 
   const int wgrp = warp >> 2;
-  if (wgrp == 0) {
+  if (TREE && len <= 0) {
+  } else if (wgrp == 0) {
     ptx::setmaxnreg_dec<kChunkRegsMma>();
-    if (warp == 0) chunk_mma_role<D, PARTS>(a, w, sbase, bars, tmem, ab);
-    else if (warp == 1) chunk_copy_role<D, PARTS>(&tm_k, &tm_v, a, w, sgen, sbase, bars, ab, lane);
+    if (warp == 0) chunk_mma_role<D, PARTS, TREE>(a, w, sbase, bars, tmem, ab);
+    else if (warp == 1) chunk_copy_role<D, PARTS, TREE>(&tm_k, &tm_v, a, w, sgen, sbase, bars, ab, lane);
   } else if (wgrp < 3) {
     ptx::setmaxnreg_inc<kChunkRegsSoftmax>();
     chunk_softmax_role<D, BF16, PARTS, TREE>(a, w, static_cast<int>(share), sgen, sbase, bars, tmem, ab,

@@ -147,10 +147,13 @@ cudaError_t launch_all(CacheAttnArgs a, const fa_cache& c, const AttnPlan& p, in
     a.rows_upto = INT_MAX;
     a.join = sides.join[1];
     a.parts = sides.parts[1];
-    const cudaError_t e =
-        p.item_rows == kChunkRows
-            ? launch_chunk<D, BF16, 0, TREE>(a, c, p, cgrid, stream, mapped)
-            : launch_chunk<D, BF16, chunk_parts(D, BF16), TREE>(a, c, p, cgrid, stream, mapped);
+    cudaError_t e;
+    if constexpr (TREE && chunk_parts(D, BF16) > 0)
+      e = launch_chunk<D, BF16, chunk_parts(D, BF16), TREE>(a, c, p, cgrid, stream, mapped);
+    else
+      e = p.item_rows == kChunkRows
+              ? launch_chunk<D, BF16, 0, TREE>(a, c, p, cgrid, stream, mapped)
+              : launch_chunk<D, BF16, chunk_parts(D, BF16), TREE>(a, c, p, cgrid, stream, mapped);
     if (e != cudaSuccess) return e;
   }
   const int n = sides.ctas[0] + sides.ctas[1];
@@ -173,7 +176,8 @@ cudaError_t launch_attn(const CacheAttnArgs& a, const fa_cache& c, bool bf16, in
   // step kernel too, which the host cannot tell from the others: one chunk of 2048
   // tokens behind 14336 others (behind none) beside 200 single tokens, 8 query heads to
   // a K / V head, takes 524 / 468 us (308 / 207), one of 512 tokens 116 / 123.
-  if (chunk_parts(c.d, bf16) > 0 && static_cast<long long>(a.T) * a.group <= 128LL * a.B)
+  // Trees: always, where there is that kernel.
+  if (chunk_parts(c.d, bf16) > 0 && (TREE || static_cast<long long>(a.T) * a.group <= 128LL * a.B))
     p.item_rows = 128;
   *mapped = true;
   if (c.d == 64)

@@ -137,12 +137,11 @@ class Batch:
         T = self.cu[-1]
         q = self.q[:T].double().cpu().numpy()
         g = self.q.shape[1] // self.scales.shape[2]
-        avg = T * g / len(self.counts)
         fp16 = self.dt == torch.float16
         # two parts of a weight: fp16, and every sequence on the kernel for few rows;
-        # queries in 8-bit parts: d 128, 17 to 128 rows on average
+        # queries in 8-bit parts: d 128, the kernel for more rows
         two = fp16 and max(self.counts) * g <= 16
-        floor = 2.0 ** -17 if q.shape[2] == 128 and avg <= 128 and max(self.counts) * g > 16 else 0.0
+        floor = 2.0 ** -17 if q.shape[2] == 128 and max(self.counts) * g > 16 else 0.0
         return D.attend(q, self.codes[0], self.codes[1], self.scales[0].astype(float),
                         self.scales[1].astype(float), self.table, self.kv, self.cu, self.masks, self.bs,
                         self.scale, 2.0 ** -10 if fp16 else 2.0 ** -7, two, floor)
