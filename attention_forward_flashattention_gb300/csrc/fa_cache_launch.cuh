@@ -24,7 +24,7 @@ struct AttnPlan {
   int item_rows = kChunkRows;  // most rows of the chunk kernel's items: 256 or 128
 };
 
-AttnPlan plan_attn(int B, int T, int group, bool ragged) {
+AttnPlan plan_attn(int B, int T, int group, bool ragged, bool tree = false) {
   AttnPlan p;
   const long long most = static_cast<long long>(T) * group;  // rows of a sequence to a K / V head
   if (!ragged || B == 1 || T <= B || most <= kStepMaxRows) {
@@ -39,7 +39,11 @@ AttnPlan plan_attn(int B, int T, int group, bool ragged) {
     const long long rows = !ragged ? most / B : (T <= B && B > 1 ? group : most);
     p.nt = rows <= 8 ? 1 : (rows <= kStepMaxRows ? 2 : 0);
     p.chunk = p.nt == 0;
-  } else if (group > kStepMaxRows) {
+  } else if (group > kStepMaxRows || (tree && most > static_cast<long long>(kStepMaxRows) * B)) {
+    // Trees of more than 16 rows on average are one launch: those of fewer rows cost
+    // the chunk kernel hardly more, and the launch before it does not take part in its
+    // shares. 32 trees of up to 16 / 32 / 64 tokens, 4 heads to a K / V head, up to
+    // 16384 keys, d 128: 153 / 157 / 234 us so, 219 / 180 / 270 as a mixture.
     p.chunk = true;
   } else {
     // a batch of single tokens and longer pieces, in a mixture that only the
@@ -168,7 +172,7 @@ cudaError_t launch_all(CacheAttnArgs a, const fa_cache& c, const AttnPlan& p, in
 template <bool TREE>
 cudaError_t launch_attn(const CacheAttnArgs& a, const fa_cache& c, bool bf16, int sm_count,
                         float* ws, cudaStream_t stream, bool* mapped) {
-  AttnPlan p = plan_attn(a.B, a.T, a.group, a.cu_q != nullptr);
+  AttnPlan p = plan_attn(a.B, a.T, a.group, a.cu_q != nullptr, TREE);
   // Items of 128 rows, K unwidened, where sequences have up to 128 rows to a K / V
   // head on average. Us of ragged calls with items of 256 rows beside it, bf16 (fp16),
   // 4 K / V heads, 8192 keys: 16 x 24 rows 70 / 77 (72 / 74), 16 x 64 rows 71 / 77
