@@ -88,7 +88,8 @@ struct ChunkLayout {
   static constexpr int kOffNan = kOffScale + 16 * 8 * 16;    // [8 items][D] uint64
   static constexpr int kOffStats = kOffNan + 8 * D * 8;      // [2][128] m, l of the second halves
   static constexpr int kOffShelf = kOffStats + 1024;  // [8 warps] 64 bytes
-  static constexpr int kOffBar = kOffShelf + 512;
+  static constexpr int kOffFactor = kOffShelf + 512;  // trees: [128] of the rows' queries
+  static constexpr int kOffBar = kOffFactor + 512;
   static constexpr int kSmem = kOffBar + 544 + 1024;  // barriers, alignment slack
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kColS = 0, kColO = 256;
@@ -124,6 +125,17 @@ __device__ __forceinline__ int keys_seen(const CacheAttnArgs& a, const SeqRows& 
   return a.causal ? min(max(s.kv_len - s.count + i + 1, 0), s.kv_len) : s.kv_len;
 }
 
+// a / b of numbers that are not negative; a division of 64 bits takes as long as five of 32.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
+}
+
+// Rows of an item: a.item_rows, which for trees (ROWS > 0) is known here.
+template <int ROWS>
+__device__ __forceinline__ int rows_of_item(const CacheAttnArgs& a) {
+  return ROWS > 0 ? ROWS : a.item_rows;
+}
+
 // Keys that every row of an item sees whose first row is that of query token i.
 template <bool TREE>
 __device__ __forceinline__ int keys_all_see(const CacheAttnArgs& a, const SeqRows& s, int i) {
@@ -132,23 +144,28 @@ __device__ __forceinline__ int keys_all_see(const CacheAttnArgs& a, const SeqRow
 
 // Row blocks of a sequence, and the tiles that one of them reads (counted: at
 // least one, so that rows without keys are written).
+template <int ROWS>
 __device__ __forceinline__ int chunk_row_blocks(const CacheAttnArgs& a, const SeqRows& s) {
+  if constexpr (ROWS > 0)  // (T * H is in int range)
+    return takes_seq(a, s) ? (s.count * a.group - 1) / ROWS + 1 : 0;
   const long long rows = static_cast<long long>(s.count) * a.group;
   return takes_seq(a, s) ? static_cast<int>((rows + a.item_rows - 1) / a.item_rows) : 0;
 }
+template <int ROWS>
 __device__ __forceinline__ int chunk_real_tiles(const CacheAttnArgs& a, const SeqRows& s, int rb) {
+  if constexpr (ROWS > 0) return (s.kv_len + kChunkKeys - 1) / kChunkKeys;
   const long long last = min((rb + 1LL) * a.item_rows, static_cast<long long>(s.count) * a.group) - 1;
   return (keys_seen(a, s, static_cast<int>(last / a.group)) + kChunkKeys - 1) / kChunkKeys;
 }
 // Tiles of one head of a sequence, as they count.
-template <bool TREE>
+template <int ROWS>
 __device__ __forceinline__ long long chunk_head_tiles(const CacheAttnArgs& a, const SeqRows& s) {
-  const int n = chunk_row_blocks(a, s);
-  if (!a.causal)
+  const int n = chunk_row_blocks<ROWS>(a, s);
+  if (ROWS > 0 || !a.causal)
     return static_cast<long long>(n) *
-           (max(1, (s.kv_len + kChunkKeys - 1) / kChunkKeys) + (TREE ? kTreeLead : 0));
+           (max(1, (s.kv_len + kChunkKeys - 1) / kChunkKeys) + (ROWS > 0 ? kTreeLead : 0));
   long long sum = 0;
-  for (int rb = 0; rb < n; ++rb) sum += max(1, chunk_real_tiles(a, s, rb));
+  for (int rb = 0; rb < n; ++rb) sum += max(1, chunk_real_tiles<ROWS>(a, s, rb));
   return sum;
 }
 
@@ -163,8 +180,9 @@ __device__ __forceinline__ int tree_cut(int x, int tiles, int piece) {
 }
 
 // A CTA's share, item by item (every role walks a copy of its own).
-template <bool TREE>
+template <int ROWS>
 struct ChunkWalk {
+  static constexpr bool TREE = ROWS > 0;
   int b, hk, rb, n_rb;
   int tiles;     // counted tiles of the item
   int t0, t1;    // the share's tiles of it
@@ -174,7 +192,7 @@ struct ChunkWalk {
   SeqRows s;
 
   __device__ __forceinline__ void item_tiles(const CacheAttnArgs& a) {
-    const int real = chunk_real_tiles(a, s, rb);
+    const int real = chunk_real_tiles<ROWS>(a, s, rb);
     tiles = max(1, real) + (TREE ? kTreeLead : 0);
     t1 = static_cast<int>(min(static_cast<long long>(tiles), t0 + left));
     real_end = min(t1, real);
@@ -193,7 +211,7 @@ struct ChunkWalk {
     left = n;
     item = 0;
     s = seq_rows(a, b);
-    n_rb = chunk_row_blocks(a, s);
+    n_rb = chunk_row_blocks<ROWS>(a, s);
     item_tiles(a);
     if (TREE && t0 == tiles) next(a);  // (the cut was moved to the item's end)
   }
@@ -208,7 +226,7 @@ struct ChunkWalk {
         do {
           ++b;
           s = seq_rows(a, b);
-          n_rb = chunk_row_blocks(a, s);
+          n_rb = chunk_row_blocks<ROWS>(a, s);
         } while (n_rb == 0);  // ends: tiles are left
       }
     }
@@ -217,6 +235,7 @@ struct ChunkWalk {
     return true;
   }
   __device__ __forceinline__ int rows(const CacheAttnArgs& a) const {
+    if constexpr (ROWS > 0) return min(ROWS, s.count * a.group - rb * ROWS);
     return static_cast<int>(min(static_cast<long long>(a.item_rows),
                                 static_cast<long long>(s.count) * a.group -
                                     static_cast<long long>(rb) * a.item_rows));
@@ -226,9 +245,9 @@ struct ChunkWalk {
 
 // ---- copies: warp 1. Lane j < 128 / block handles the j-th block of a tile,
 // lane g < 8 the scales of the g-th 16-key group.
-template <int D, int PARTS, bool TREE>
+template <int D, int PARTS, int ROWS>
 __device__ __forceinline__ void chunk_copy_role(const CUtensorMap* tm_k, const CUtensorMap* tm_v,
-                                                const CacheAttnArgs& a, ChunkWalk<TREE> w,
+                                                const CacheAttnArgs& a, ChunkWalk<ROWS> w,
                                                 uint8_t* sgen, uint32_t sbase, uint32_t bars, const AbortCtx& ab,
                                                 int lane) {
   using L = ChunkLayout<D, PARTS>;
@@ -345,8 +364,8 @@ __device__ __forceinline__ void chunk_copy_role(const CUtensorMap* tm_k, const C
 
 // ---- converters: warps 12-15. A thread takes 16 codes of a row at a time: 32
 // bytes in two chunks of one of the row's 128-byte panels.
-template <int D, int PARTS, bool TREE>
-__device__ __forceinline__ void chunk_convert_role(const CacheAttnArgs& a, ChunkWalk<TREE> w,
+template <int D, int PARTS, int ROWS>
+__device__ __forceinline__ void chunk_convert_role(const CacheAttnArgs& a, ChunkWalk<ROWS> w,
                                                    uint8_t* sgen, uint32_t sbase, uint32_t bars,
                                                    const AbortCtx& ab, int warp, int lane) {
   using L = ChunkLayout<D, PARTS>;
@@ -377,7 +396,7 @@ __device__ __forceinline__ void chunk_convert_role(const CacheAttnArgs& a, Chunk
   uint32_t ring = 0, count = 0;  // slots filled, tiles done
   bool ok = true;
   do {
-    const int first_seen = keys_all_see<TREE>(
+    const int first_seen = keys_all_see<(ROWS > 0)>(
         a, w.s, static_cast<int>(static_cast<long long>(w.rb) * a.item_rows / a.group));
     const int halves = L::kHalves * max(0, w.real_end - w.t0);  // (K and) V of each tile
 #pragma unroll 1
@@ -483,8 +502,8 @@ __device__ __forceinline__ void issue_pv_half(uint32_t d_tmem, uint32_t p_tmem, 
 }
 
 // ---- MMA issue: warp 0
-template <int D, int PARTS, bool TREE>
-__device__ __forceinline__ void chunk_mma_role(const CacheAttnArgs& a, ChunkWalk<TREE> w,
+template <int D, int PARTS, int ROWS>
+__device__ __forceinline__ void chunk_mma_role(const CacheAttnArgs& a, ChunkWalk<ROWS> w,
                                                uint32_t sbase, uint32_t bars, uint32_t tmem, const AbortCtx& ab) {
   using L = ChunkLayout<D, PARTS>;
   constexpr int S = L::kStages;
@@ -597,16 +616,16 @@ __device__ __forceinline__ void chunk_mma_role(const CacheAttnArgs& a, ChunkWalk
 
 // What a softmax warp needs between its tile loops only, kept in shared memory
 // meanwhile (16 words a warp): the loop holds 128 scores in registers.
-template <bool TREE>
+template <int ROWS>
 struct ChunkShelf {
-  ChunkWalk<TREE> w;
+  ChunkWalk<ROWS> w;
   uint32_t flags;  // parities: bits 0-1 items with O_i, bit 2 split items
   int share;
 };
-static_assert(sizeof(ChunkWalk<true>) == 56 && sizeof(ChunkShelf<true>) == 64, "16 words");
+static_assert(sizeof(ChunkWalk<128>) == 56 && sizeof(ChunkShelf<true>) == 64, "16 words");
 
-template <bool TREE>
-__device__ __forceinline__ void shelve(uint32_t at, const ChunkShelf<TREE>& k, int lane) {
+template <int ROWS>
+__device__ __forceinline__ void shelve(uint32_t at, const ChunkShelf<ROWS>& k, int lane) {
   uint32_t u[16];
   __builtin_memcpy(u, &k, 64);
   if (lane == 0) {
@@ -615,8 +634,8 @@ __device__ __forceinline__ void shelve(uint32_t at, const ChunkShelf<TREE>& k, i
   }
   __syncwarp();
 }
-template <bool TREE>
-__device__ __forceinline__ ChunkShelf<TREE> unshelve(uint32_t at) {
+template <int ROWS>
+__device__ __forceinline__ ChunkShelf<ROWS> unshelve(uint32_t at) {
   uint32_t u[16];
 #pragma unroll
   for (int i = 0; i < 16; i += 4) {
@@ -627,7 +646,7 @@ __device__ __forceinline__ ChunkShelf<TREE> unshelve(uint32_t at) {
     u[i + 3] = v.w;
   }
   __syncwarp();
-  ChunkShelf<TREE> k;
+  ChunkShelf<ROWS> k;
   __builtin_memcpy(&k, u, 64);
   return k;
 }
@@ -645,9 +664,9 @@ __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
   return a;
 }
 
-template <bool TREE>
-__device__ __forceinline__ RowAt row_at(const CacheAttnArgs& a, const ChunkWalk<TREE>& w, int r) {
-  const int row = w.rb * a.item_rows + r;  // (T * H is in int range)
+template <int ROWS>
+__device__ __forceinline__ RowAt row_at(const CacheAttnArgs& a, const ChunkWalk<ROWS>& w, int r) {
+  const int row = w.rb * rows_of_item<ROWS>(a) + r;  // (T * H is in int range)
   const int i = row / a.group;
   return {i, w.hk * a.group + row - i * a.group};
 }
@@ -660,6 +679,34 @@ __device__ __forceinline__ float e4m3_step(uint32_t top) {
   const int e = max(static_cast<int>(__float_as_uint(big) >> 23) - 127 - 7, -126);
   const float fac = top == 0u ? 1.f : __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
   return top >= (BF16 ? 0x7F80u : 0x7C00u) ? __int_as_float(0x7FFFFFFF) : fac;
+}
+
+// 16 elements of a query row (h: packed pairs) as PARTS e4m3 rows at `to` (row r of tiles
+// of kChunkKeys rows, chunk e of them): see query_parts.
+template <int D, bool BF16, int PARTS>
+__device__ __forceinline__ void cut_parts(uint32_t (&h)[8], float inv, uint32_t to, int r, int e) {
+#pragma unroll
+  for (int x = 0; x < 8; ++x) {
+    float2 f;
+    if constexpr (BF16)
+      f = make_float2(__uint_as_float(h[x] << 16), __uint_as_float(h[x] & 0xFFFF0000u));
+    else
+      f = unpack_f16(h[x]);
+    h[x] = pack_f16(f.x * inv, f.y * inv);
+  }
+#pragma unroll
+  for (int q = 0; q < PARTS; ++q) {
+    uint32_t code[4];
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      const uint16_t c = ptx::f16x2_to_e4m3x2(h[x]);
+      code[x >> 1] = x & 1 ? code[x >> 1] | (static_cast<uint32_t>(c) << 16) : c;
+      if (q + 1 < PARTS) h[x] = sub_f16x2(h[x], ptx::e4m3x2_to_f16x2(c));
+    }
+    ptx::st_shared_v4(to + static_cast<uint32_t>(q * kChunkKeys * D + r * D) +
+                          (static_cast<uint32_t>(e ^ (r & 7)) << 4),
+                      code[0], code[1], code[2], code[3]);
+  }
 }
 
 // Chunks e0 .. e1 - 1 (16 elements each) of this thread's query row p as PARTS
@@ -678,35 +725,14 @@ __device__ __forceinline__ void query_parts(const uint16_t* p, float fac, uint32
     const uint4 u0 = *reinterpret_cast<const uint4*>(p + 16 * e);
     const uint4 u1 = *reinterpret_cast<const uint4*>(p + 16 * e + 8);
     uint32_t h[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
-#pragma unroll
-    for (int x = 0; x < 8; ++x) {
-      float2 f;
-      if constexpr (BF16)
-        f = make_float2(__uint_as_float(h[x] << 16), __uint_as_float(h[x] & 0xFFFF0000u));
-      else
-        f = unpack_f16(h[x]);
-      h[x] = pack_f16(f.x * inv, f.y * inv);
-    }
-#pragma unroll
-    for (int q = 0; q < PARTS; ++q) {
-      uint32_t code[4];
-#pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        const uint16_t c = ptx::f16x2_to_e4m3x2(h[x]);
-        code[x >> 1] = x & 1 ? code[x >> 1] | (static_cast<uint32_t>(c) << 16) : c;
-        if (q + 1 < PARTS) h[x] = sub_f16x2(h[x], ptx::e4m3x2_to_f16x2(c));
-      }
-      ptx::st_shared_v4(to + static_cast<uint32_t>(q * kChunkKeys * D + r * D) +
-                            (static_cast<uint32_t>(e ^ (r & 7)) << 4),
-                        code[0], code[1], code[2], code[3]);
-    }
+    cut_parts<D, BF16, PARTS>(h, inv, to, r, e);
   }
 }
 
 // The first key of a block that exists in the share's tiles of the item (2^31 - 1:
 // none). Called by whole warps.
-template <bool TREE>
-__device__ __forceinline__ int first_key(const CacheAttnArgs& a, const ChunkWalk<TREE>& w, int lane) {
+template <int ROWS>
+__device__ __forceinline__ int first_key(const CacheAttnArgs& a, const ChunkWalk<ROWS>& w, int lane) {
   const int32_t* const table = a.table + static_cast<long long>(w.b) * a.table_width;
   const long long keys = min(static_cast<long long>(w.s.kv_len), 1LL * w.real_end * kChunkKeys);
   const int end = static_cast<int>((keys + (1 << a.block_shift) - 1) >> a.block_shift);
@@ -720,7 +746,8 @@ __device__ __forceinline__ int first_key(const CacheAttnArgs& a, const ChunkWalk
 
 // Whether a row sees a key of a block that exists in the share's tiles of the item,
 // of which `first` is the first one.
-__device__ __forceinline__ bool tree_sees_block(const CacheAttnArgs& a, const ChunkWalk<true>& w,
+template <int ROWS>
+__device__ __forceinline__ bool tree_sees_block(const CacheAttnArgs& a, const ChunkWalk<ROWS>& w,
                                                 int row, int first) {
   const long long end = min(static_cast<long long>(w.s.kv_len), 1LL * w.real_end * kChunkKeys);
 #pragma unroll 1
@@ -889,12 +916,13 @@ __device__ __forceinline__ bool softmax_tiles(const CacheAttnArgs& a, const Tile
   return true;
 }
 
-template <int D, bool BF16, int PARTS, bool TREE>
-__device__ __forceinline__ void chunk_softmax_role(const CacheAttnArgs& a, const ChunkWalk<TREE>& start,
+template <int D, bool BF16, int PARTS, int ROWS>
+__device__ __forceinline__ void chunk_softmax_role(const CacheAttnArgs& a, const ChunkWalk<ROWS>& start,
                                                    int share, uint8_t* sgen, uint32_t sbase,
                                                    uint32_t bars, uint32_t tmem, const AbortCtx& ab,
                                                    int warp, int lane) {
   using L = ChunkLayout<D, PARTS>;
+  constexpr bool TREE = ROWS > 0;
   constexpr int kLanes = D / 8, kRowsPerTurn = 32 / kLanes;  // 16 bytes of a 16-bit row each
   auto bar = [&](int i) { return bars + 8u * static_cast<uint32_t>(i); };
   const int wg = (warp >> 2) - 1;
@@ -902,7 +930,7 @@ __device__ __forceinline__ void chunk_softmax_role(const CacheAttnArgs& a, const
   const uint32_t tl = ptx::tmem_lane_base(tmem, warp);
   const uint32_t shelf = sbase + L::kOffShelf + static_cast<uint32_t>(warp - 4) * 64u;
   uint32_t phase = 0, count = 0;  // parities (bits 0, 1: S_i; 2: O steps); tiles before the item
-  shelve(shelf, ChunkShelf<TREE>{start, 0u, share}, lane);
+  shelve(shelf, ChunkShelf<ROWS>{start, 0u, share}, lane);
   for (;;) {
     // ---- an item: Q, and what its tile loop needs
     int n;
@@ -910,8 +938,8 @@ __device__ __forceinline__ void chunk_softmax_role(const CacheAttnArgs& a, const
     TileLoop x;
     x.crow = a.scale_log2;
     {
-      const ChunkShelf<TREE> k = unshelve<TREE>(shelf);
-      const ChunkWalk<TREE>& w = k.w;
+      const ChunkShelf<ROWS> k = unshelve<ROWS>(shelf);
+      const ChunkWalk<ROWS>& w = k.w;
       n = w.n();
       const int rows = w.rows(a);
       const bool pair = PARTS == 0 && rows > 128;
@@ -997,8 +1025,8 @@ __device__ __forceinline__ void chunk_softmax_role(const CacheAttnArgs& a, const
     }
 
     // ---- epilogue
-    ChunkShelf<TREE> k = unshelve<TREE>(shelf);
-    ChunkWalk<TREE>& w = k.w;
+    ChunkShelf<ROWS> k = unshelve<ROWS>(shelf);
+    ChunkWalk<ROWS>& w = k.w;
     const int rows = w.rows(a);
     const bool pair = PARTS == 0 && rows > 128;
     const int base = pair ? 128 * wg : 0;
@@ -1155,11 +1183,231 @@ __device__ __forceinline__ void chunk_softmax_role(const CacheAttnArgs& a, const
   }
 }
 
+// ---- softmax and epilogue for trees, items of up to 128 rows with queries in parts.
+// As chunk_softmax_role in split mode, but the second warpgroup, which has nothing
+// to do while the first one writes the item's results, brings the next item's queries
+// meanwhile (all of them; of the first item each warpgroup half). Their factors go to the
+// first warpgroup through shared memory, and results go from registers to
+// global memory, since the queries' tiles are not free to stage them: code that runs
+// once for an item is fetched for each, so what is short is fast.
+
+// Row p of the queries into parts, chunks e0 .. e1 - 1 of 16 elements, the next ones requested
+// while these are cut up.
+template <int D, bool BF16, int PARTS>
+__device__ __forceinline__ void tree_query_parts(const uint16_t* p, float fac, uint32_t to, int r,
+                                                 int e0, int e1) {
+  const float inv = 1.f / fac;
+  uint4 n0 = *reinterpret_cast<const uint4*>(p + 16 * e0);
+  uint4 n1 = *reinterpret_cast<const uint4*>(p + 16 * e0 + 8);
+#pragma unroll 1
+  for (int e = e0; e < e1; ++e) {
+    uint32_t h[8] = {n0.x, n0.y, n0.z, n0.w, n1.x, n1.y, n1.z, n1.w};
+    const int next = min(e + 1, e1 - 1);
+    n0 = *reinterpret_cast<const uint4*>(p + 16 * next);
+    n1 = *reinterpret_cast<const uint4*>(p + 16 * next + 8);
+    cut_parts<D, BF16, PARTS>(h, inv, to, r, e);
+  }
+}
+
+// Brings this thread's row of an item's queries: chunks e0 .. e1 - 1 of it. Returns its factor.
+template <int D, bool BF16, int PARTS>
+__device__ __forceinline__ float tree_queries(const CacheAttnArgs& a, const ChunkWalk<128>& w, int r,
+                                              uint32_t s_q, int e0, int e1) {
+  const int rows = w.rows(a);
+  const bool there = r < rows;
+  const RowAt at = row_at(a, w, there ? r : 0);
+  const uint16_t* p = static_cast<const uint16_t*>(a.q) + q_offset(a, w.b, w.s, at.i, at.head);
+  uint32_t top = 0;
+  if (there) {
+#pragma unroll
+    for (int e = 0; e < D / 8; ++e) {
+      const uint4 v = *reinterpret_cast<const uint4*>(p + 8 * e);
+      constexpr uint32_t kAbs = 0x7FFF7FFFu;
+      top = __vmaxu2(__vmaxu2(top, __vmaxu2(v.x & kAbs, v.y & kAbs)),
+                     __vmaxu2(v.z & kAbs, v.w & kAbs));
+    }
+  }
+  const float fac = e4m3_step<BF16>(max(top & 0xFFFFu, top >> 16));
+  if (there) tree_query_parts<D, BF16, PARTS>(p, fac, s_q, r, e0, e1);
+  return fac;
+}
+
+template <int D, bool BF16, int PARTS>
+__device__ __forceinline__ void tree_softmax_role(const CacheAttnArgs& a, const ChunkWalk<128>& start,
+                                                  int share, uint8_t* sgen, uint32_t sbase,
+                                                  uint32_t bars, uint32_t tmem, const AbortCtx& ab,
+                                                  int warp, int lane) {
+  using L = ChunkLayout<D, PARTS>;
+  constexpr int kRows = 128;
+  auto bar = [&](int i) { return bars + 8u * static_cast<uint32_t>(i); };
+  const int wg = (warp >> 2) - 1;
+  const int r = (warp & 3) * 32 + lane;
+  const uint32_t tl = ptx::tmem_lane_base(tmem, warp);
+  const uint32_t shelf = sbase + L::kOffShelf + static_cast<uint32_t>(warp - 4) * 64u;
+  float* const s_factor = reinterpret_cast<float*>(sgen + L::kOffFactor);
+  float* const s_m = reinterpret_cast<float*>(sgen + L::kOffStats);
+  uint32_t phase = 0, count = 0;  // parities (bits 0, 1: S_i; 2: O steps); tiles before the item
+  float fac = 1.f;  // of this thread's row
+  // flags, parities: bit 0 items with O and Q, bit 2 items
+  shelve(shelf, ChunkShelf<128>{start, 0u, share}, lane);
+  if (start.n() > 0) {
+    fac = tree_queries<D, BF16, PARTS>(a, start, r, sbase + L::kOffQ, wg * (D / 32),
+                                                   (wg + 1) * (D / 32));
+    ptx::fence_proxy_async_smem();
+    ptx::mbar_arrive(bar(kCbQFull + wg));
+  }
+  for (;;) {
+    int n;
+    TileLoop x;
+    {
+      const ChunkShelf<128> k = unshelve<128>(shelf);
+      const ChunkWalk<128>& w = k.w;
+      n = w.n();
+      const int rows = w.rows(a);
+      x.tl = tl;
+      x.phase = phase;
+      x.wg = wg;
+      x.n = n;
+      x.count = count;
+      x.k0 = w.t0 * kChunkKeys;
+      x.lim = w.s.first + row_at(a, w, r < rows ? r : 0).i;
+      x.lim0 = w.s.kv_len - w.s.count;
+      x.kv_len = w.s.kv_len;
+      x.idle = r - lane >= rows;
+      x.crow = fmaxf(a.scale_log2 * fac, 0x1p-80f);  // (as in chunk_softmax_role)
+    }
+    float m_ref = -INFINITY, l = 0.f;
+    if (!softmax_tiles<D, 64, PARTS, true>(a, x, sgen, bars, ab, m_ref, l)) return;
+    phase ^= static_cast<uint32_t>((((n + 1) >> 1) & 1) | (n & 2) | ((n & 1) << 2));
+
+    ChunkShelf<128> k = unshelve<128>(shelf);
+    ChunkWalk<128>& w = k.w;
+    const uint32_t flags = k.flags;
+    const bool begins = w.t0 == 0, ends = w.t1 == w.tiles;
+    if (wg == 1) {
+      s_m[r] = m_ref;
+      s_m[kRows + r] = l;
+      ptx::mbar_arrive(bar(kCbStats));
+    } else {
+      const int rows = w.rows(a);
+      const bool there = r < rows;
+      float* part = nullptr;
+      if (!begins || !ends)
+        part = a.parts + (2LL * blockIdx.x + (begins ? 1 : 0)) * partial_floats(kRows, D);
+      if (!ends && begins && r == 0)
+        a.join[blockIdx.x] = join_item(w.b, w.hk, w.rb, rows, w.parts(k.share));
+      // the last V of the item has been converted: its NaN columns are known
+      if (n > 0) {
+        const uint32_t tix = count + static_cast<uint32_t>(n - 1);
+        if (!wait_bounded_warp(bar(kCbVDone + (tix & 7u)), (tix >> 3) & 1u, ab, kStatusEpilogue) ||
+            !wait_bounded_warp(bar(kCbOFull), flags & 1u, ab, kStatusEpilogue))
+          return;
+      }
+      if (!wait_bounded_warp(bar(kCbStats), (flags >> 2) & 1u, ab, kStatusEpilogue)) return;
+      const float m1 = s_m[r], l1 = s_m[kRows + r], top = fmaxf(m_ref, m1);
+      float f0 = m_ref == -INFINITY ? 0.f : ptx::ex2(m_ref - top);
+      float f1 = m1 == -INFINITY ? 0.f : ptx::ex2(m1 - top);
+      l = l * f0 + l1 * f1;
+      m_ref = top;
+      ptx::tc_fence_after();
+      // Scores of NaN against the zeros of hidden blocks (as in chunk_softmax_role)
+      if (__any_sync(0xffffffffu, l != l)) {
+        const int first = first_key(a, w, lane);
+        if (l != l && !tree_sees_block(a, w, x.lim, first)) {
+          m_ref = -INFINITY;
+          l = 0.f;
+        }
+      }
+      const bool none = n == 0 || no_weight(m_ref, l);
+      const RowAt at = row_at(a, w, there ? r : 0);
+      uint16_t* const out = static_cast<uint16_t*>(a.o) + o_offset(a, w.b, w.s, at.i, at.head);
+      if (part == nullptr) {
+        const float inv = none ? 0.f : 1.f / l;
+        f0 *= inv;
+        f1 *= inv;
+        if (there)
+          a.lse[lse_index(a, w.b, w.s, at.i, at.head)] =
+              none ? -INFINITY : (m_ref + log2f(l)) * 0.69314718055994531f;
+      } else if (there) {
+        part[kRows * D + r] = m_ref;
+        part[kRows * D + kRows + r] = l;
+      }
+      const uint32_t tO = tl + L::kColO;
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o0[32], o1[32];
+        ptx::tmem_ld32(tO + 32u * c, o0);
+        ptx::tmem_ld32(tO + D + 32u * c, o1);
+        ptx::tmem_ld_wait(o0);
+        ptx::tmem_ld_wait(o1);
+        float v[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          v[e] = fmaf(__uint_as_float(o1[e]), f1, __uint_as_float(o0[e]) * f0);
+          if (none) v[e] = 0.f;
+        }
+        if (!there) continue;
+        if (part == nullptr) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8)
+            *reinterpret_cast<uint4*>(out + 32 * c + e) =
+                make_uint4(pack2<BF16>(v[e], v[e + 1]), pack2<BF16>(v[e + 2], v[e + 3]),
+                           pack2<BF16>(v[e + 4], v[e + 5]), pack2<BF16>(v[e + 6], v[e + 7]));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) part[(32 * c + e) * kRows + r] = v[e];
+        }
+      }
+      // columns with NaN in a drafted key that the row sees
+      if (*reinterpret_cast<const volatile uint32_t*>(sgen + L::kOffBar + kChunkSlotAnyNan) != 0u &&
+          there) {
+        const unsigned long long* nan =
+            reinterpret_cast<const unsigned long long*>(sgen + L::kOffNan) + (w.item & 7) * D;
+#pragma unroll 1
+        for (int c = 0; c < D; ++c) {
+          if (static_cast<int>(nan[c] >> 32) != w.item + 1 ||
+              !tree_nan(a, w.b, w.hk, w.s, x.lim, c))
+            continue;
+          if (part == nullptr) out[c] = 0x7FFFu;
+          else part[c * kRows + r] = __int_as_float(0x7FFFFFFF);
+        }
+      }
+    }
+    k.flags ^= (n > 0 ? 1u : 0u) | 4u;
+    count += static_cast<uint32_t>(n);
+    const bool more = w.next(a), queries = more && w.n() > 0;
+    if (wg == 1) {
+      // (the item's last scores are there, so its queries are not needed any more)
+      if (queries) {
+        fac = tree_queries<D, BF16, PARTS>(a, w, r, sbase + L::kOffQ, 0, D / 16);
+        s_factor[r] = fac;
+        ptx::fence_proxy_async_smem();
+        ptx::mbar_arrive(bar(kCbQFull));
+        ptx::mbar_arrive(bar(kCbQFull + 1));
+      }
+      // O1 and the stats are free for the next item only when they have been read
+      if (!wait_bounded_warp(bar(kCbMerged), (flags >> 2) & 1u, ab, kStatusEpilogue)) return;
+      ptx::tc_fence_after();
+    } else {
+      // (before the other warpgroup may go on, and so before it writes the factors again)
+      if (queries) {
+        if (!wait_bounded_warp(bar(kCbQFull + 1), k.flags & 1u, ab, kStatusSoftmax)) return;
+        fac = s_factor[r];
+      }
+      ptx::tc_fence_before();
+      ptx::mbar_arrive(bar(kCbMerged));
+    }
+    if (!more) return;
+    shelve(shelf, k, lane);
+  }
+}
+
 template <int D, bool BF16, int PARTS, bool TREE>
 __global__ void __launch_bounds__(kChunkThreads, 1)
     fa_cache_chunk_kernel(const __grid_constant__ CUtensorMap tm_k,
                           const __grid_constant__ CUtensorMap tm_v, const CacheAttnArgs a) {
   using L = ChunkLayout<D, PARTS>;
+  constexpr int ROWS = TREE ? (PARTS > 0 ? kChunkRows / 2 : kChunkRows) : 0;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = ptx::smem_u32(smem_raw);
   const uint32_t sbase = (raw + 1023u) & ~1023u;
@@ -1176,34 +1424,25 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   auto bar = [&](int i) { return bars + 8u * static_cast<uint32_t>(i); };
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
+  {
+    // a barrier for each thread
+    constexpr int kStages = kCbKVFull + 2 * L::kStages, kRawSlots = kStages + 2 * L::kRaw;
+    constexpr int kBars = kRawSlots + 2 * L::kDirect;
+    const int i = tid;
+    if (i < kBars) {
+      uint32_t n = 1;
+      if ((i >> 1) == kCbQFull / 2 || (i >> 1) == kCbPFull / 2 || (i >> 1) == kCbStats / 2) n = 128;
+      else if (i == kCbPSplit || i == kCbPSplit + 1) n = 256;
+      else if ((i >= kCbVDone && i < kCbKVFull + L::kStages) || (i >= kStages + L::kRaw && i < kRawSlots))
+        n = 4;
+      ptx::mbar_init(bar(i), n);
+      ptx::fence_mbar_init();
+    }
+    static_assert(kCbMerged == kCbStats + 1 && kCbVDone + 8 == kCbKVFull, "the counts above");
+  }
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(bar(kCbQFull + i), 128);
-      ptx::mbar_init(bar(kCbSFull + i), 1);
-      ptx::mbar_init(bar(kCbPFull + i), 128);
-      ptx::mbar_init(bar(kCbOFull + i), 1);
-    }
-    ptx::mbar_init(bar(kCbStats), 128);
-    ptx::mbar_init(bar(kCbMerged), 128);
-    ptx::mbar_init(bar(kCbDrain), 1);
-    ptx::mbar_init(bar(kCbPSplit), 256);
-    ptx::mbar_init(bar(kCbPSplit + 1), 256);
-    ptx::mbar_init(bar(kCbOStep), 1);
-    for (int i = 0; i < 16; ++i) ptx::mbar_init(bar(kCbScaleFull + i), 1);
-    for (int i = 0; i < 8; ++i) ptx::mbar_init(bar(kCbVDone + i), 4);
-    for (int i = 0; i < L::kStages; ++i) {
-      ptx::mbar_init(bar(kCbKVFull + i), 4);
-      ptx::mbar_init(bar(kCbKVFull + L::kStages + i), 1);
-    }
-    for (int i = 0; i < L::kRaw; ++i) {
-      ptx::mbar_init(bar(kCbKVFull + 2 * L::kStages + i), 1);
-      ptx::mbar_init(bar(kCbKVFull + 2 * L::kStages + L::kRaw + i), 4);
-    }
-    for (int i = 0; i < 2 * L::kDirect; ++i)
-      ptx::mbar_init(bar(kCbKVFull + 2 * L::kStages + 2 * L::kRaw + i), 1);
     *abort_flag = 0u;
     *reinterpret_cast<uint32_t*>(sgen + L::kOffBar + kChunkSlotAnyNan) = 0u;
-    ptx::fence_mbar_init();
     a.join[blockIdx.x] = JoinItem{0, 0, 0, 0};
   }
   for (int i = tid; i < 8 * D; i += kChunkThreads)
@@ -1214,7 +1453,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   const int run = (a.B + kChunkThreads - 1) / kChunkThreads;
   const int b0 = min(tid * run, a.B), b1 = min(b0 + run, a.B);
   long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += a.Hkv * chunk_head_tiles<TREE>(a, seq_rows(a, b));
+  for (int b = b0; b < b1; ++b) mine += a.Hkv * chunk_head_tiles<ROWS>(a, seq_rows(a, b));
   long long upto = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -1229,8 +1468,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     if (k < warp) upto += s_scan[k];
     total += s_scan[k];
   }
-  const long long share = max((total + gridDim.x - 1) / gridDim.x,
-                              static_cast<long long>(kChunkMinShare));
+  const long long share =
+      max(quotient(total + gridDim.x - 1, gridDim.x), static_cast<long long>(kChunkMinShare));
   const long long u0 = share * blockIdx.x, u1 = min(u0 + share, total);
   if (u0 >= u1) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1243,15 +1482,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     SeqRows s;
     for (;; ++b) {
       s = seq_rows(a, b);
-      head_tiles = chunk_head_tiles<TREE>(a, s);
+      head_tiles = chunk_head_tiles<ROWS>(a, s);
       if (u < at + a.Hkv * head_tiles) break;
       at += a.Hkv * head_tiles;
     }
-    const int hk = static_cast<int>((u - at) / head_tiles);
+    const int hk = static_cast<int>(quotient(u - at, head_tiles));
     long long rest = u - at - hk * head_tiles;
     int rb = 0, n;
     for (;; ++rb) {
-      n = max(1, chunk_real_tiles(a, s, rb)) + (TREE ? kTreeLead : 0);
+      n = max(1, chunk_real_tiles<ROWS>(a, s, rb)) + (TREE ? kTreeLead : 0);
       if (rest < n) break;
       rest -= n;
     }
@@ -1288,7 +1527,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  ChunkWalk<TREE> w;
+  ChunkWalk<ROWS> w;
   // (trees: a share whose ends were moved to one place has no tiles)
   const long long len = TREE ? u1 + s_moved[1] - u0 - s_moved[0] : u1 - u0;
   if (len > 0) w.start(a, s_start[0], s_start[1], s_start[2], s_start[3], len);
@@ -1297,15 +1536,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   if (TREE && len <= 0) {
   } else if (wgrp == 0) {
     ptx::setmaxnreg_dec<kChunkRegsMma>();
-    if (warp == 0) chunk_mma_role<D, PARTS, TREE>(a, w, sbase, bars, tmem, ab);
-    else if (warp == 1) chunk_copy_role<D, PARTS, TREE>(&tm_k, &tm_v, a, w, sgen, sbase, bars, ab, lane);
+    if (warp == 0) chunk_mma_role<D, PARTS, ROWS>(a, w, sbase, bars, tmem, ab);
+    else if (warp == 1) chunk_copy_role<D, PARTS, ROWS>(&tm_k, &tm_v, a, w, sgen, sbase, bars, ab, lane);
   } else if (wgrp < 3) {
     ptx::setmaxnreg_inc<kChunkRegsSoftmax>();
-    chunk_softmax_role<D, BF16, PARTS, TREE>(a, w, static_cast<int>(share), sgen, sbase, bars, tmem, ab,
-                                             warp, lane);
+    if constexpr (TREE && PARTS > 0)
+      tree_softmax_role<D, BF16, PARTS>(a, w, static_cast<int>(share), sgen, sbase, bars, tmem, ab, warp,
+                                        lane);
+    else
+      chunk_softmax_role<D, BF16, PARTS, ROWS>(a, w, static_cast<int>(share), sgen, sbase, bars, tmem, ab,
+                                               warp, lane);
   } else {
     ptx::setmaxnreg_dec<kChunkRegsConvert>();
-    chunk_convert_role<D, PARTS, TREE>(a, w, sgen, sbase, bars, ab, warp, lane);
+    chunk_convert_role<D, PARTS, ROWS>(a, w, sgen, sbase, bars, ab, warp, lane);
   }
   __syncwarp();
   ptx::tc_fence_before();
