@@ -61,7 +61,7 @@ constexpr int kChunkMinShare = 2;  // tiles
 // Trees: tiles' time that an item takes beside its own (Q, the first scores, the last
 // products, the epilogue), which counts in the list, and the fewest tiles for which
 // an item is cut.
-constexpr int kTreeLead = 12, kTreePiece = 4;
+constexpr int kTreeLead = 8, kTreePiece = 2;
 // Registers a thread after setmaxnreg (sum 512 = 4 x 128): MMA and copy
 // warpgroup, each softmax warpgroup, converters.
 constexpr uint32_t kChunkRegsMma = 64, kChunkRegsSoftmax = 184, kChunkRegsConvert = 80;
