@@ -17,12 +17,18 @@ namespace {
 // written is no later token's source, and the rows move in order, kRows at a
 // time (all read before any is written), with no copy in between. Blocks are done
 // one after another, each with its own new scale.
+//
+// A chain of loads (lengths and words - table - scales - rows), so what counts is how
+// many warps are in it. Half of up to 96 tokens of 256 requests, 32 heads, d 128, 97 MB:
+// 22.8 us (4.3 TB/s); with 32 rows of a warp under way, 8 warps to a CTA and 3 CTAs 29.7,
+// 16 rows, 5 CTAs of 8 warps 23.6, 64 rows 40. A path of 16 requests, 4 heads: 3.6 us.
 
-constexpr int kKeepWarps = 8;
+constexpr int kKeepWarps = 4;
 constexpr int kKeepThreads = 32 * kKeepWarps;
+constexpr int kKeepCtas = 10;  // on an SM
 constexpr int kMostKept = 64 * kMaxWords;
 constexpr int kMostBlocks = kMostKept / 16 + 1;  // that the kept tokens lie in
-constexpr int kRows = 32;                        // rows of a warp under way together
+constexpr int kRows = 16;                        // rows of a warp under way together
 
 struct PageArgs {
   uint8_t* k;
@@ -43,7 +49,7 @@ struct PageArgs {
 __device__ __forceinline__ float counted(float s) { return s > 0.f ? pow2_above(s) : 0.f; }
 
 template <int D>
-__global__ void __launch_bounds__(kKeepThreads) fa_cache_keep_kernel(const PageArgs a, const int groups) {
+__global__ void __launch_bounds__(kKeepThreads, kKeepCtas) fa_cache_keep_kernel(const PageArgs a, const int groups) {
   constexpr int kLanes = D / 16;            // of a row, 16 codes each
   constexpr int kPerLoad = 32 / kLanes;     // rows
   constexpr int kLoads = kRows / kPerLoad;
@@ -154,15 +160,19 @@ __global__ void __launch_bounds__(kKeepThreads) fa_cache_keep_kernel(const PageA
 
 // ------------------------------------------------------------ release
 //
-// One CTA. Entries are numbered through all requests, a thread takes
-// kEntries of them at a time. With counts of holders three passes: every entry
+// Entries are numbered through all requests; a cluster of CTAs takes equal ranges of
+// them, a thread kEntries at a time. With counts of holders three passes: every entry
 // lowers its block's count; entries of a block that nobody holds any more leave the
 // smallest of their numbers in its place; that one entry puts the block on the
-// list, at its rank among them (a scan over the threads), and clears the count.
-// So the list does not depend on which request came first in time.
+// list, at its rank among them (a scan over the threads, and over the CTAs through
+// their shared memory), and clears the count. So the list does not depend on which
+// request came first in time. Up to 4096 entries are the first CTA's alone. Latency:
+// the blocks behind the kept tokens of 256 requests 5.9 us, with counts 8.1; 32768
+// entries 9.4 and 24.6 (one CTA for any number: 40 and 152), 524288 127 and 354.
 
 constexpr int kReleaseThreads = 1024;
 constexpr int kEntries = 4;
+constexpr int kReleaseCtas = 8;
 
 struct ReleaseArgs {
   const int32_t* table;
@@ -215,13 +225,28 @@ __device__ __forceinline__ Scan block_scan(int v, int* s_warp) {
   return {in - v + (warp > 0 ? s_warp[warp - 1] : 0), s_warp[(blockDim.x >> 5) - 1]};
 }
 
-__global__ void __launch_bounds__(kReleaseThreads) fa_cache_release_kernel(const ReleaseArgs a) {
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile(
+      "barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// An int of another CTA of the cluster, at the address that it has in this one.
+__device__ __forceinline__ int of_cta(const int* own, int cta) {
+  uint32_t at;
+  int v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(ptx::smem_u32(own)), "r"(cta));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+
+__global__ void __cluster_dims__(kReleaseCtas, 1, 1) __launch_bounds__(kReleaseThreads)
+    fa_cache_release_kernel(const ReleaseArgs a) {
   __shared__ int s_first[kReleaseThreads];  // number of the first entry of each thread's requests
   __shared__ int s_warp[32];
-  const int tid = static_cast<int>(threadIdx.x);
+  __shared__ int s_count;  // blocks that this CTA puts on the list
+  const int tid = static_cast<int>(threadIdx.x), cta = static_cast<int>(blockIdx.x);
   const int pos = __ldg(a.free_pos);
   if (pos < 0 || pos > a.n_free) {
-    if (tid == 0) *a.free_next = pos;
+    if (cta == 0 && tid == 0) *a.free_next = pos;
     return;
   }
   const int run = (a.B + kReleaseThreads - 1) / kReleaseThreads;
@@ -230,8 +255,18 @@ __global__ void __launch_bounds__(kReleaseThreads) fa_cache_release_kernel(const
   for (int b = b0; b < b1; ++b) mine += given(a, b).count;
   const Scan s = block_scan(mine, s_warp);
   s_first[tid] = s.before;
-  const int total = s.total;
+  const int total = s.total, step = kReleaseThreads * kEntries;
+  const bool alone = total <= step;  // (all CTAs see the same)
+  if (alone && cta != 0) return;
   __syncthreads();
+  // this CTA's entries [from, to)
+  const int per = alone ? step : (total + kReleaseCtas * kEntries - 1) / (kReleaseCtas * kEntries) * kEntries;
+  const int from = min(cta * per, total), to = min(from + per, total);
+  auto sync = [&] {
+    __threadfence();
+    if (alone) __syncthreads();
+    else cluster_sync();
+  };
 
   // the block of entry e, -1 for one that does not exist
   auto block_of_entry = [&](int e) {
@@ -251,16 +286,25 @@ __global__ void __launch_bounds__(kReleaseThreads) fa_cache_release_kernel(const
       at += g.count;
     }
   };
-  // passes over the entries, kEntries of neighbouring numbers to a thread
-  const int step = kReleaseThreads * kEntries;
-  auto ids_at = [&](int e0, int (&id)[kEntries]) {
+  auto look_up = [&](int e0, int (&id)[kEntries]) {
 #pragma unroll
-    for (int i = 0; i < kEntries; ++i) id[i] = e0 + i < total ? block_of_entry(e0 + i) : -1;
+    for (int i = 0; i < kEntries; ++i) id[i] = e0 + i < to ? block_of_entry(e0 + i) : -1;
+  };
+  // (those of the first round are looked up once for all passes)
+  int first_ids[kEntries];
+  look_up(from + tid * kEntries, first_ids);
+  auto ids_at = [&](int e0, int (&id)[kEntries]) {
+    if (e0 >= from + step) {
+      look_up(e0, id);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kEntries; ++i) id[i] = first_ids[i];
+    }
   };
   const bool counted_blocks = a.shares != nullptr;
   if (counted_blocks) {
     for (int pass = 0; pass < 2; ++pass) {
-      for (int e0 = tid * kEntries; e0 < total; e0 += step) {
+      for (int e0 = from + tid * kEntries; e0 < to; e0 += step) {
         int id[kEntries], held[kEntries];
         ids_at(e0, id);
         if (pass == 0) {
@@ -275,20 +319,37 @@ __global__ void __launch_bounds__(kReleaseThreads) fa_cache_release_kernel(const
             if (held[i] < 0) atomicMin(a.shares + id[i], INT32_MIN + e0 + i);
         }
       }
-      __threadfence();
-      __syncthreads();
+      sync();
     }
   }
-  int rank = 0;  // blocks on the list so far
-  for (int at = 0; at < total; at += step) {
-    const int e0 = at + tid * kEntries;
-    int id[kEntries], n = 0;
+  // entries that put their block on the list
+  auto winners = [&](int e0, int (&id)[kEntries]) {
+    int n = 0;
     ids_at(e0, id);
 #pragma unroll
     for (int i = 0; i < kEntries; ++i) {
       if (counted_blocks && id[i] >= 0 && __ldcg(a.shares + id[i]) != INT32_MIN + e0 + i) id[i] = -1;
       n += id[i] >= 0;
     }
+    return n;
+  };
+  int rank = 0, listed = 0;  // blocks of the CTAs before this one, of all
+  if (!alone) {
+    int id[kEntries], n = 0;
+    for (int e0 = from + tid * kEntries; e0 < to; e0 += step) n += winners(e0, id);
+    const Scan all = block_scan(n, s_warp);
+    if (tid == 0) s_count = all.total;
+    cluster_sync();
+    for (int c = 0; c < kReleaseCtas; ++c) {
+      const int other = of_cta(&s_count, c);
+      rank += c < cta ? other : 0;
+      listed += other;
+    }
+    cluster_sync();  // (no CTA clears a count, or ends, before all have seen them)
+  }
+  for (int at = from; at < to; at += step) {
+    int id[kEntries];
+    const int n = winners(at + tid * kEntries, id);
     const Scan all = block_scan(n, s_warp);
     int place = pos - 1 - rank - all.before;
 #pragma unroll
@@ -300,7 +361,7 @@ __global__ void __launch_bounds__(kReleaseThreads) fa_cache_release_kernel(const
     }
     rank += all.total;
   }
-  if (tid == 0) *a.free_next = max(pos - rank, 0);
+  if (cta == 0 && tid == 0) *a.free_next = max(pos - (alone ? rank : listed), 0);
 }
 
 // ------------------------------------------------------------ fork
@@ -523,7 +584,7 @@ fa_status fa_cache_release(const int32_t* block_table, int table_width, const in
   a.B = B;
   a.block_shift = shift;
   (void)cudaGetLastError();
-  fa::fa_cache_release_kernel<<<1, fa::kReleaseThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+  fa::fa_cache_release_kernel<<<fa::kReleaseCtas, fa::kReleaseThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
   return fa::launched();
 }
 

@@ -18,15 +18,20 @@
 #include "fa_cache.cuh"
 #include "fa_check.h"
 #include "fa_rope.h"
+#include "ptx.cuh"
 
 namespace fa {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kFwdBatch = 4;  // rows of a lane group under way together
-constexpr int kFwdCtas = 4;   // on an SM
-constexpr int kBwdBatch = 4;
-constexpr int kBwdCtas = 2;
+// Threads of a CTA, rows of a lane group under way together, CTAs on an SM. What
+// counts is the rows under way on an SM, for which the registers have to suffice. Us,
+// prompt of 16384 tokens, 32 + 8 heads, d 128 / B4 H16 N4096 d 128 / B2 H32 N8191 d 64.
+// Forward, 128 threads, 4 rows, 8 CTAs 56.5 / 43.8 / 27.0; 256, 4, 4: 58.0 / 44.9 / 28.0;
+// 256, 8, 3: 61.7 / 48.4 / 29.3; 256, 4, 5, whose registers spill, 76.6 / 62.7 / 42.1.
+// Backward (- / B4 / B2), 256, 4, 2: 76.0 / 48.3; 128, 4, 4: 76.0 / 49.4; 256, 2, 3: 95.4 /
+// 60.4; the next rows requested while these are worked on, 256, 2, 2: 80.0 / 52.3.
+constexpr int kFwdThreads = 128, kFwdBatch = 4, kFwdCtas = 8;
+constexpr int kBwdThreads = 256, kBwdBatch = 4, kBwdCtas = 2;
 
 struct RowsOf {  // q or k: its heads, and element strides of each operand
   const uint16_t* x;
@@ -81,20 +86,18 @@ __device__ __forceinline__ uint32_t narrow(float lo, float hi) {
 struct Eight {
   uint2 lo, hi;
 };
+using Eight32 = float2[4];
 template <bool BF16>
-__device__ __forceinline__ void widen8(const Eight& e, float (&f)[8]) {
-  const uint32_t w[4] = {e.lo.x, e.lo.y, e.hi.x, e.hi.y};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 v = widen<BF16>(w[i]);
-    f[2 * i] = v.x;
-    f[2 * i + 1] = v.y;
-  }
+__device__ __forceinline__ void widen8(const Eight& e, Eight32& f) {
+  f[0] = widen<BF16>(e.lo.x);
+  f[1] = widen<BF16>(e.lo.y);
+  f[2] = widen<BF16>(e.hi.x);
+  f[3] = widen<BF16>(e.hi.y);
 }
 template <bool BF16>
-__device__ __forceinline__ Eight narrow8(const float (&f)[8]) {
-  return {make_uint2(narrow<BF16>(f[0], f[1]), narrow<BF16>(f[2], f[3])),
-          make_uint2(narrow<BF16>(f[4], f[5]), narrow<BF16>(f[6], f[7]))};
+__device__ __forceinline__ Eight narrow8(const Eight32& f) {
+  return {make_uint2(narrow<BF16>(f[0].x, f[0].y), narrow<BF16>(f[1].x, f[1].y)),
+          make_uint2(narrow<BF16>(f[2].x, f[2].y), narrow<BF16>(f[3].x, f[3].y))};
 }
 
 // Where a lane's two fours lie in a row.
@@ -124,31 +127,55 @@ __device__ __forceinline__ Turn turn_of(const RopeArgs& a, const Place& w, int b
   }
   return t;
 }
-// Turns the four pairs of f by the angles (kBack: by their opposites).
+// The rotation of eight elements as factors of each one (own) and of the one that it
+// is paired with (other), two at a time. kBack: by the opposite angles.
+struct Factors {
+  Eight32 own, other;
+};
 template <bool INTERLEAVED, bool kBack>
-__device__ __forceinline__ void rotate(float (&f)[8], const Turn& t) {
-  const float c[4] = {t.c.x, t.c.y, t.c.z, t.c.w}, s[4] = {t.s.x, t.s.y, t.s.z, t.s.w};
+__device__ __forceinline__ Factors factors_of(const Turn& t) {
+  Factors f;
+  const float sign = kBack ? -1.f : 1.f;
+  const float c[4] = {t.c.x, t.c.y, t.c.z, t.c.w};
+  const float s[4] = {sign * t.s.x, sign * t.s.y, sign * t.s.z, sign * t.s.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int x = INTERLEAVED ? 2 * i : i, y = INTERLEAVED ? 2 * i + 1 : i + 4;
-    const float u = f[x], v = f[y], sn = kBack ? -s[i] : s[i];
-    f[x] = u * c[i] - v * sn;
-    f[y] = v * c[i] + u * sn;
+    if constexpr (INTERLEAVED) {
+      f.own[i] = make_float2(c[i], c[i]);
+      f.other[i] = make_float2(-s[i], s[i]);
+    } else {
+      const int j = 2 * (i & 1);
+      f.own[i] = make_float2(c[j], c[j + 1]);
+      f.other[i] = i < 2 ? make_float2(-s[j], -s[j + 1]) : make_float2(s[j], s[j + 1]);
+    }
   }
+  return f;
+}
+template <bool INTERLEAVED>
+__device__ __forceinline__ float2 partner(const Eight32& f, int i) {
+  return INTERLEAVED ? make_float2(f[i].y, f[i].x) : f[i ^ 2];
+}
+template <bool INTERLEAVED>
+__device__ __forceinline__ void rotate(const Eight32& f, const Factors& k, Eight32& out) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    out[i] = ptx::ffma2(partner<INTERLEAVED>(f, i), k.other[i], ptx::fmul2(f[i], k.own[i]));
 }
 
 template <bool BF16>
 __device__ __forceinline__ void weights_of(const RopeArgs& a, const void* w, const Place& at,
-                                           float (&f)[8]) {
+                                           Eight32& f) {
   if (w == nullptr) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = 1.f;
+    for (int i = 0; i < 4; ++i) f[i] = make_float2(1.f, 1.f);
   } else if (a.weights_fp32) {
     const float* p = static_cast<const float*>(w);
     const float4 x = __ldg(reinterpret_cast<const float4*>(p + at.lo));
     const float4 y = __ldg(reinterpret_cast<const float4*>(p + at.hi));
-    f[0] = x.x, f[1] = x.y, f[2] = x.z, f[3] = x.w;
-    f[4] = y.x, f[5] = y.y, f[6] = y.z, f[7] = y.w;
+    f[0] = make_float2(x.x, x.y);
+    f[1] = make_float2(x.z, x.w);
+    f[2] = make_float2(y.x, y.y);
+    f[3] = make_float2(y.z, y.w);
   } else {
     const uint16_t* p = static_cast<const uint16_t*>(w);
     widen8<BF16>({__ldg(reinterpret_cast<const uint2*>(p + at.lo)),
@@ -172,6 +199,14 @@ __device__ __forceinline__ float group_sum(float v) {
   for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
+
+__device__ __forceinline__ float dot8(const Eight32& x, const Eight32& y) {
+  float2 s = ptx::fmul2(x[0], y[0]);
+#pragma unroll
+  for (int i = 1; i < 4; ++i) s = ptx::ffma2(x[i], y[i], s);
+  return s.x + s.y;
+}
+__device__ __forceinline__ float squares(const Eight32& x) { return dot8(x, x); }
 
 struct Unit {
   int b, n, h0, h1;  // token, heads h0 .. h1 - 1
@@ -211,12 +246,12 @@ __device__ __forceinline__ void load_rows(const uint16_t* x, const fa_strides& s
 }
 
 template <int D, bool BF16, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads, kFwdCtas) fa_norm_rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kFwdThreads, kFwdCtas) fa_norm_rope_kernel(const RopeArgs a) {
   constexpr int L = D / 8;
   const int lane = static_cast<int>(threadIdx.x) % L;
   const int which = static_cast<int>(blockIdx.x) >= a.ctas[0];
   const long long u = static_cast<long long>(static_cast<int>(blockIdx.x) - (which ? a.ctas[0] : 0)) *
-                          (kThreads / L) + threadIdx.x / L;
+                          (kFwdThreads / L) + threadIdx.x / L;
   // (a group without a unit takes part in the sums)
   const bool there = u < a.units[which];
   const Unit w = unit_of(a, which, there ? u : 0);
@@ -225,40 +260,45 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas) fa_norm_rope_kernel(const 
   Eight x[kFwdBatch];
   // (the rows first: the table waits for the positions)
   load_rows(o.x, o.xs, w, there, w.h0, at, x);
-  const Turn turn = turn_of(a, at, w.b, w.n);
-  float wt[8];
+  Factors k = factors_of<INTERLEAVED, false>(turn_of(a, at, w.b, w.n));
+  Eight32 wt;
   weights_of<BF16>(a, o.weight, at, wt);
+  // the weights go into the rotation's factors, 1 / rms behind it
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    k.own[i] = ptx::fmul2(k.own[i], wt[i]);
+    k.other[i] = ptx::fmul2(k.other[i], partner<INTERLEAVED>(wt, i));
+  }
   for (int h0 = w.h0; h0 < w.h0 + a.per_unit; h0 += kFwdBatch) {  // (as often for all groups)
     if (h0 > w.h0) load_rows(o.x, o.xs, w, there, h0, at, x);
     uint16_t* out = o.out + row_at(o.outs, w, h0);
 #pragma unroll
     for (int i = 0; i < kFwdBatch; ++i, out += o.outs.h) {
-      float f[8];
+      Eight32 f, y;
       widen8<BF16>(x[i], f);
-      float sum = 0.f;
+      const float inv = rsqrtf(fmaf(group_sum<L>(squares(f)), 1.f / D, a.eps));
+      rotate<INTERLEAVED>(f, k, y);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sum = fmaf(f[e], f[e], sum);
-      const float inv = rsqrtf(fmaf(group_sum<L>(sum), 1.f / D, a.eps));
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = f[e] * inv * wt[e];
-      rotate<INTERLEAVED, false>(f, turn);
-      if (there && h0 + i < w.h1) store8(out, at, narrow8<BF16>(f));
+      for (int e = 0; e < 4; ++e) y[e] = ptx::fmul2(y[e], make_float2(inv, inv));
+      if (there && h0 + i < w.h1) store8(out, at, narrow8<BF16>(y));
     }
   }
 }
 
 // dx, and each CTA's sum for the weights of q or k.
 template <int D, bool BF16, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads, kBwdCtas) fa_norm_rope_bwd_kernel(const RopeArgs a) {
-  constexpr int L = D / 8, kGroups = kThreads / L;
+__global__ void __launch_bounds__(kBwdThreads, kBwdCtas) fa_norm_rope_bwd_kernel(const RopeArgs a) {
+  constexpr int L = D / 8, kGroups = kBwdThreads / L;
   __shared__ float s_sum[kGroups][D];
   const int lane = static_cast<int>(threadIdx.x) % L, group = static_cast<int>(threadIdx.x) / L;
   const int which = static_cast<int>(blockIdx.x) >= a.ctas[0];
   const int cta = static_cast<int>(blockIdx.x) - (which ? a.ctas[0] : 0);
   const RowsOf& o = a.of[which];
   const Place at = place_of<D>(a, lane);
-  float wt[8], dw[8] = {};
+  Eight32 wt, dw;
   weights_of<BF16>(a, o.weight, at, wt);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) dw[e] = make_float2(0.f, 0.f);
   const long long step_units = static_cast<long long>(a.ctas[which]) * kGroups;
   for (long long u0 = static_cast<long long>(cta) * kGroups; u0 < a.units[which]; u0 += step_units) {
     const long long u = u0 + group;
@@ -267,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) fa_norm_rope_bwd_kernel(co
     Eight x[kBwdBatch], dy[kBwdBatch];
     load_rows(o.x, o.xs, w, there, w.h0, at, x);
     load_rows(o.dy, o.dys, w, there, w.h0, at, dy);
-    const Turn turn = turn_of(a, at, w.b, w.n);
+    const Factors k = factors_of<INTERLEAVED, true>(turn_of(a, at, w.b, w.n));
     for (int h0 = w.h0; h0 < w.h0 + a.per_unit; h0 += kBwdBatch) {
       if (h0 > w.h0) {
         load_rows(o.x, o.xs, w, there, h0, at, x);
@@ -276,25 +316,21 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) fa_norm_rope_bwd_kernel(co
       uint16_t* out = o.out + row_at(o.outs, w, h0);
 #pragma unroll
       for (int i = 0; i < kBwdBatch; ++i, out += o.outs.h) {
-        float f[8], t[8];
+        Eight32 f, t, u;
         widen8<BF16>(x[i], f);
-        widen8<BF16>(dy[i], t);
-        rotate<INTERLEAVED, true>(t, turn);
-        float sum = 0.f, dot = 0.f;
+        widen8<BF16>(dy[i], u);
+        rotate<INTERLEAVED>(u, k, t);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          sum = fmaf(f[e], f[e], sum);
-          dot = fmaf(t[e] * wt[e], f[e], dot);
-        }
-        sum = group_sum<L>(sum);
-        dot = group_sum<L>(dot);
+        for (int e = 0; e < 4; ++e) u[e] = ptx::fmul2(t[e], wt[e]);
+        const float sum = group_sum<L>(squares(f)), dot = group_sum<L>(dot8(u, f));
         const float inv = rsqrtf(fmaf(sum, 1.f / D, a.eps));
         const float mean = dot * inv * (1.f / D);
+        const float2 inv2 = make_float2(inv, inv), mean2 = make_float2(-mean, -mean);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float n = f[e] * inv;
-          dw[e] = fmaf(t[e], n, dw[e]);
-          f[e] = inv * fmaf(-n, mean, t[e] * wt[e]);
+        for (int e = 0; e < 4; ++e) {
+          const float2 n = ptx::fmul2(f[e], inv2);
+          dw[e] = ptx::ffma2(t[e], n, dw[e]);
+          f[e] = ptx::fmul2(ptx::ffma2(n, mean2, u[e]), inv2);
         }
         if (there && h0 + i < w.h1) store8(out, at, narrow8<BF16>(f));
       }
@@ -303,9 +339,10 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) fa_norm_rope_bwd_kernel(co
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (a.partial == nullptr) return;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) s_sum[group][(e < 4 ? at.lo + e : at.hi + e - 4)] = dw[e];
+  for (int e = 0; e < 4; ++e)
+    *reinterpret_cast<float2*>(&s_sum[group][(e < 2 ? at.lo : at.hi) + 2 * (e & 1)]) = dw[e];
   __syncthreads();
-  for (int c = static_cast<int>(threadIdx.x); c < D; c += kThreads) {
+  for (int c = static_cast<int>(threadIdx.x); c < D; c += kBwdThreads) {
     float v = 0.f;
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) v += s_sum[g][c];
@@ -401,17 +438,17 @@ void split(RopeArgs& a, int most, long long groups) {
 
 template <int D, bool BF16>
 cudaError_t launch_forward(RopeArgs a, cudaStream_t s) {
-  constexpr int kGroups = kThreads / (D / 8);
+  constexpr int kGroups = kFwdThreads / (D / 8);
   for (int i = 0; i < 2; ++i) a.ctas[i] = static_cast<int>((a.units[i] + kGroups - 1) / kGroups);
   const unsigned grid = static_cast<unsigned>(a.ctas[0]) + static_cast<unsigned>(a.ctas[1]);
-  if (a.interleaved) fa_norm_rope_kernel<D, BF16, true><<<grid, kThreads, 0, s>>>(a);
-  else fa_norm_rope_kernel<D, BF16, false><<<grid, kThreads, 0, s>>>(a);
+  if (a.interleaved) fa_norm_rope_kernel<D, BF16, true><<<grid, kFwdThreads, 0, s>>>(a);
+  else fa_norm_rope_kernel<D, BF16, false><<<grid, kFwdThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 
 template <int D, bool BF16>
 cudaError_t launch_backward(RopeArgs a, int most, float* dqw, float* dkw, cudaStream_t s) {
-  constexpr int kGroups = kThreads / (D / 8);
+  constexpr int kGroups = kBwdThreads / (D / 8);
   // CTAs that run at once, shared out by the units of q and k
   const long long want[2] = {(a.units[0] + kGroups - 1) / kGroups, (a.units[1] + kGroups - 1) / kGroups};
   const long long share = (most * a.units[1] + (a.units[0] + a.units[1]) / 2) / (a.units[0] + a.units[1]);
@@ -419,8 +456,8 @@ cudaError_t launch_backward(RopeArgs a, int most, float* dqw, float* dkw, cudaSt
   a.ctas[1] = static_cast<int>(want[1] < k ? want[1] : k);
   a.ctas[0] = static_cast<int>(want[0] < most - k ? want[0] : most - k);
   const unsigned grid = static_cast<unsigned>(a.ctas[0] + a.ctas[1]);
-  if (a.interleaved) fa_norm_rope_bwd_kernel<D, BF16, true><<<grid, kThreads, 0, s>>>(a);
-  else fa_norm_rope_bwd_kernel<D, BF16, false><<<grid, kThreads, 0, s>>>(a);
+  if (a.interleaved) fa_norm_rope_bwd_kernel<D, BF16, true><<<grid, kBwdThreads, 0, s>>>(a);
+  else fa_norm_rope_bwd_kernel<D, BF16, false><<<grid, kBwdThreads, 0, s>>>(a);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || a.partial == nullptr) return e;
   cudaLaunchConfig_t cfg{};

@@ -80,7 +80,7 @@ fa_status fa_cache_keep(const fa_cache* cache, const int32_t* block_table, int t
  * free_next   : [1] int32, written: free_pos of the next call.
  * Written arrays must differ from each other and from read ones. Pointers 4-byte aligned;
  * 1 <= B <= 2^20, table_width >= 1, B * table_width <= 2^30, n_free >= 0.
- * Deterministic; one launch, of one CTA: some 4000 entries at a time.
+ * Deterministic; one launch.
  */
 fa_status fa_cache_release(const int32_t* block_table, int table_width, const int32_t* lens,
                            const int32_t* new_lens, int32_t* shares, int num_blocks,

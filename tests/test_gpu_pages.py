@@ -168,7 +168,7 @@ def check_release(table, lens, new, free, pos, bs, shares=None):
 
 @pytest.mark.parametrize("counted", [False, True])
 @pytest.mark.parametrize("B,top,bs", [(1, 0, 16), (1, 100, 16), (1, 20000, 16), (3, 700, 128), (37, 300, 32),
-                                      (700, 90, 16), (3000, 40, 16)])
+                                      (700, 90, 16), (3000, 40, 16), (40, 9000, 16), (5000, 300, 16)])
 def test_release(B, top, bs, counted):
     rng = np.random.default_rng(B + top)
     lens = rng.integers(0, top + 1, B).tolist()
@@ -189,6 +189,17 @@ def test_release_of_shared_blocks():
     for extra in (-1, 0, 1, 3):
         check_release(table, lens, new, list(range(100, 160)), 50, 16,
                       np.maximum(holders - 1 + extra, 0).tolist())
+
+
+def test_release_of_shared_blocks_by_many():
+    """More entries than one CTA takes at a time, from blocks of few."""
+    rng = np.random.default_rng(28)
+    table = rng.integers(-2, 3000, (400, 30))
+    lens, new = rng.integers(0, 481, 400).tolist(), [0] * 400
+    held = np.bincount([x for b in range(400) for x in table[b, :-(-lens[b] // 16)] if x >= 0], minlength=3000)
+    shares = np.maximum(held - 1 + rng.integers(-1, 2, 3000), 0)
+    check_release(table, lens, new, [-7] * 3100, 3050, 16, shares.tolist())
+    check_release(table, lens, new, [-7] * 3100, 17, 16, shares.tolist())
 
 
 @pytest.mark.parametrize("case", [
