@@ -25,8 +25,11 @@ PyObject* cache_tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
   at::Tensor masks, positions;
   if (a[4] == Py_None) {
     if (words < 1) return status(FA_ERR_INVALID_ARG);
-    masks = empty({T, words}, at::kLong, dev);
-    positions = empty({T}, at::kInt, dev);
+    // one allocation for both, the positions behind the masks
+    const int64_t n_masks = int64_t{T} * words;
+    const at::Tensor all = empty({n_masks + (int64_t{T} + 1) / 2}, at::kLong, dev);
+    masks = part(all, 0, {T, words}, at::kLong);
+    positions = part(all, 2 * n_masks, {T}, at::kInt);
   } else {
     if (!PyTuple_Check(a[4]) || PyTuple_GET_SIZE(a[4]) != 2)
       refuse(PyExc_TypeError, "out is (masks, positions)");

@@ -118,10 +118,15 @@ PyObject* cache_fork(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   CallStream cs(a[8], dev);
   at::Tensor rows, lens, copies, next;
   if (a[7] == Py_None) {
-    rows = empty({n, width}, at::kInt, dev);
-    lens = empty({n}, at::kInt, dev);
-    copies = empty({n, 3}, at::kInt, dev);
-    next = empty({1}, at::kInt, dev);
+    // one allocation for all four, each from a multiple of 16 bytes on
+    auto up = [](int64_t x) { return (x + 3) & ~int64_t{3}; };
+    const int64_t at_lens = up(int64_t{n} * width), at_copies = at_lens + up(n);
+    const int64_t at_next = at_copies + up(int64_t{3} * n);
+    const at::Tensor all = empty({at_next + 1}, at::kInt, dev);
+    rows = part(all, 0, {n, width}, at::kInt);
+    lens = part(all, at_lens, n);
+    copies = part(all, at_copies, {n, 3}, at::kInt);
+    next = part(all, at_next, 1);
   } else {
     if (!PyTuple_Check(a[7]) || PyTuple_GET_SIZE(a[7]) != 4)
       refuse(PyExc_TypeError, "out is (new_table, new_lens, copies, free_next)");

@@ -108,13 +108,18 @@ at::Tensor empty(at::IntArrayRef shape, at::ScalarType type, int dev) {
       shape, type, c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(dev)), std::nullopt));
 }
 
-// Elements from .. from + n - 1 of `whole`, a tensor of one axis, on its memory.
-at::Tensor part(const at::Tensor& whole, int64_t from, int64_t n) {
+// A contiguous tensor of `shape` on the memory of `whole`, from element `from` on (of
+// `type`, where that is another one than the whole's).
+at::Tensor part(const at::Tensor& whole, int64_t from, at::IntArrayRef shape,
+                at::ScalarType type) {
   auto t = c10::make_intrusive<at::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(),
-                                               whole.dtype());
+                                               c10::scalarTypeToTypeMeta(type));
   t->set_storage_offset(from);
-  t->set_sizes_contiguous({n});
+  t->set_sizes_contiguous(shape);
   return at::Tensor(std::move(t));
+}
+at::Tensor part(const at::Tensor& whole, int64_t from, int64_t n) {
+  return part(whole, from, {n}, whole.scalar_type());
 }
 
 PyObject* status(fa_status s) { return PyLong_FromLong(static_cast<long>(s)); }

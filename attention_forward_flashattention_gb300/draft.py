@@ -53,8 +53,8 @@ def cache_tree(parents, cu, lens, words: int = 1, stream=None):
     the numbers of their parents among their request's tokens (-1: the context), cu
     [B + 1] the requests' rows (cache_plan's cu_new) and lens [B] the lengths of their
     contexts (before the drafted tokens), all int32. Rows that belong to no request
-    are not written."""
-    r = cache._module().cache_tree(parents, cu, lens, words, None, stream)
+    are not written. The two are parts of one allocation."""
+    r = (cache._native or cache._module()).cache_tree(parents, cu, lens, words, None, stream)
     if type(r) is int:
         raise FaError(r, "fa_cache_tree")
     return r

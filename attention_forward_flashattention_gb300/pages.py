@@ -99,7 +99,8 @@ def cache_fork(block_table, lens, src, free_blocks, free_pos, shares, block: int
     """(new_table [n, width], new_lens [n], copies [n, 3], free_next [1]), int32, of
     requests that start as copies of requests src [n]: full blocks are shared (their
     counts in shares [num_blocks] go up, in place), a last one that is not full gets a
-    free block in its place, which cache_copy fills. `out`: those four, to be written."""
+    free block in its place, which cache_copy fills. `out`: those four, to be written
+    (otherwise they are parts of one allocation)."""
     return _result(cache._module().cache_fork(block_table, lens, src, free_blocks, free_pos, shares, block,
                                               out, stream), "fa_cache_fork")
 

@@ -103,8 +103,8 @@ def qk_norm_rope_forward(q, k, rope, positions, q_weight=None, k_weight=None, ep
     """(q, k) normalised and rotated, as new contiguous tensors. rope: float32
     [positions, rotary_dim] (rope_table); positions: int32, taken as within the
     table; weights: [d] tensors, both float32 or both of q's dtype, None for ones."""
-    r = cache._module().qk_norm_rope(q, k, rope, positions, q_weight, k_weight, eps, interleaved, None,
-                                     stream)
+    r = (cache._native or cache._module()).qk_norm_rope(q, k, rope, positions, q_weight, k_weight, eps,
+                                                        interleaved, None, stream)
     if type(r) is int:
         raise FaError(r, "fa_qk_norm_rope")
     return r
@@ -149,6 +149,7 @@ def _function():
                 return qk_norm_rope_forward(q, k, rope, positions, q_weight, k_weight, eps, interleaved)
 
             @staticmethod
+            @torch.autograd.function.once_differentiable
             def backward(ctx, dq, dk):
                 q, k, rope, positions, qw, kw = ctx.saved_tensors
                 # (a gradient may be a broadcast one, of strides that rows cannot have)
@@ -163,6 +164,6 @@ def _function():
 
 def qk_norm_rope(q, k, rope, positions, q_weight=None, k_weight=None, eps: float = 1e-6,
                  interleaved: bool = False):
-    """qk_norm_rope_forward, differentiable in q, k and the weights: autograd runs
+    """qk_norm_rope_forward, differentiable (once) in q, k and the weights: autograd runs
     fa_qk_norm_rope_bwd on the saved inputs."""
     return _function().apply(q, k, rope, positions, q_weight, k_weight, float(eps), bool(interleaved))

@@ -60,6 +60,12 @@ fa_status fa_cache_tree(const int32_t* parents, const int32_t* cu, const int32_t
  *         tree: any set is allowed, the token's own bit is like any other.
  * words : 1 .. 16; T * words <= 2^31 - 1.
  * workspace : of fa_fwd_cache_workspace_size bytes, as there.
+ *
+ * Roundings are fa_fwd_cache's, but for which sequences are taken for large: a call
+ * with cu_q and more than 16 rows to a K / V head on average computes all of its
+ * sequences as those of more rows, and with d = 128 these are the ones whose small query
+ * elements may be rounded (by 2^-17 of their row's largest), however many rows
+ * there are. Launches: one kernel for such a call, and one that joins; otherwise as there.
  */
 fa_status fa_fwd_cache_tree(const void* q, const fa_cache* cache, const int32_t* block_table,
                             int table_width, const int32_t* kv_lens, const int32_t* cu_q,
