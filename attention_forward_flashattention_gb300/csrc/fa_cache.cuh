@@ -176,8 +176,9 @@ __device__ __forceinline__ int block_of(const CacheAttnArgs& a, int b, int key) 
 __device__ __forceinline__ bool tree_nan(const CacheAttnArgs& a, int b, int hk, const SeqRows& s,
                                          int row, int col) {
   const int behind = s.kv_len - s.count;
+  const int end = min(s.kv_len, behind + min(s.count, 64 * a.words));  // of those with bits
 #pragma unroll 1
-  for (int key = max(behind, 0); key < s.kv_len; ++key) {
+  for (int key = max(behind, 0); key < end; ++key) {
     if (!tree_sees(a, s, row, key)) continue;
     const int id = block_of(a, b, key);
     if (id < 0) continue;

@@ -749,7 +749,10 @@ __device__ __forceinline__ int first_key(const CacheAttnArgs& a, const ChunkWalk
 template <int ROWS>
 __device__ __forceinline__ bool tree_sees_block(const CacheAttnArgs& a, const ChunkWalk<ROWS>& w,
                                                 int row, int first) {
-  const long long end = min(static_cast<long long>(w.s.kv_len), 1LL * w.real_end * kChunkKeys);
+  // (a key of the context ends the search at once; of the drafted ones those with bits count)
+  const long long end = min(
+      static_cast<long long>(w.s.kv_len) - w.s.count + min(w.s.count, 64 * a.words),
+      1LL * w.real_end * kChunkKeys);
 #pragma unroll 1
   for (int key = first; key < end; ++key) {
     if (!tree_sees(a, w.s, row, key)) continue;

@@ -1,7 +1,7 @@
 """Upkeep of the block cache (``include/fa_pages.h``): dropping drafted tokens that
 were not accepted, handing blocks back, sharing them between requests.
 
-    # after the drafts have been judged: `keep` is the mask of the last accepted token
+    # after the drafts have been verified: `keep` is the mask of the last accepted token
     kv_lens_after = fa.cache_keep(cache, table, kv_lens, cu, keep)            # each layer's cache
     pos = fa.cache_release(table, kv_lens, kv_lens_after, free, pos, block)   # once
 

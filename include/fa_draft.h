@@ -36,7 +36,7 @@ extern "C" {
  *             clamped to 0 .. T).
  * lens      : [B] int32, tokens of each request's context (below 0: taken as 0).
  * masks     : [T][words] uint64, written: itself and its ancestors. Tokens from
- *             64 * words on have no bit.
+ *             64 * words on have no bit, and no ancestors: their masks are empty.
  * positions : [T] int32, written: lens plus the number of its ancestors.
  * Rows that belong to no request are left as they are.
  * Pointers 4-byte (masks 8-byte) aligned; 1 <= B <= 2^20, T >= 0 (0: nothing is

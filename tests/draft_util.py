@@ -16,9 +16,10 @@ def masks_of(parents, cu, lens, words):
         sets = []
         for i in range(max(hi - lo, 0)):
             p = parents[lo + i]
-            sets.append((sets[p] if 0 <= p < i else set()) | {i})
+            # (a token without a bit has no ancestors either)
+            sets.append(((sets[p] if 0 <= p < i else set()) | {i}) if i < 64 * words else set())
             masks[lo + i] = [sum(1 << c % 64 for c in sets[i] if c // 64 == w) for w in range(words)]
-            positions[lo + i] = max(lens[b], 0) + len(sets[i]) - 1
+            positions[lo + i] = max(lens[b], 0) + max(len(sets[i]) - 1, 0)
     return masks, positions
 
 

@@ -224,6 +224,23 @@ def test_masks_with_too_few_words():
     Batch(12, [100, 64, 3], [50, 0, 20], 4, 4, 64, 16, torch.bfloat16, "any", words=1).check()
 
 
+@pytest.mark.parametrize("group", [1, 4, 12])
+def test_few_tokens_of_many_sequences(group):
+    """No more tokens than sequences: taken for single tokens, and right if they are not."""
+    counts = [0, 0, 5, 0, 1, 0, 0, 0, 2, 0]
+    Batch(31 + group, counts, [9, 0, 130, 70, 0, 33, 1, 0, 257, 2], 2 * group, 2, 64, 16, torch.float16).check()
+
+
+def test_nothing_but_spare_rows():
+    b = Batch(33, [0, 0], [5, 40], 4, 2, 128, 16, torch.bfloat16, spare=40, words=1)
+    o = torch.full_like(b.q, 7.0)
+    lse = torch.full(b.q.shape[:2], 7.0, device=DEV)
+    ws = torch.empty(fa.fa_fwd_cache_workspace_size(2, 40, 4, 2, 128), dtype=torch.uint8, device=DEV)
+    fa.attention_forward_cache_tree_into(b.q, b.cache(), ints(b.table), ints(b.kv), longs([[0]] * 40), o, lse, ws,
+                                         ints([0, 0, 0]))
+    assert bool((o == 7).all()) and bool((lse == 7).all())
+
+
 def test_sixteen_words():
     Batch(13, [1024], [100], 1, 1, 64, 128, torch.bfloat16, "any", words=16).check()
 

@@ -227,7 +227,7 @@ def check_fork(table, lens, src, free, pos, shares, bs):
 
 
 @pytest.mark.parametrize("B,n,top,bs", [(1, 1, 0, 16), (1, 5, 100, 16), (4, 32, 3000, 128), (20, 700, 50, 32),
-                                        (300, 2000, 64, 16)])
+                                        (300, 2000, 64, 16), (2, 611, 900, 16), (900, 9001, 40, 16)])
 def test_fork(B, n, top, bs):
     rng = np.random.default_rng(n)
     lens = rng.integers(0, top + 1, B).tolist()
