@@ -60,6 +60,11 @@ AttnPlan plan_attn(int B, int T, int group, bool ragged, bool tree = false) {
   return p;
 }
 
+// Rounds of tiles up to which a sequence of a tree batch is not cut: us with 1 / 3 / 6,
+// 5 tokens behind 250 keys, 2 heads, d 64: 9.4 / 8.3 / 8.2, 64 x 2 tokens behind 500 keys, 32
+// heads on 8: 20.9 / 19.7 / 19.7, the same behind 1000 keys, 6 rounds: 25.1 / 25.0 / 27.4.
+constexpr int kTreeRounds = 3;
+
 int step_grid(const AttnPlan& p, int sm_count) { return p.nt == 0 ? 0 : step_ctas(p.nt) * sm_count; }
 
 // Workspace: the join items of both launches, then their partial results.
@@ -129,9 +134,9 @@ cudaError_t launch_all(CacheAttnArgs a, const fa_cache& c, const AttnPlan& p, in
   sides.ctas[1] = cgrid;
   if (p.nt != 0) {
     // sequences of at most one round of tiles (one for each warp) are not cut:
-    // nothing to join
+    // nothing to join. (Trees: of up to kTreeRounds.)
     const bool whole = (static_cast<long long>(a.table_width) << a.block_shift) <=
-                       kStepWarps * step_keys(D);
+                       (TREE ? kTreeRounds : 1) * kStepWarps * step_keys(D);
     sides.ctas[0] = whole ? 0 : sgrid;
     a.rows_over = 0;
     a.rows_upto = p.upto;

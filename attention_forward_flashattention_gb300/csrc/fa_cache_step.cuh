@@ -552,6 +552,21 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas(NT))
         }
       }
 
+      // trees: which of the tile's keys the rows see
+      [[maybe_unused]] unsigned long long see[NT][2];
+      if constexpr (TREE) {
+        static_assert(KT <= 64, "a word of bits");
+        if (edge) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              see[nt][h] = lim[nt][h] < 0
+                               ? 0ull
+                               : tree_seen64(a, now.s.kv_len, behind, lim[nt][h], key0);
+        }
+      }
+
       // e = S (c ks) + log2 vs, its largest per row
       float iv[kSub];
       float top[NT][2];
@@ -574,9 +589,10 @@ __global__ void __launch_bounds__(kStepThreads, step_ctas(NT))
             const int ka = key0 + 16 * u + g;
             const bool no = ((hidden >> box) & 1u) != 0u;
             if constexpr (TREE) {
+              const int at = 16 * u + g;
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                if (no || !tree_sees(a, now.s, lim[nt][e & 1], ka + 4 * (e & 2)))
+                if (no || ((see[nt][e & 1] >> (at + 4 * (e & 2))) & 1ull) == 0ull)
                   s[u][nt][e] = -INFINITY;
             } else {
               if (no || ka >= lim[nt][0]) s[u][nt][0] = -INFINITY;
