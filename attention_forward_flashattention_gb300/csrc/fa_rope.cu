@@ -211,22 +211,24 @@ __device__ __forceinline__ float squares(const Eight32& x) { return dot8(x, x); 
 struct Unit {
   int b, n, h0, h1;  // token, heads h0 .. h1 - 1
 };
-__device__ __forceinline__ Unit unit_of(const RopeArgs& a, int which, long long u) {
-  const int chunks = a.chunks[which];
-  long long token;
-  int chunk;
+// (B * N * (H + Hkv), and so everything here, is below 2^31: divisions of 64 bits would take
+// as long as a row's work)
+__device__ __forceinline__ Unit unit_of(const RopeArgs& a, int which, uint32_t u) {
+  uint32_t token, chunk;
   if (a.heads_inner) {
+    const uint32_t chunks = static_cast<uint32_t>(a.chunks[which]);
     token = u / chunks;
-    chunk = static_cast<int>(u - token * chunks);
+    chunk = u - token * chunks;
   } else {
-    const long long tokens = static_cast<long long>(a.B) * a.N;
-    chunk = static_cast<int>(u / tokens);
+    const uint32_t tokens = static_cast<uint32_t>(a.B) * static_cast<uint32_t>(a.N);
+    chunk = u / tokens;
     token = u - chunk * tokens;
   }
+  const uint32_t b = token / static_cast<uint32_t>(a.N);
   Unit r;
-  r.b = static_cast<int>(token / a.N);
-  r.n = static_cast<int>(token - static_cast<long long>(r.b) * a.N);
-  r.h0 = chunk * a.per_unit;
+  r.b = static_cast<int>(b);
+  r.n = static_cast<int>(token - b * static_cast<uint32_t>(a.N));
+  r.h0 = static_cast<int>(chunk) * a.per_unit;
   r.h1 = min(r.h0 + a.per_unit, a.of[which].heads);
   return r;
 }
@@ -254,7 +256,7 @@ __global__ void __launch_bounds__(kFwdThreads, kFwdCtas) fa_norm_rope_kernel(con
                           (kFwdThreads / L) + threadIdx.x / L;
   // (a group without a unit takes part in the sums)
   const bool there = u < a.units[which];
-  const Unit w = unit_of(a, which, there ? u : 0);
+  const Unit w = unit_of(a, which, there ? static_cast<uint32_t>(u) : 0u);
   const RowsOf& o = a.of[which];
   const Place at = place_of<D>(a, lane);
   Eight x[kFwdBatch];
@@ -303,7 +305,7 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdCtas) fa_norm_rope_bwd_kernel
   for (long long u0 = static_cast<long long>(cta) * kGroups; u0 < a.units[which]; u0 += step_units) {
     const long long u = u0 + group;
     const bool there = u < a.units[which];
-    const Unit w = unit_of(a, which, there ? u : 0);
+    const Unit w = unit_of(a, which, there ? static_cast<uint32_t>(u) : 0u);
     Eight x[kBwdBatch], dy[kBwdBatch];
     load_rows(o.x, o.xs, w, there, w.h0, at, x);
     load_rows(o.dy, o.dys, w, there, w.h0, at, dy);
