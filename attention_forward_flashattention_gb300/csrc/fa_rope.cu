@@ -26,7 +26,8 @@ namespace {
 // Threads of a CTA, rows of a lane group under way together, CTAs on an SM. What
 // counts is the rows under way on an SM, for which the registers have to suffice. Us,
 // prompt of 16384 tokens, 32 + 8 heads, d 128 / B4 H16 N4096 d 128 / B2 H32 N8191 d 64.
-// Forward, 128 threads, 4 rows, 8 CTAs 56.5 / 43.8 / 27.0; 256, 4, 4: 58.0 / 44.9 / 28.0;
+// Forward, 128 threads, 4 rows, 8 CTAs 56.2 / 43.2 / 26.8 (6.0 / 6.2 / 5.6 TB/s, 87 % of a
+// copy's rate for the prompt); 256, 4, 4: 58.0 / 44.9 / 28.0;
 // 256, 8, 3: 61.7 / 48.4 / 29.3; 256, 4, 5, whose registers spill, 76.6 / 62.7 / 42.1.
 // Backward (- / B4 / B2), 256, 4, 2: 76.0 / 48.3; 128, 4, 4: 76.0 / 49.4; 256, 2, 3: 95.4 /
 // 60.4; the next rows requested while these are worked on, 256, 2, 2: 80.0 / 52.3.

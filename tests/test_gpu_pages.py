@@ -373,6 +373,42 @@ def test_binding_refuses():
             fa.cache_copy(cache, bad)
 
 
+# ------------------------------------------------------------ far blocks
+
+def test_blocks_behind_four_gigabytes():
+    """Codes whose distance from the cache's start does not fit into 32 bits: attention over
+    them, tokens kept in them, blocks copied there, as in a small cache."""
+    rng = np.random.default_rng(14)
+    bs, heads, d, num = 64, 8, 128, 70000
+    counts, base = [20, 70], [100, 64]
+    kv = [x + n for x, n in zip(base, counts)]
+    table, _ = random_table(rng, kv, bs, 8, 4)
+    small = make_cache(8, heads, bs, d, "head", rng)
+    far = fa.Cache(*(torch.empty(num, heads, bs, d, dtype=torch.uint8, device=DEV) for _ in range(2)),
+                   *(torch.ones(num, heads, device=DEV) for _ in range(2)))
+    assert (num - 8) * heads * bs * d > 2 ** 32
+    for a, b in zip(far, small):
+        a[num - 8:] = b
+    words = random_words(rng, 90, 2)
+    masks, q = torch.from_numpy(D.signed(words)).to(DEV), torch.randn(90, 16, d, device=DEV).half()
+    cu, ftab = ints([0, 20, 90]), np.where(table >= 0, table + num - 8, table)
+    for n, rows in ((1, slice(18, 22)), (90, slice(0, 90))):   # the kernels for few rows and for many
+        c = cu if n > 1 else ints([0, 2, 4])
+        got, want = (fa.attention_forward_cache_tree(q[rows], x, ints(t), ints(kv), masks[rows].contiguous(), c)
+                     for x, t in ((far, ftab), (small, table)))
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    keep = masks[:2].contiguous()
+    after = [fa.cache_keep(x, ints(t), ints(kv), cu, keep) for x, t in ((far, ftab), (small, table))]
+    assert torch.equal(*after)
+    fa.cache_copy(far, ints([(num - 8, num - 9, 33), (num - 7, 5, 64)]))
+    for a, b in zip(far, small):
+        assert torch.equal(a[num - 8:], b)
+    for a, b in zip(far[:2], small[:2]):
+        assert torch.equal(a[num - 9, :, :33], b[0, :, :33]) and torch.equal(a[5], b[1])
+    for a, b in zip(far[2:], small[2:]):
+        assert torch.equal(a[num - 9], b[0]) and torch.equal(a[5], b[1])
+
+
 # ------------------------------------------------------------ together
 
 @pytest.mark.parametrize("bs,d,H,Hkv,dt", [(16, 64, 4, 2, torch.float16), (32, 128, 8, 1, torch.bfloat16)])

@@ -195,6 +195,23 @@ def test_output_views_and_what_lies_around_them():
     assert bool((room == 7.0).all())
 
 
+def test_rows_behind_four_gigabytes():
+    """Distances between rows that do not fit into 32 bits, of inputs and of outputs."""
+    g = torch.Generator().manual_seed(16)
+    room = torch.empty(2 ** 31 + 2 ** 20, dtype=torch.bfloat16, device=DEV)
+    far = [room[i * 2048:].as_strided((3, h, 128), (2 ** 30, 128, 1)) for i, h in enumerate((4, 2, 4, 2))]
+    near = [torch.randn(3, h, 128, generator=g).to(DEV, torch.bfloat16) for h in (4, 2)]
+    for a, b in zip(far, near):
+        a.copy_(b)
+    table, pos = fa.rope_table(9, 128, device=DEV), torch.tensor([2, 8, 0], dtype=torch.int32, device=DEV)
+    want = fa.qk_norm_rope_forward(*near, table, pos)
+    fa.qk_norm_rope_forward_into(far[0], far[1], far[2], far[3], table, pos)
+    assert torch.equal(far[2], want[0]) and torch.equal(far[3], want[1])
+    dwant = fa.qk_norm_rope_backward(*want, *near, table, pos)
+    got = fa.qk_norm_rope_backward(far[2], far[3], far[0], far[1], table, pos)
+    assert torch.equal(got[0], dwant[0]) and torch.equal(got[1], dwant[1])
+
+
 def test_no_tokens():
     q, k = (torch.zeros(2, h, 0, 64, dtype=torch.float16, device=DEV) for h in (4, 2))
     table, pos = fa.rope_table(3, 64, device=DEV), torch.zeros(0, dtype=torch.int32, device=DEV)
