@@ -190,8 +190,10 @@ def test_attention_without_offsets(n, group, d):
 
 
 @pytest.mark.parametrize("group", [1, 3, 6, 16, 20])
-def test_attention_groups(group):
-    Batch(group, [3, 11], [77, 140], 2 * group, 2, 64, 16, torch.float16, "any").check()
+@pytest.mark.parametrize("d", [64, 128])
+def test_attention_groups(group, d):
+    Batch(group, [3, 11], [77, 140], 2 * group, 2, d, 16, torch.float16, "any").check()
+    Batch(group, [1, 1, 1], [77, 0, 140], group, 1, d, 16, torch.bfloat16, "any", uniform=True).check()
 
 
 @pytest.mark.parametrize("counts", [[3, 2], [30, 50], [140, 90]])
