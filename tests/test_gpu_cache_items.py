@@ -1,12 +1,14 @@
 """Many items to a CTA of the kernel for many rows: sequences without keys between
 others, and trees of many sizes whose shares hold several items and cut some of them,
-element by element against the 64-bit implementation; NaN in drafted keys."""
+element by element against the 64-bit implementation; NaN in drafted keys; chains
+by their masks and by the causal rule."""
 import numpy as np
 import pytest
 import torch
 
 import attention_forward_flashattention_gb300 as fa
-from test_gpu_draft import Batch, ints, longs
+import draft_util as D
+from test_gpu_draft import Batch, ints, longs, offsets
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -114,3 +116,19 @@ def test_nan_in_many_items_of_a_cta(d):
     o, lse = b.call(cache)
     assert torch.equal(torch.isnan(o), want)
     assert torch.equal(torch.where(want, 0, o), torch.where(want, 0, clean[0])) and torch.equal(lse, clean[1])
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("counts", [[1, 4, 2], [3, 30, 17], [200, 60], [9] * 40])
+def test_chains_and_the_causal_attention_within_bounds(counts, dt, d):
+    """The masks of chains and the causal rule, each element by element: the two calls may
+    take other kernels and cuts, so they agree within their bounds."""
+    ctx = [(97 * i) % 400 for i in range(len(counts))]
+    b = Batch(17, counts, ctx, 4, 2, d, 32, dt)
+    b.masks, _ = D.masks_of([i - 1 for n in counts for i in range(n)], offsets(counts), ctx, b.words)
+    b.check()
+    o, lse = fa.attention_forward_cache(b.q, b.cache(), ints(b.table), ints(b.kv), ints(b.cu), causal=True,
+                                        scale=b.scale)
+    O, L, to, tl = b.reference()
+    assert (np.abs(o.double().cpu().numpy() - O) <= to).all()
+    assert (np.abs(lse.double().cpu().numpy() - L) <= tl).all()
