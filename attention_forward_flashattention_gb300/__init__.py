@@ -258,6 +258,15 @@ def _allocating_on(stream):
     return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
 
 
+def _wrote(*tensors) -> None:
+    """Notes that a call has written to tensors of the caller's: autograd then refuses the
+    backward pass of an operation that saved what they held before."""
+    import torch
+    for t in tensors:
+        if not t.is_inference():
+            torch.autograd.graph.increment_version(t)
+
+
 def _stream_handle(stream) -> int:
     import torch
     if stream is None:
@@ -291,6 +300,7 @@ def attention_forward_into(q, k, v, o, lse, causal: bool = False, scale: float |
         what = "fa_fwd_strided"
     if rc != FA_OK:
         raise FaError(rc, what)
+    _wrote(o, lse)
 
 
 def attention_forward_pair_into(q, k, v, o, lse, causal: bool = False,
@@ -309,6 +319,7 @@ def attention_forward_pair_into(q, k, v, o, lse, causal: bool = False,
                      B, H, N, d, causal, scale, _dtype_code(q), _stream_handle(stream))
     if rc != FA_OK:
         raise FaError(rc, "fa_fwd_pair")
+    _wrote(o, lse)
 
 
 def attention_forward(q, k, v, causal: bool = False, scale: float | None = None, stream=None):
@@ -346,6 +357,7 @@ def attention_forward_host_into(q, k, v, o, lse, workspace, causal: bool = False
                          _stream_handle(stream))
     if rc != FA_OK:
         raise FaError(rc, "fa_fwd_host")
+    _wrote(o, lse)
 
 
 def attention_forward_host(q, k, v, causal: bool = False, scale: float | None = None,
@@ -394,6 +406,7 @@ def attention_forward_fp8_into(q8, k8, vt8, o, lse, q_scale: float, k_scales, v_
             _stream_handle(stream))
     if rc != FA_OK:
         raise FaError(rc, fn.__name__)
+    _wrote(o, lse)
 
 
 def attention_forward_fp8(q8, k8, vt8, q_scale: float, k_scales, v_scale: float,

@@ -66,7 +66,9 @@ PyObject* cache_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
                      block, cs.stream);
   Py_END_ALLOW_THREADS;
   if (rc != FA_OK) return status(rc);
+  wrote({&table});
   if (a[5] != Py_None) {
+    wrote({&slots, &cu, &kv, &next});
     Py_INCREF(a[5]);
     return a[5];
   }
@@ -106,6 +108,7 @@ PyObject* cache_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   rc = fa_cache_append(k.data_ptr(), v.data_ptr(), st, slots, T, &c, dt, cs.stream);
   Py_END_ALLOW_THREADS;
   if (rc != FA_OK) return status(rc);
+  wrote_cache(a[3]);
   Py_RETURN_NONE;
   END_HANDLE_TH_ERRORS
 }
@@ -210,6 +213,7 @@ PyObject* attention_forward_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
                         cs.stream);
     Py_END_ALLOW_THREADS;
     if (rc != FA_OK) return status(rc);
+    if (a[5] != Py_None) wrote({&o, &lse});
   }
   PyObject* out = PyTuple_New(2);
   if (!out) throw python_error();

@@ -48,6 +48,7 @@ PyObject* cache_tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
                        words, cs.stream);
     Py_END_ALLOW_THREADS;
     if (rc != FA_OK) return status(rc);
+    if (a[4] != Py_None) wrote({&masks, &positions});
   }
   return tuple_of({&masks, &positions});
   END_HANDLE_TH_ERRORS

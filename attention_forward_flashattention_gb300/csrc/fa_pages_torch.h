@@ -52,7 +52,10 @@ PyObject* cache_keep(PyObject*, PyObject* const* a, Py_ssize_t n) {
   rc = fa_cache_keep(&c, p_table, width, p_kv, p_cu, static_cast<const uint64_t*>(keep.data_ptr()), words,
                      p_out, B, cs.stream);
   Py_END_ALLOW_THREADS;
-  return rc == FA_OK ? THPVariable_Wrap(out) : status(rc);
+  if (rc != FA_OK) return status(rc);
+  wrote_cache(a[0]);
+  if (a[5] != Py_None) wrote({&out});
+  return THPVariable_Wrap(out);
   END_HANDLE_TH_ERRORS
 }
 
@@ -89,7 +92,11 @@ PyObject* cache_release(PyObject*, PyObject* const* a, Py_ssize_t n) {
   rc = fa_cache_release(p_table, width, p_lens, p_new, p_shares, num_blocks, p_free, n_free, p_pos, p_next,
                         B, block, cs.stream);
   Py_END_ALLOW_THREADS;
-  return rc == FA_OK ? THPVariable_Wrap(next) : status(rc);
+  if (rc != FA_OK) return status(rc);
+  wrote({&free});
+  if (a[6] != Py_None) wrote({&THPVariable_Unpack(a[6])});
+  if (a[7] != Py_None) wrote({&next});
+  return THPVariable_Wrap(next);
   END_HANDLE_TH_ERRORS
 }
 
@@ -145,6 +152,8 @@ PyObject* cache_fork(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
                      p_rows, p_new, p_copies, p_next, block, cs.stream);
   Py_END_ALLOW_THREADS;
   if (rc != FA_OK) return status(rc);
+  wrote({&shares});
+  if (a[7] != Py_None) wrote({&rows, &lens, &copies, &next});
   return tuple_of({&rows, &lens, &copies, &next});
   END_HANDLE_TH_ERRORS
 }
@@ -166,6 +175,7 @@ PyObject* cache_copy(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   rc = fa_cache_copy(&c, p, n, cs.stream);
   Py_END_ALLOW_THREADS;
   if (rc != FA_OK) return status(rc);
+  wrote_cache(a[0]);
   Py_RETURN_NONE;
   END_HANDLE_TH_ERRORS
 }

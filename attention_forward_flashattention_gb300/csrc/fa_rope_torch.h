@@ -114,6 +114,10 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     ko = tensor(PyTuple_GET_ITEM(a[8], 1), "k_out");
     same_rows(qo, q, "q_out");
     same_rows(ko, k, "k_out");
+    if (c10::GradMode::is_enabled() && (qo.requires_grad() || ko.requires_grad()))
+      refuse(PyExc_ValueError,
+             "q_out and k_out must not require gradients: what is written to them has none (use "
+             "qk_norm_rope, or torch.no_grad)");
   }
   const int B = narrow(vq.B, "too many batches"), N = narrow(vq.N, "too many tokens");
   const int H = narrow(vq.H, "too many heads"), Hkv = narrow(vk.H, "too many heads");
@@ -127,6 +131,7 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
                          st, &r, dt, cs.stream);
     Py_END_ALLOW_THREADS;
     if (rc != FA_OK) return status(rc);
+    if (a[8] != Py_None) wrote({&qo, &ko});
   }
   return tuple_of({&qo, &ko});
   END_HANDLE_TH_ERRORS

@@ -7,6 +7,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
@@ -120,6 +121,16 @@ at::Tensor part(const at::Tensor& whole, int64_t from, at::IntArrayRef shape,
 }
 at::Tensor part(const at::Tensor& whole, int64_t from, int64_t n) {
   return part(whole, from, {n}, whole.scalar_type());
+}
+
+// A call has written to tensors of the caller's: autograd then refuses the backward pass of
+// an operation that saved what they held before, as after torch's own in-place calls.
+void wrote(std::initializer_list<const at::Tensor*> ts) {
+  for (const at::Tensor* t : ts)
+    if (t->defined() && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+}
+void wrote_cache(PyObject* cache) {  // one that describe() has checked
+  for (Py_ssize_t i = 0; i < 4; ++i) wrote({&THPVariable_Unpack(PyTuple_GET_ITEM(cache, i))});
 }
 
 PyObject* status(fa_status s) { return PyLong_FromLong(static_cast<long>(s)); }
