@@ -104,12 +104,11 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.fa_status_string.restype = ctypes.c_char_p
         lib.fa_version.argtypes = []
         lib.fa_version.restype = i
-        if hasattr(lib, "fa_fwd_cache"):
-            from . import cache, draft, pages, rope
-            cache.bind(lib)
-            draft.bind(lib)
-            pages.bind(lib)
-            rope.bind(lib)
+        from . import cache, draft, pages, rope
+        for entry, group in (("fa_fwd_cache", cache), ("fa_fwd_cache_tree", draft),
+                             ("fa_cache_keep", pages), ("fa_qk_norm_rope", rope)):
+            if hasattr(lib, entry):
+                group.bind(lib)
         if path is None:
             _lib = lib
         return lib

@@ -117,3 +117,31 @@ def test_a_unit_that_does_not_compile_is_named(tools):
     with pytest.raises(RuntimeError, match="fa_bwd_d64.cu"):
         fabuild.build()
     assert built() == set()
+
+
+# ------------------------------------------------------------ libraries of fewer entry points
+
+CORE = ("fa_fwd fa_fwd_pair fa_fwd_noalloc fa_check fa_sm_clock_read fa_query_launch fa_sm_clock_probe "
+        "fa_status_string fa_version").split()
+GROUPS = {"cache": ["fa_cache_plan", "fa_cache_append", "fa_fwd_cache", "fa_fwd_cache_workspace_size"],
+          "draft": ["fa_cache_tree", "fa_fwd_cache_tree"],
+          "pages": ["fa_cache_keep", "fa_cache_release", "fa_cache_fork", "fa_cache_copy"],
+          "rope": ["fa_qk_norm_rope", "fa_qk_norm_rope_bwd", "fa_qk_norm_rope_bwd_workspace_size"]}
+
+
+@pytest.mark.parametrize("groups", [[], ["cache"], ["rope"], ["cache", "draft"], ["cache", "pages"], list(GROUPS)])
+def test_a_library_of_fewer_entry_points_loads(groups, tmp_path):
+    """load_library(path) binds the groups of calls that the library has, each by itself."""
+    import subprocess
+
+    import attention_forward_flashattention_gb300 as fa
+    names = CORE + [n for g in groups for n in GROUPS[g]]
+    (tmp_path / "lib.c").write_text("".join(f"int {n}(void) {{ return 7; }}\n" for n in names))
+    path = str(tmp_path / "libfew.so")
+    subprocess.run(["gcc", "-shared", "-fPIC", "-o", path, str(tmp_path / "lib.c")], check=True)
+    lib = fa.load_library(path)
+    for g, calls in GROUPS.items():
+        for n in calls:
+            assert hasattr(lib, n) == (g in groups)
+            if g in groups:
+                assert getattr(lib, n).argtypes
