@@ -266,6 +266,13 @@ def _wrote(*tensors) -> None:
             torch.autograd.graph.increment_version(t)
 
 
+def _gradient(t):
+    """A gradient as the kernels read it: contiguous (one that was broadcast has strides of 0)
+    and from a multiple of 16 bytes on (one that is part of a larger tensor's need not be)."""
+    t = t.contiguous()
+    return t.clone() if t.data_ptr() % 16 else t
+
+
 def _stream_handle(stream) -> int:
     import torch
     if stream is None:
@@ -472,7 +479,7 @@ def _attention_function():
             def backward(ctx, do):
                 q, k, v, o, lse = ctx.saved_tensors
                 dq, dk, dv = attention_backward(*(t.contiguous() for t in (q, k, v, o)), lse,
-                                                do.contiguous(), causal=ctx.causal,
+                                                _gradient(do), causal=ctx.causal,
                                                 scale=ctx.scale)
                 return dq, dk, dv, None, None
 

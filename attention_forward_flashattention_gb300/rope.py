@@ -15,7 +15,7 @@ from __future__ import annotations
 import ctypes
 import os
 
-from . import FA_OK, FaError, FaStrides, _build, cache, load_library
+from . import FA_OK, FaError, FaStrides, _build, _gradient, cache, load_library
 
 HEADER = os.path.join(_build.INCLUDE, "fa_rope.h")
 
@@ -154,8 +154,7 @@ def _function():
             @torch.autograd.function.once_differentiable
             def backward(ctx, dq, dk):
                 q, k, rope, positions, qw, kw = ctx.saved_tensors
-                # (a gradient may be a broadcast one, of strides that rows cannot have)
-                g = qk_norm_rope_backward(dq.contiguous(), dk.contiguous(), q, k, rope, positions, qw, kw,
+                g = qk_norm_rope_backward(_gradient(dq), _gradient(dk), q, k, rope, positions, qw, kw,
                                           ctx.eps, ctx.interleaved)
                 dw = [None if w is None else x.to(w.dtype) for x, w in zip(g[2:], (qw, kw))]
                 return g[0], g[1], None, None, dw[0], dw[1], None, None

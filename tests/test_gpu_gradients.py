@@ -1,0 +1,47 @@
+"""Gradients as autograd hands them over, to the norm and rotation and to the attention:
+parts of larger tensors at any address."""
+import pytest
+import torch
+
+import attention_forward_flashattention_gb300 as fa
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    torch.cuda.init()
+    fa.build.build()
+    fa.load_library()
+
+
+def heads(n=5, h=2):
+    return torch.randn(1, h, n, 64, device=DEV).half().requires_grad_()
+
+
+@pytest.mark.parametrize("odd", [1, 3, 8])
+def test_gradients_that_are_parts_of_a_larger_tensor(odd):
+    """The gradient of torch.cat's result reaches its inputs as views, behind `odd` elements."""
+    x, y, z = heads(), heads(), torch.randn(odd, device=DEV).half().requires_grad_()
+    table, pos = fa.rope_table(5, 64, device=DEV), torch.arange(5, dtype=torch.int32, device=DEV)
+    q, k = fa.qk_norm_rope(x, y, table, pos)
+    all_ = torch.cat([z, q.flatten(), k.flatten()])
+    g = torch.randn_like(all_)
+    all_.backward(g)
+    want = fa.qk_norm_rope_backward(g[odd:odd + q.numel()].clone().view_as(q), g[odd + q.numel():].clone().view_as(k),
+                                    x.detach(), y.detach(), table, pos)
+    assert torch.equal(x.grad, want[0]) and torch.equal(y.grad, want[1])
+
+
+@pytest.mark.parametrize("odd", [1, 3, 8])
+def test_attention_gradient_that_is_a_part_of_a_larger_tensor(odd):
+    q, k, v, z = heads(), heads(), heads(), torch.randn(odd, device=DEV).half().requires_grad_()
+    o = fa.attention(q, k, v)
+    all_ = torch.cat([z, o.flatten()])
+    g = torch.randn_like(all_)
+    all_.backward(g)
+    with torch.no_grad():
+        o, lse = fa.attention_forward(q, k, v)
+        want = fa.attention_backward(q, k, v, o, lse, g[odd:].clone().view_as(o))
+    assert all(torch.equal(a.grad, b) for a, b in zip((q, k, v), want))
