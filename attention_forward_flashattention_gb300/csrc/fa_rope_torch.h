@@ -11,15 +11,16 @@ struct HeadsView {
   int64_t B, H, N, d;
 };
 HeadsView heads_view(const at::Tensor& t, const char* what) {
-  if ((t.dim() != 3 && t.dim() != 4) || t.stride(t.dim() - 1) != 1) {
+  if ((t.dim() != 3 && t.dim() != 4) || (t.numel() > 0 && t.stride(t.dim() - 1) != 1)) {
     PyErr_Format(PyExc_ValueError, "%s must be [B, H, N, d] or [T, H, d] with unit d stride", what);
     throw python_error();
   }
   if (t.dim() == 3) return {1, t.size(1), t.size(0), t.size(2)};
   return {t.size(0), t.size(1), t.size(2), t.size(3)};
 }
-// Its strides; an axis of length one has none of its own.
+// Its strides; an axis of length one has none of its own, a tensor without elements no axis.
 fa_strides heads_strides(const at::Tensor& t, const HeadsView& v) {
+  if (t.numel() == 0) return {v.d, v.d, v.d};
   const bool rows = t.dim() == 3;
   return {v.B > 1 ? t.stride(0) : 8, v.H > 1 ? t.stride(1) : v.d,
           v.N > 1 ? t.stride(rows ? 0 : 2) : v.d};
@@ -34,7 +35,7 @@ void* address(const at::Tensor& t) {
 // Tensors of one call: every one like the first of its pair.
 void same_rows(const at::Tensor& t, const at::Tensor& like, const char* what) {
   if (!(t.sizes() == like.sizes() && t.scalar_type() == like.scalar_type() &&
-        t.stride(t.dim() - 1) == 1 && on(t, like.get_device()))) {
+        (t.numel() == 0 || t.stride(t.dim() - 1) == 1) && on(t, like.get_device()))) {
     PyErr_Format(PyExc_ValueError,
                  "%s must have the shape, dtype and device of its input and unit d stride", what);
     throw python_error();
@@ -162,8 +163,7 @@ PyObject* qk_norm_rope_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int B = narrow(vq.B, "too many batches"), N = narrow(vq.N, "too many tokens");
   const int H = narrow(vq.H, "too many heads"), Hkv = narrow(vk.H, "too many heads");
   const int d = narrow(vq.d, "d too large");
-  if (B == 0 || (N == 0 && (H == 0 || Hkv == 0)))
-    refuse(PyExc_ValueError, "no batches or heads");
+  if (H == 0 || Hkv == 0) refuse(PyExc_ValueError, "no heads");
   size_t bytes = 0;
   if (r.q_weight || r.k_weight) {
     const fa_status s = fa_qk_norm_rope_bwd_workspace_size(d, &bytes);
@@ -177,8 +177,10 @@ PyObject* qk_norm_rope_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   void* const pws = ws.defined() ? ws.data_ptr() : nullptr;
   fa_status rc;
   Py_BEGIN_ALLOW_THREADS;
+  // (no batches: as one without tokens)
   rc = fa_qk_norm_rope_bwd(address(dqo), address(dko), address(q), address(k), address(dq), address(dk),
-                           pqw, pkw, B, H, Hkv, N, d, st, &r, dt, pws, bytes, cs.stream);
+                           pqw, pkw, B > 0 ? B : 1, H, Hkv, B > 0 ? N : 0, d, st, &r, dt, pws, bytes,
+                           cs.stream);
   Py_END_ALLOW_THREADS;
   if (rc != FA_OK) return status(rc);
   return tuple_of({&dq, &dk, &dqw, &dkw});

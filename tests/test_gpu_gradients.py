@@ -1,5 +1,5 @@
 """Gradients as autograd hands them over, to the norm and rotation and to the attention:
-parts of larger tensors at any address."""
+parts of larger tensors at any address, and of batches without tokens."""
 import pytest
 import torch
 
@@ -45,3 +45,23 @@ def test_attention_gradient_that_is_a_part_of_a_larger_tensor(odd):
         o, lse = fa.attention_forward(q, k, v)
         want = fa.attention_backward(q, k, v, o, lse, g[odd:].clone().view_as(o))
     assert all(torch.equal(a.grad, b) for a, b in zip((q, k, v), want))
+
+
+@pytest.mark.parametrize("shape", [(2, 4, 0, 64), (0, 4, 5, 64), (0, 4, 0, 64), (0, 4, 64)])
+@pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16])
+def test_batches_without_tokens(shape, dt):
+    """Empty gradients, and weights whose gradient is 0: from sums, whose gradients are broadcast, too."""
+    kshape = (*shape[:1], 2, *shape[2:])
+    q, k = (torch.zeros(s, device=DEV, dtype=dt, requires_grad=True) for s in (shape, kshape))
+    w = [torch.ones(64, device=DEV, requires_grad=True) for _ in range(2)]
+    table = fa.rope_table(5, 64, device=DEV)
+    pos = torch.zeros(shape[2] if len(shape) == 4 else shape[0], dtype=torch.int32, device=DEV)
+    for broadcast in (False, True):
+        a, b = fa.qk_norm_rope(q, k, table, pos, *w)
+        assert a.shape == q.shape and b.shape == k.shape
+        if broadcast:
+            got = torch.autograd.grad(a.sum() + b.sum(), (q, k, *w))
+        else:
+            got = torch.autograd.grad((a, b), (q, k, *w), (torch.zeros_like(a), torch.zeros_like(b)))
+        assert got[0].shape == q.shape and got[1].shape == k.shape
+        assert all(x.shape == (64,) and bool((x == 0).all()) for x in got[2:])
