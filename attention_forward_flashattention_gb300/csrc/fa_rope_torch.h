@@ -139,10 +139,17 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // (dq_out, dk_out, q, k, table, positions, q_weight, k_weight, eps, interleaved,
-// stream). Returns (dq, dk, dq_weight, dk_weight), None for a weight that is None.
+// stream, of_q_weight, of_k_weight). Returns (dq, dk, dq_weight, dk_weight), None for a
+// weight that is None or whose gradient is not asked for.
 PyObject* qk_norm_rope_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  count_args(n, 11);
+  count_args(n, 13);
+  bool wanted[2];
+  for (int i = 0; i < 2; ++i) {
+    const int truth = PyObject_IsTrue(a[11 + i]);
+    if (truth < 0) throw python_error();
+    wanted[i] = truth != 0;
+  }
   const at::Tensor& dqo = tensor(a[0], "dq_out");
   const at::Tensor& dko = tensor(a[1], "dk_out");
   const at::Tensor& q = tensor(a[2], "q");
@@ -158,14 +165,14 @@ PyObject* qk_norm_rope_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const at::Tensor dq = empty(q.sizes(), q.scalar_type(), dev);
   const at::Tensor dk = empty(k.sizes(), k.scalar_type(), dev);
   at::Tensor dqw, dkw, ws;
-  if (r.q_weight) dqw = empty({vq.d}, at::kFloat, dev);
-  if (r.k_weight) dkw = empty({vq.d}, at::kFloat, dev);
+  if (r.q_weight && wanted[0]) dqw = empty({vq.d}, at::kFloat, dev);
+  if (r.k_weight && wanted[1]) dkw = empty({vq.d}, at::kFloat, dev);
   const int B = narrow(vq.B, "too many batches"), N = narrow(vq.N, "too many tokens");
   const int H = narrow(vq.H, "too many heads"), Hkv = narrow(vk.H, "too many heads");
   const int d = narrow(vq.d, "d too large");
   if (H == 0 || Hkv == 0) refuse(PyExc_ValueError, "no heads");
   size_t bytes = 0;
-  if (r.q_weight || r.k_weight) {
+  if (dqw.defined() || dkw.defined()) {
     const fa_status s = fa_qk_norm_rope_bwd_workspace_size(d, &bytes);
     if (s != FA_OK) return status(s);
     ws = empty({static_cast<int64_t>(bytes)}, at::kByte, dev);

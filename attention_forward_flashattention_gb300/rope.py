@@ -123,12 +123,14 @@ def qk_norm_rope_forward_into(q, k, q_out, k_out, rope, positions, q_weight=None
 
 
 def qk_norm_rope_backward(dq_out, dk_out, q, k, rope, positions, q_weight=None, k_weight=None,
-                          eps: float = 1e-6, interleaved: bool = False, stream=None):
+                          eps: float = 1e-6, interleaved: bool = False, stream=None,
+                          weight_grads=(True, True)):
     """Gradients (dq, dk, dq_weight, dk_weight) at the forward's inputs q and k for
     the gradients dq_out and dk_out of its results: dq and dk contiguous, those of the
-    weights float32 (None for a weight that is None)."""
+    weights float32 (None for a weight that is None, or whose entry in weight_grads is
+    False: without either there is no sum over the rows and no second launch)."""
     r = cache._module().qk_norm_rope_bwd(dq_out, dk_out, q, k, rope, positions, q_weight, k_weight, eps,
-                                         interleaved, stream)
+                                         interleaved, stream, *weight_grads)
     if type(r) is int:
         raise FaError(r, "fa_qk_norm_rope_bwd")
     return r
@@ -155,8 +157,9 @@ def _function():
             def backward(ctx, dq, dk):
                 q, k, rope, positions, qw, kw = ctx.saved_tensors
                 g = qk_norm_rope_backward(_gradient(dq), _gradient(dk), q, k, rope, positions, qw, kw,
-                                          ctx.eps, ctx.interleaved)
-                dw = [None if w is None else x.to(w.dtype) for x, w in zip(g[2:], (qw, kw))]
+                                          ctx.eps, ctx.interleaved,
+                                          weight_grads=ctx.needs_input_grad[4:6])
+                dw = [None if x is None else x.to(w.dtype) for x, w in zip(g[2:], (qw, kw))]
                 return g[0], g[1], None, None, dw[0], dw[1], None, None
 
         _autograd_fn = _QkNormRope

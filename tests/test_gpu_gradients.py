@@ -1,9 +1,11 @@
 """Gradients as autograd hands them over, to the norm and rotation and to the attention:
-parts of larger tensors at any address, and of batches without tokens."""
+parts of larger tensors at any address, of batches without tokens, with weights
+that need none."""
 import pytest
 import torch
 
 import attention_forward_flashattention_gb300 as fa
+from attention_forward_flashattention_gb300 import rope as fr
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -65,3 +67,25 @@ def test_batches_without_tokens(shape, dt):
             got = torch.autograd.grad((a, b), (q, k, *w), (torch.zeros_like(a), torch.zeros_like(b)))
         assert got[0].shape == q.shape and got[1].shape == k.shape
         assert all(x.shape == (64,) and bool((x == 0).all()) for x in got[2:])
+
+
+@pytest.mark.parametrize("of_q,of_k", [(False, False), (True, False), (False, True), (True, True)])
+def test_weights_that_need_no_gradient(of_q, of_k, monkeypatch):
+    """Their sums are not formed, and everything else has the same bits."""
+    x, y = heads(700, 8), heads(700, 4)
+    w = [(1 + 0.1 * torch.randn(64, device=DEV)).requires_grad_(need) for need in (of_q, of_k)]
+    table, pos = fa.rope_table(700, 64, device=DEV), torch.arange(700, dtype=torch.int32, device=DEV)
+    plain = fa.qk_norm_rope_backward
+    made = []
+    monkeypatch.setattr(fr, "qk_norm_rope_backward", lambda *a, **kw: made.append(plain(*a, **kw)) or made[-1])
+    q, k = fa.qk_norm_rope(x, y, table, pos, *w)
+    dq, dk = torch.randn_like(q), torch.randn_like(k)
+    torch.autograd.backward((q, k), (dq, dk))
+    with torch.no_grad():
+        want = plain(dq, dk, x, y, table, pos, *w)
+    assert torch.equal(x.grad, want[0]) and torch.equal(y.grad, want[1])
+    for i, need in enumerate((of_q, of_k)):
+        assert (made[0][2 + i] is not None) == need
+        assert torch.equal(w[i].grad, want[2 + i]) if need else w[i].grad is None
+    none = plain(dq, dk, x.detach(), y.detach(), table, pos, *w, weight_grads=(False, False))
+    assert none[2] is None and none[3] is None and torch.equal(none[0], want[0])
