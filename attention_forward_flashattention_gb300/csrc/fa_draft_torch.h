@@ -1,12 +1,18 @@
 // fa_cache_tree on torch tensors (see fa_cache_torch.cpp).
 #pragma once
 
+#include <algorithm>
+
+#include "fa_check.h"
 #include "fa_draft.h"
 #include "fa_torch.h"
 
 namespace {
 
-// (parents, cu, lens, words, out, stream); out: None, or (masks, positions). Returns those.
+using fa::kMaxWords;
+
+// (parents, cu, lens, words, out, stream); words: or None, as many as one request of all the
+// tokens needs (up to the most there are); out: None, or (masks, positions). Returns those.
 PyObject* cache_tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   count_args(n, 6);
@@ -17,7 +23,8 @@ PyObject* cache_tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
     refuse(PyExc_ValueError, "parents and lens have one axis");
   const int T = narrow(parents.size(0), "too many tokens");
   const int B = narrow(lens.size(0), "too many requests");
-  const int words = narrow(integer(a[3]), "words out of range");
+  const int words = a[3] == Py_None ? std::min(std::max((T - 1) / 64 + 1, 1), kMaxWords)
+                                    : narrow(integer(a[3]), "words out of range");
   const int32_t* p_parents = index(parents, dev, T, -1, "parents");
   const int32_t* p_cu = index(tensor(a[1], "cu"), dev, int64_t{B} + 1, -1, "cu");
   const int32_t* p_lens = index(lens, dev, B, -1, "lens");

@@ -1,6 +1,6 @@
 """Trees of drafted tokens over the block cache (``include/fa_draft.h``).
 
-    masks, positions = fa.cache_tree(parents, cu, lens, words=1)
+    masks, positions = fa.cache_tree(parents, cu, lens)
     o, lse = fa.attention_forward_cache_tree(q, cache, table, kv_lens, masks, cu)
 
 Masks are int64 tensors whose bits are a set of 64 * words drafted tokens. Like
@@ -48,12 +48,15 @@ def fa_fwd_cache_tree(q: int, cache_: cache.FaCache, block_table: int, table_wid
 
 # ------------------------------------------------------------ torch helpers
 
-def cache_tree(parents, cu, lens, words: int = 1, stream=None):
+def cache_tree(parents, cu, lens, words: int | None = None, stream=None):
     """(masks int64 [T, words], positions int32 [T]) of drafted tokens: parents [T] are
     the numbers of their parents among their request's tokens (-1: the context), cu
     [B + 1] the requests' rows (cache_plan's cu_new) and lens [B] the lengths of their
-    contexts (before the drafted tokens), all int32. Rows that belong to no request
-    are not written. The two are parts of one allocation."""
+    contexts (before the drafted tokens), all int32. A request's tokens from 64 * words on
+    are seen by none, themselves neither; by default there are words for T tokens of
+    one request, at most 16 (1024 tokens): a program that knows its requests to be
+    smaller says how many it needs. Rows that belong to no request are not written.
+    The two are parts of one allocation."""
     r = (cache._native or cache._module()).cache_tree(parents, cu, lens, words, None, stream)
     if type(r) is int:
         raise FaError(r, "fa_cache_tree")

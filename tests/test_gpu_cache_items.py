@@ -132,3 +132,16 @@ def test_chains_and_the_causal_attention_within_bounds(counts, dt, d):
     O, L, to, tl = b.reference()
     assert (np.abs(o.double().cpu().numpy() - O) <= to).all()
     assert (np.abs(lse.double().cpu().numpy() - L) <= tl).all()
+
+
+@pytest.mark.parametrize("counts", [[1], [64], [65], [3, 70], [40, 40], [200, 1], [1024], [1500]])
+def test_masks_hold_all_tokens_without_being_told(counts):
+    """cache_tree without a number of words hides no token of up to 1024: each sees itself."""
+    T = sum(counts)
+    parents = [-1 if i == 0 else i // 2 for n in counts for i in range(n)]
+    cu, lens = offsets(counts), [7] * len(counts)
+    masks, pos = fa.cache_tree(ints(parents), ints(cu), ints(lens))
+    words = min(-(-T // 64), 16)
+    want, wpos = D.masks_of(parents, cu, lens, words)
+    assert masks.shape == (T, words)
+    assert torch.equal(masks.cpu(), torch.from_numpy(D.signed(want))) and pos.tolist() == wpos
