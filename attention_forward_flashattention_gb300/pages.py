@@ -9,6 +9,13 @@ were not accepted, handing blocks back, sharing them between requests.
     table, lens, copies, pos = fa.cache_fork(table, lens, src, free, pos, shares, block)   # once
     fa.cache_copy(cache, copies)                                              # each layer's cache
 
+Shared blocks must not be written: drafts are dropped before a fork, and a request that goes back to
+a token inside a block that it may share goes on as a fork of itself, after which its old row ends:
+
+    row, back, copies, pos = fa.cache_fork(table, shorter, src, free, pos, shares, block)
+    fa.cache_copy(cache, copies)                                              # each layer's cache
+    pos = fa.cache_release(table, lens, zeros, free, pos, block, shares)
+
 Like the rest of the binding this only marshals arguments.
 """
 from __future__ import annotations

@@ -11,9 +11,19 @@
  * Blocks that several requests hold are counted in shares [num_blocks]: the
  * number of holders beside the first one. Blocks that fa_cache_plan hands out
  * have one holder, so an array of zeros is where a program starts, and
- * fa_cache_release leaves 0 where it hands a block back. A request only ever
- * writes into its last block and those behind it, and fa_cache_fork does not
- * share a last block that is not full: so a shared block is never written.
+ * fa_cache_release leaves 0 where it hands a block back.
+ *
+ * Tokens are appended to a request's last block, if that is not full, and to those
+ * behind it, and fa_cache_fork does not share a last block that is not full. So a
+ * shared block is not written while requests only grow. A request must not be
+ * shortened to a length inside a block that it shares and then grow again: what it
+ * appends, and a scale that grows, would change the other holders' tokens, and no
+ * call notices. Hence:
+ *   - drafted tokens that are not kept are dropped before a request is forked;
+ *   - a request that goes back to an earlier token of its own goes on as a fork of
+ *     itself: fa_cache_fork with the shorter length (the block that it then ends in is
+ *     copied by fa_cache_copy), then fa_cache_release of its whole old row
+ *     (new_lens 0).
  *
  * Conventions are fa_cache.h's.
  */
@@ -66,6 +76,7 @@ fa_status fa_cache_keep(const fa_cache* cache, const int32_t* block_table, int t
  *               stay in the table as they are.
  * lens, new_lens : [B] int32: tokens held, and kept (0: all blocks go back). A request
  *               without 0 <= new_lens <= lens <= table_width * block gives up nothing.
+ *               (One that keeps a part of a block that it shares must not grow: see above.)
  * shares      : [num_blocks] int32, in and out, or NULL: blocks have one holder. A block
  *               goes to the free list when its last holder gives it up; before that
  *               its count falls. (Given up more often than it has holders, it goes
@@ -90,7 +101,8 @@ fa_status fa_cache_release(const int32_t* block_table, int table_width, const in
 /*
  * fa_cache_fork - requests that go on from other requests' tokens.
  *
- * block_table : [B][table_width] int32 and lens [B] int32, the present requests'.
+ * block_table : [B][table_width] int32 and lens [B] int32, the present requests'. (Lengths
+ *               may be shorter than what requests hold: the new ones start from those.)
  * src         : [n] int32: new request k starts as a copy of request src[k] (any number
  *               of them from the same one).
  * shares      : [num_blocks] int32, in and out: counts of the full blocks that are now

@@ -487,3 +487,60 @@ def test_a_serving_loop(bs, d, H, Hkv, dt):
                     tol = np.abs(want) * 2.0 ** -4 + scales[p][:, None] * 2.0 ** -10 * 8
                     assert (np.abs(got - want) <= tol).all()
     assert fa.fa_check(int(torch.cuda.current_stream().cuda_stream)) == fa.FA_OK
+
+
+@pytest.mark.parametrize("back", [0, 5, 16, 21, 32, 40])
+@pytest.mark.parametrize("d,dt", [(64, torch.float16), (128, torch.bfloat16)])
+def test_a_request_that_goes_back_inside_a_shared_block(d, dt, back):
+    """A request of 40 tokens is forked, goes back to an earlier token as a fork of itself, and
+    grows by larger values than before: the sibling's tokens keep their codes and scales, no
+    block is lost or held twice, and the request has what it kept and what it appended."""
+    rng = np.random.default_rng(back + d)
+    bs, heads, num, width = 16, 2, 20, 8
+    cache = fa.cache_empty(num, heads, bs, d, device=DEV)
+    free, pos, shares = ints(rng.permutation(num)), ints([0]), ints([0] * num)
+    table, lens = ints(np.full((1, width), -1)), ints([0])
+
+    def grow(table, lens, n, size):
+        nonlocal pos
+        slots, cu, kv, pos = fa.cache_plan(lens, ints([n]), table, free, pos, n, bs)
+        k, v = (torch.from_numpy(size * rng.standard_normal((n, heads, d))).to(DEV, dt) for _ in range(2))
+        fa.cache_append(k, v, slots, cache)
+        return kv
+
+    def rows(table, n):
+        """Values of a request's first n tokens."""
+        codes, out = host(cache), []
+        for x, s in ((codes[0], codes[2]), (codes[1], codes[3])):
+            ids, at = table[0].cpu().numpy()[np.arange(n) // bs], np.arange(n) % bs
+            out.append(U.CODE_VALUES[x[ids, :, at]] * s[ids][:, :, None])
+        return out
+
+    def account(*held):
+        """Blocks held and free are all blocks; counts of holders beside the first one."""
+        ids = [int(x) for t, n in held for x in t[0, :-(-n // bs)].tolist()]
+        left = free.tolist()[pos.tolist()[0]:]
+        assert len(left) == len(set(left)) and not set(ids) & set(left) and set(ids) | set(left) == set(range(num))
+        assert shares.tolist() == np.maximum(np.bincount(ids, minlength=num) - 1, 0).tolist()
+
+    lens = grow(table, lens, 40, 1.0)
+    sibling, sib_lens, copies, pos = fa.cache_fork(table, lens, ints([0]), free, pos, shares, bs)
+    fa.cache_copy(cache, copies)
+    account((table, 40), (sibling, 40))
+    before = rows(sibling, 40)
+    own, own_lens, copies, pos = fa.cache_fork(table, ints([back]), ints([0]), free, pos, shares, bs)
+    fa.cache_copy(cache, copies)
+    pos = fa.cache_release(table, lens, ints([0]), free, pos, bs, shares)
+    account((own, back), (sibling, 40))
+    kept = rows(own, back)
+    assert all(np.array_equal(a, b[:back]) for a, b in zip(kept, before))
+    own_lens = grow(own, own_lens, 30, 500.0)
+    assert own_lens.tolist() == [back + 30]
+    account((own, back + 30), (sibling, 40))
+    after = rows(sibling, 40)
+    assert all(np.array_equal(a, b) for a, b in zip(after, before))
+    # the kept tokens, rounded once more where their block's scale grew: half of the smallest code of it
+    for a, b, s in zip(rows(own, back), kept, host(cache)[2:]):
+        if back:
+            scale = s[own[0].cpu().numpy()[np.arange(back) // bs]][:, :, None]
+            assert (np.abs(a - b) <= scale * 2.0 ** -10 + np.abs(b) * 2.0 ** -4).all()
