@@ -406,6 +406,12 @@ fa_status check_shape(int B, int H, int Hkv, int N, int d, fa_dtype dtype, const
   return FA_OK;
 }
 
+// Whether an output that is one of its own side's inputs has its rows where that has them. (An
+// axis of length one has no stride of its own.)
+bool in_place(const void* out, const void* in, const fa_strides& x, const fa_strides& y, int B, int heads, int N) {
+  return out != in || ((B == 1 || x.b == y.b) && (heads == 1 || x.h == y.h) && (N <= 1 || x.n == y.n));
+}
+
 RopeArgs common(const fa_rope& r, int B, int N, int H, int Hkv, const fa_strides& q) {
   RopeArgs a{};
   a.of[0].weight = r.q_weight;
@@ -488,6 +494,10 @@ fa_status fa_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out
     if (!p || !fa::aligned(p, 16)) return FA_ERR_INVALID_ARG;
   const fa_status cs = fa::check_shape(B, H, Hkv, N, d, dtype, strides, 4);
   if (cs == FA_ERR_INVALID_ARG) return cs;
+  if (N > 0 && (q_out == k_out || q_out == k || k_out == q ||
+                !fa::in_place(q_out, q, strides[2], strides[0], B, H, N) ||
+                !fa::in_place(k_out, k, strides[3], strides[1], B, Hkv, N)))
+    return FA_ERR_INVALID_ARG;
   const fa_status cr = fa::check_rope(rope, d);
   if (cr != FA_OK) return cr;
   if (cs != FA_OK) return cs;
@@ -535,6 +545,12 @@ fa_status fa_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void
   if ((sums && !workspace) || (sums && dq_weight == dk_weight)) return FA_ERR_INVALID_ARG;
   const fa_status cs = fa::check_shape(B, H, Hkv, N, d, dtype, strides, 6);
   if (cs == FA_ERR_INVALID_ARG) return cs;
+  if (N > 0 && (dq == dk || dq == dk_out || dk == dq_out || dq == k || dk == q ||
+                !fa::in_place(dq, dq_out, strides[4], strides[0], B, H, N) ||
+                !fa::in_place(dq, q, strides[4], strides[2], B, H, N) ||
+                !fa::in_place(dk, dk_out, strides[5], strides[1], B, Hkv, N) ||
+                !fa::in_place(dk, k, strides[5], strides[3], B, Hkv, N)))
+    return FA_ERR_INVALID_ARG;
   const fa_status cr = fa::check_rope(rope, d);
   if (cr != FA_OK) return cr;
   if (cs != FA_OK) return cs;

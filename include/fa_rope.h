@@ -44,7 +44,9 @@ typedef struct fa_rope {
  *
  * q, k         : [B][H][N][d] and [B][Hkv][N][d] views of `dtype`, read only.
  * q_out, k_out : the same shapes, written. Either may be its input itself, with
- *                the same strides (in place); no other overlap.
+ *                the same strides (in place); no other overlap. (An output at the
+ *                address of another operand, or of its input with other strides, is
+ *                refused.)
  * strides      : host pointer to four fa_strides, of q, k, q_out, k_out, in
  *                elements: positive multiples of 8 below 2^38. A batch of one
  *                token each row is [1][H][T][d].
@@ -67,7 +69,7 @@ fa_status fa_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out
  * dq_out, dk_out       : gradients of q_out and k_out, read only.
  * q, k                 : the forward's inputs, read only.
  * dq, dk               : written; either may be its dq_out or dk_out itself, with
- *                        the same strides; no other overlap.
+ *                        the same strides; no other overlap (refused as above).
  * dq_weight, dk_weight : float32 [d], written; NULL: not wanted.
  * strides              : of dq_out, dk_out, q, k, dq, dk, as above.
  * workspace            : device scratch of fa_qk_norm_rope_bwd_workspace_size bytes,

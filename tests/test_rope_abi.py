@@ -148,3 +148,35 @@ def test_reference_gradient_is_the_differences(pairs):
         e = torch.zeros(16, dtype=torch.float64)
         e[i] = h
         assert abs(((f(x, w + e) - f(x, w - e)) / (2 * h) - dw[i]).item()) < 1e-8
+
+
+# ------------------------------------------------------------ outputs at their inputs' addresses
+
+TOK = (128, 4096, 128 * 64)   # the same memory, other places of the rows
+
+
+@pytest.mark.parametrize("kw", [dict(qo=addr(3)), dict(qo=addr(1)), dict(ko=addr(0)), dict(q=addr(1), qo=addr(1)),
+                                dict(qo=addr(0), st=(ST, ST, TOK, ST)), dict(ko=addr(1), st=(ST, ST, ST, TOK)),
+                                dict(qo=addr(0), st=(ST, ST, (8192, 128, 520), ST))])
+def test_forward_refuses_outputs_over_other_rows(kw):
+    assert fwd_rc(**kw) == fa.FA_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("kw", [dict(dq=addr(5)), dict(dq=addr(1)), dict(dk=addr(0)), dict(dq=addr(3)),
+                                dict(dk=addr(2)), dict(dq=addr(0), st=(ST,) * 4 + (TOK, ST)),
+                                dict(dk=addr(1), st=(ST,) * 5 + (TOK,)), dict(dq=addr(2), st=(ST,) * 4 + (TOK, ST))])
+def test_backward_refuses_outputs_over_other_rows(kw):
+    assert bwd_rc(**kw) == fa.FA_ERR_INVALID_ARG
+
+
+def test_in_place_is_not_refused():
+    """Accepted as far as the device is asked for (no GPU) or, without tokens, altogether; strides
+    of axes of length one do not count."""
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present")
+    none = (fa.FA_ERR_CUDA, fa.FA_ERR_ARCH)
+    assert fwd_rc(qo=addr(0), ko=addr(1)) in none
+    assert fwd_rc(qo=addr(0), ko=addr(1), st=(ST, ST, (64, 128, 512), (64, 128, 512)), B=1) in none
+    assert fwd_rc(qo=addr(0), ko=addr(1), st=(ST, ST, (64, 8, 8), (64, 8, 8)), B=1, H=1, Hkv=1, N=1) in none
+    assert fwd_rc(qo=addr(3), N=0) in none
+    assert bwd_rc(dq=addr(0), dk=addr(1)) in none
