@@ -40,8 +40,10 @@
 //
 // What bounds it. Pair mode: the chain S - softmax - P V - S of each Q tile, as in
 // the forward kernel of whole matrices; tensor memory is full, so S has no second
-// buffer. 2048 tokens behind 14336 others, 32 heads of d 128 on 8: 371 us, 1.39
-// PFLOP/s (72 % of a matrix product's burst rate), tensor pipe active 61 %. Split
+// buffer. 2048 tokens behind 14336 others, 32 heads of d 128 on 8: 378 us, 1.36
+// PFLOP/s (71 % of a matrix product's burst rate), tensor pipe active 61 %. (The start's code
+// decides between two forms of the tile loop's, 1 % faster for those inputs or 2 % for
+// others: see the barriers.) Split
 // mode: 16 x 40 rows, 4 K / V heads, 8192 keys: 60 us a call of equal sequences, 70
 // a ragged one, whose launch of the step kernel finds nothing to do (9 us less than
 // with all of K widened, too, and whole tiles for each warpgroup); a KV tile takes
@@ -1436,7 +1438,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   {
-    // a barrier for each thread
+    // A barrier for each thread. With one thread for all, divisions of 64 bits and a start that
+    // no condition precedes, each of which runs once, the tile loop takes another time, for a
+    // reason not found: us here / so, d 128, 32 heads on 8, 2048 tokens behind 14336, bf16
+    // with the measured case's inputs 378.8 / 375.8, with random codes 394 / 401, fp16 388 / 393;
+    // 4 x 512 behind 4096 156 / 159; 32 ragged pieces of up to 64 behind up to 16384 402 / 418.
     constexpr int kStages = kCbKVFull + 2 * L::kStages, kRawSlots = kStages + 2 * L::kRaw;
     constexpr int kBars = kRawSlots + 2 * L::kDirect;
     const int i = tid;

@@ -19,9 +19,13 @@ namespace {
 // one after another, each with its own new scale.
 //
 // A chain of loads (lengths and words - table - scales - rows), so what counts is how
-// many warps are in it. Half of up to 96 tokens of 256 requests, 32 heads, d 128, 97 MB:
-// 22.8 us (4.3 TB/s); with 32 rows of a warp under way, 8 warps to a CTA and 3 CTAs 29.7,
-// 16 rows, 5 CTAs of 8 warps 23.6, 64 rows 40. A path of 16 requests, 4 heads: 3.6 us.
+// many warps are in it. Half of up to 96 tokens of 256 requests, 32 heads, blocks of 128, d
+// 128: 97 MB of kept tokens, and 49 MB of older rows whose block's scale grows, which are
+// re-coded one load and store after another: 49.5 us on a cache as it comes (2.9 TB/s). On
+// a cache that has been through it, so without older rows, 26.7, in L2 22.8; in that form,
+// 32 rows of a warp under way, 8 warps to a CTA and 3 CTAs 29.7, 16 rows, 5 CTAs of 8
+// warps 23.6, 64 rows 40. Paths of up to 64 tokens in place of halves 31.6 (as it
+// comes); a path of 16 requests, 4 heads: 4.5, repeated 3.6.
 
 constexpr int kKeepWarps = 4;
 constexpr int kKeepThreads = 32 * kKeepWarps;
@@ -167,8 +171,9 @@ __global__ void __launch_bounds__(kKeepThreads, kKeepCtas) fa_cache_keep_kernel(
 // list, at its rank among them (a scan over the threads, and over the CTAs through
 // their shared memory), and clears the count. So the list does not depend on which
 // request came first in time. Up to 4096 entries are the first CTA's alone. Latency:
-// the blocks behind the kept tokens of 256 requests 5.9 us, with counts 8.1; 32768
-// entries 9.4 and 24.6 (one CTA for any number: 40 and 152), 524288 127 and 354.
+// the blocks behind the kept tokens of 256 requests 5.9 us, with counts 8.1; all 128 blocks of
+// 256 requests, in random order, 9.3 and 24.2 (one CTA for any number: 40 and 152), of 4096
+// requests 182 and 440.
 
 constexpr int kReleaseThreads = 1024;
 constexpr int kEntries = 4;
@@ -370,7 +375,9 @@ __global__ void __cluster_dims__(kReleaseCtas, 1, 1) __launch_bounds__(kReleaseT
 // free block) for itself and writes its share of the rows, neighbouring ones, so that
 // the sum goes on from row to row; a warp for a row, or where there are enough CTAs all
 // of its warps. Which block a row gets does not depend on order in time, counts go up by
-// integer additions. Latency: 4 rows 3 us, 512 6, 4096 25, 65536 343.
+// integer additions. Latency: 4 rows 2.8 us, 512 of up to 5 blocks 5.6. Rows of 7 shared blocks
+// and a copied one, eight to a source: 512 9.5, 4096 35, 65536 442. (32 registers a thread,
+// 4 bytes of them spilled.)
 
 constexpr int kForkThreads = 256;
 
@@ -474,7 +481,7 @@ __global__ void __launch_bounds__(kForkThreads) fa_cache_fork_kernel(const ForkA
 // memory, the entry and the rows, so many small CTAs: a beam of 512 copies of 128-token
 // blocks, 32 heads, d 128, 537 MB: 64 us (8.4 TB/s, the eight copies of a block are read
 // from L2) with 8 CTAs on an SM, 74 with 4 that request four rows at a time, 108 with 2
-// and eight rows.
+// and eight rows. (Eight CTAs leave 32 registers a thread, 52 bytes of which are spilled.)
 
 constexpr int kCopyThreads = 256, kCopyCtas = 8;
 

@@ -63,9 +63,11 @@ fa_status fa_cache_tree(const int32_t* parents, const int32_t* cu, const int32_t
  *
  * Roundings are fa_fwd_cache's, but for which sequences are taken for large: a call
  * with cu_q and more than 16 rows to a K / V head on average computes all of its
- * sequences as those of more rows, and with d = 128 these are the ones whose small query
- * elements may be rounded (by 2^-17 of their row's largest), however many rows
- * there are. Launches: one kernel for such a call, and one that joins; otherwise as there.
+ * sequences as those of more rows, however many rows each has. So with
+ * FA_DTYPE_FP16 the weights of a small sequence in such a call are one fp16 value (2^-11
+ * of themselves, not 2^-22), and with d = 128 its small query elements may be rounded (by
+ * 2^-17 of their row's largest): the last bits of its results depend on the
+ * sequences beside it. Launches: one kernel for such a call, and one that joins; otherwise as there.
  */
 fa_status fa_fwd_cache_tree(const void* q, const fa_cache* cache, const int32_t* block_table,
                             int table_width, const int32_t* kv_lens, const int32_t* cu_q,

@@ -62,7 +62,7 @@ def test_nan_on_both_sides_of_sequences_without_keys(tree, dt, d, group):
 
 def odd_batch(seed, d, dt, kind="tree"):
     """170 trees over contexts of 0 to 600 keys, some of no keys at all, of more than 128 rows, of a
-    context of many tiles: 60 counted tiles and several items to a CTA, cut items among them."""
+    context of many tiles: some 50 counted tiles and several items to a CTA, cut items among them."""
     rng = np.random.default_rng(seed)
     counts = rng.integers(1, 65, 170).tolist()
     ctx = rng.integers(0, 601, 170).tolist()
