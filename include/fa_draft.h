@@ -62,8 +62,9 @@ fa_status fa_cache_tree(const int32_t* parents, const int32_t* cu, const int32_t
  * workspace : of fa_fwd_cache_workspace_size bytes, as there.
  *
  * Roundings are fa_fwd_cache's, but for which sequences are taken for large: a call
- * with cu_q and more than 16 rows to a K / V head on average computes all of its
- * sequences as those of more rows, however many rows each has. So with
+ * with cu_q and more than 16 rows to a K / V head on average (T * H / Hkv over B, rows
+ * of no sequence included) computes all of its sequences as those of more rows,
+ * however many rows each has. So with
  * FA_DTYPE_FP16 the weights of a small sequence in such a call are one fp16 value (2^-11
  * of themselves, not 2^-22), and with d = 128 its small query elements may be rounded (by
  * 2^-17 of their row's largest): the last bits of its results depend on the
