@@ -113,9 +113,10 @@ def qk_norm_rope_forward(q, k, rope, positions, q_weight=None, k_weight=None, ep
 def qk_norm_rope_forward_into(q, k, q_out, k_out, rope, positions, q_weight=None, k_weight=None,
                               eps: float = 1e-6, interleaved: bool = False, stream=None) -> None:
     """qk_norm_rope_forward into q_out and k_out: q and k themselves (views of the
-    same strides), or tensors that share no memory with them. Not differentiable: tensors that require gradients are
-    refused unless gradients are off, and what autograd has saved of the overwritten
-    ones counts as changed, as after torch's in-place calls."""
+    same strides), or tensors that share no memory with them. Not differentiable:
+    tensors that require gradients are refused unless gradients are off, and what
+    autograd has saved of the overwritten ones counts as changed, as after torch's
+    in-place calls."""
     r = cache._module().qk_norm_rope(q, k, rope, positions, q_weight, k_weight, eps, interleaved,
                                      (q_out, k_out), stream)
     if type(r) is int:
